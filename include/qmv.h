@@ -370,6 +370,158 @@ qmv_status qmv_moe_matvec_noalloc(qmv_type type, const void* w, int64_t n_expert
                                   void* stream);
 
 /*
+ * The attention half of a decode layer: norm -> q/k/v matvecs -> cache append
+ * -> attention -> output matvec.  (Castagna Veloce page, "Fused operations":
+ * norm and Q8 activations in one step; zhuai.tech GLM-5.3 page, "Where the
+ * bits go": the cache held in 8 bits with group scales.)
+ *
+ * qmv_rmsnorm_quantize -- residual addition, root-mean-square norm and the Q8
+ * activation blocks of the result in one launch.  For row t:
+ *   r = x + residual                          (fp32; r = x without one),
+ *   inv = fp32(1 / sqrt(sum r^2 / k + eps))   (the sum and root in fp64),
+ *   y = (r * inv) * weight                    (each product rounded to fp32),
+ * then the Q8 blocks of y exactly as qmv_quantize_act makes them.  The codes
+ * do not depend on how the row is split over threads.
+ * x        : fp32 [n_tok][ldx] (device), finite values.
+ * residual : NULL, or fp32 [n_tok][ldr] (device).
+ * weight   : fp32 [k] (device).
+ * sum_out  : NULL, or fp32 [n_tok][lds] (device) that receives r; it may be
+ *            x or residual themselves (same pointer and stride).
+ * y_out    : NULL, or fp32 [n_tok][ldy] (device) that receives y; it must not
+ *            overlap another argument, but may be x or residual themselves
+ *            if sum_out is not the same one.
+ * xq       : activation buffer of qmv_act_bytes(n_tok, k) bytes (device,
+ *            256-byte aligned); fully overwritten.
+ * Every fp32 pointer 16-byte aligned and every stride a multiple of 4 (else
+ * QMV_ERR_MISALIGNED); strides at least k; k a positive multiple of 32, eps
+ * positive and finite (else QMV_ERR_INVALID_ARG); n_tok <= QMV_MAX_ACT_ROWS
+ * and k <= QMV_MAX_NORM_K (else QMV_ERR_UNSUPPORTED).
+ * Asynchronous on `stream`; allocates nothing.
+ */
+#define QMV_MAX_NORM_K 65536
+qmv_status qmv_rmsnorm_quantize(const float* x, int64_t ldx, const float* residual, int64_t ldr, int64_t n_tok,
+                                int64_t k, const float* weight, float eps, float* sum_out, int64_t lds,
+                                float* y_out, int64_t ldy, void* xq, void* stream);
+
+/*
+ * qmv_kv -- a key/value cache held in 8 bits and the sequences of one call
+ * (HOST struct, read during the call only; its pointers are device pointers).
+ *
+ * The cache is a pool of blocks of QMV_KV_BLOCK = 64 tokens.  A block holds
+ * int8 codes of all kv heads and one fp32 scale for each kv head of its keys
+ * and of its values; value = scale * code.
+ *   codes  : int8 [n_blocks][2][n_kv_heads][64 * head_dim], 16-byte aligned:
+ *            the key part of a head is [64 slots][head_dim], its value part
+ *            [head_dim][64 slots];
+ *   scales : fp32 [n_blocks][2][n_kv_heads] (keys, then values).
+ * Neither needs to be initialized: a block's codes and scale count from the
+ * first token on that qmv_kv_append writes into its slot 0.
+ *
+ * Sequence s of n_seqs has seq_lens[s] tokens, the new ones of the call among
+ * them (at its end).  Its token at position p lies in slot p % 64 of block
+ * block_table[s][p / 64].
+ *   block_table : int32 [n_seqs][table_width]; entries past a sequence's
+ *                 length are not read.  Positions past the table, and blocks
+ *                 whose id is outside [0, n_blocks), are not in the cache:
+ *                 nothing is written to them and no query sees them.
+ *   seq_lens    : int32 [n_seqs]; a negative one counts as 0.
+ *   tok_start   : NULL, or int32 [n_seqs + 1]: the rows of sequence s in the
+ *                 call's row arrays are tok_start[s] .. tok_start[s + 1] - 1
+ *                 (clamped to 0 .. n_tok; at most max_q of them, further ones
+ *                 are ignored).  NULL: every sequence has max_q rows, and
+ *                 n_tok = n_seqs * max_q.  Rows of no sequence are neither
+ *                 read nor written.
+ *   max_q       : the most new tokens of a sequence.
+ * With n new tokens, row i of sequence s is position seq_lens[s] - n + i;
+ * rows at negative positions are not appended and attend to nothing.
+ * Sequences may share blocks that the call only reads; blocks that it writes
+ * must belong to one sequence.
+ * head_dim is a positive multiple of 16 (else QMV_ERR_INVALID_ARG) of at most
+ * QMV_MAX_HEAD_DIM; n_kv_heads, n_seqs, n_tok, max_q, table_width and
+ * n_blocks are positive and at most 1024, 65535, QMV_MAX_ACT_ROWS,
+ * QMV_MAX_ACT_ROWS, 2^24 and 2^31 - 1 (else QMV_ERR_UNSUPPORTED).
+ */
+#define QMV_KV_BLOCK 64
+#define QMV_MAX_HEAD_DIM 256
+#define QMV_MAX_KV_HEADS 1024
+#define QMV_MAX_HEADS 16384
+#define QMV_MAX_KV_SEQS 65535
+typedef struct {
+  int8_t* codes;
+  float* scales;
+  int64_t n_blocks;
+  int64_t n_kv_heads;
+  int64_t head_dim;
+  const int32_t* block_table;
+  int64_t table_width;
+  const int32_t* seq_lens;
+  const int32_t* tok_start;
+  int64_t n_seqs;
+  int64_t n_tok;
+  int64_t max_q;
+} qmv_kv;
+
+/*
+ * qmv_kv_append -- write the new tokens' keys and values into the cache.
+ * For each block that gets new tokens, each kv head, and keys and values
+ * apart:
+ *   d = max(d_old, amax / 127) over the new values in the block, d_old being
+ *       the block's scale if tokens stand before the new ones in it, else 0
+ *       (fp32, correctly rounded);
+ *   if d grew, the codes q of the tokens before become round(q * (d_old / d));
+ *   the new codes are round(x / d), 0 where d is 0 (rounding half away from
+ *   zero, clamped to [-127, 127]).
+ * Slots behind the new tokens keep their bytes.  After a rollback (shorter
+ * seq_lens) the next append writes over the tokens taken back; the block's
+ * scale stays as it was unless its slot 0 is written again.
+ * k, v : fp32 [n_tok][ldk], [n_tok][ldv] (device), 16-byte aligned, finite;
+ *        head h of a row at columns h * head_dim ..; ldk and ldv multiples
+ *        of 4 (else QMV_ERR_MISALIGNED), at least n_kv_heads * head_dim.
+ * Asynchronous on `stream`; allocates nothing.
+ */
+qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const float* v, int64_t ldv, void* stream);
+
+/*
+ * qmv_kv_attn -- attention of the new tokens' query heads over the cache
+ * (which holds the new tokens already: qmv_kv_append first).
+ *   out[row][h] = sum_j P_j v_j,  P = softmax over the seen j of
+ *                                     scale * (q[row][h] . k_j),
+ * with the keys and values of kv head h / (n_heads / n_kv_heads).  The row at
+ * position p sees the positions j <= p, with window > 0 only j > p - window.
+ * A row that sees nothing gives zeros; a row of q that is not finite gives
+ * NaN in that row.  Sums, maxima and totals are fp32; the cached codes enter
+ * the products as they are, q and the softmax weights with 24 bits relative
+ * to a row's largest (the weights: its largest in each block of 64).
+ * q    : fp32 [n_tok][ldq] (device), 16-byte aligned, head h of a row at
+ *        columns h * head_dim ..; ldq a multiple of 4, at least
+ *        n_heads * head_dim.
+ * out  : NULL, or fp32 [n_tok][ldo] (device, 16-byte aligned, ldo as ldq); it
+ *        may be q itself (same pointer and stride).
+ * xq   : NULL, or an activation buffer of
+ *        qmv_act_bytes(n_tok, n_heads * head_dim) bytes (device, 256-byte
+ *        aligned) that receives the Q8 blocks of the output rows, exactly as
+ *        qmv_quantize_act makes them from out (the output projection's
+ *        input); head_dim a multiple of 32.  One of out and xq is needed.
+ * ws   : optional workspace (device, 256-byte aligned) of
+ *        qmv_kv_attn_workspace_bytes(...) bytes, zero-filled once when
+ *        allocated and left so in its counters by every completed call; it
+ *        lets workgroups share a sequence's blocks, which calls with few
+ *        sequences and heads need for speed.  NULL runs without.  One
+ *        workspace may serve calls of different shapes that do not overlap
+ *        in time.  The result with a workspace is the same on every call
+ *        with the same arguments, and differs from the one without in
+ *        rounding only.
+ * n_heads a positive multiple of n_kv_heads of at most QMV_MAX_HEADS, window
+ * >= 0, scale finite.  Asynchronous on `stream`; allocates nothing.
+ * qmv_kv_attn_workspace_bytes is host only; 0: the arguments are invalid, or
+ * no workspace is used.
+ */
+size_t qmv_kv_attn_workspace_bytes(int64_t n_seqs, int64_t n_tok, int64_t max_q, int64_t n_heads,
+                                   int64_t n_kv_heads, int64_t head_dim, int64_t table_width);
+qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, int64_t n_heads, float scale, int64_t window,
+                       float* out, int64_t ldo, void* xq, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qmv_block_dots -- test hook: the exact integer partial of every 32-weight
  * block, computed by the same device decode and dot routines as qmv_matvec.
  * out : int32 [n_tok][n_rows][k/32][c] (device), c = 2 for q4_K and q5_K

@@ -12,6 +12,7 @@ If the library has not been built, importing works but the first call raises
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -24,6 +25,7 @@ __all__ = [
     "moe_gate_up_swiglu",
     "block_dots",
     "block_dots_mx", "moe_block_dots", "stream_read",
+    "rmsnorm_quantize", "kv_append", "kv_attn", "kv_attn_workspace_bytes", "KV_BLOCK",
     "set_tuning", "swiglu_quantize", "router_topk", "variant_name", "variants", "pick_variant", "matvec_plan", "MAX_TOKENS", "MAX_MOE_TOKENS",
 ]
 
@@ -31,6 +33,7 @@ Q8_0, Q4_K, IQ4_XS, Q5_K, Q6_K, Q8G128 = 0, 1, 2, 3, 4, 5
 MAX_TOKENS = 16
 MAX_MOE_TOKENS = 64
 MAX_BATCH = 8
+KV_BLOCK = 64
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
@@ -43,6 +46,14 @@ class _Item(ctypes.Structure):
     """qmv_matvec_item of include/qmv.h."""
     _fields_ = [("w", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("y", ctypes.c_void_p),
                 ("ldy", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64)]
+
+
+class _Kv(ctypes.Structure):
+    """qmv_kv of include/qmv.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n_blocks", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                ("table_width", ctypes.c_int64), ("seq_lens", ctypes.c_void_p), ("tok_start", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int64), ("n_tok", ctypes.c_int64), ("max_q", ctypes.c_int64)]
 
 
 class QmvError(RuntimeError):
@@ -94,6 +105,10 @@ def lib():
         "qmv_moe_matvec": ([I, P, I64, I64, I64, P, I, P, P, I64, I64, P, P, SZ, P], I),
         "qmv_moe_matvec_noalloc": ([I, P, I64, I64, I64, P, I, P, P, I64, I64, P, P], I),
         "qmv_moe_gate_up_swiglu": ([I, P, I64, I64, I64, P, P, I64, I64, P, P, P, SZ, P], I),
+        "qmv_rmsnorm_quantize": ([P, I64, P, I64, I64, I64, P, ctypes.c_float, P, I64, P, I64, P, P], I),
+        "qmv_kv_append": ([ctypes.POINTER(_Kv), P, I64, P, I64, P], I),
+        "qmv_kv_attn_workspace_bytes": ([I64, I64, I64, I64, I64, I64, I64], SZ),
+        "qmv_kv_attn": ([ctypes.POINTER(_Kv), P, I64, I64, ctypes.c_float, I64, P, I64, P, P, SZ, P], I),
         "qmv_block_dots": ([I, P, I64, I64, P, I64, P, P], I),
         "qmv_block_dots_mx": ([I, P, I64, I64, P, I64, I64, I, P, P], I),
         "qmv_moe_block_dots": ([I, P, I64, I64, I64, P, I, P, I64, I64, I64, P, P, SZ, P], I),
@@ -395,6 +410,144 @@ def moe_matvec_noalloc(fmt: int, w: torch.Tensor, n_experts: int, n_rows: int, k
                                         _ptr(ids), _ptr(route_w), n_tok, top_k, _ptr(y), _stream(stream)),
            "qmv_moe_matvec_noalloc")
     return y
+
+
+# ------------------------------------- norm, cache append and attention
+def _here(*tensors) -> torch.device:
+    """The current device, on which every tensor has to be: the call is
+    enqueued on one of its streams."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device (cuda:{dev})")
+    return torch.device("cuda", dev)
+
+
+def _new(shape, dtype, dev, stream) -> torch.Tensor:
+    """A tensor for a call on `stream` to write, of that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _rows(t: torch.Tensor, shape, name: str) -> int:
+    """Checks an fp32 row array and gives its row stride."""
+    if t.dtype != torch.float32 or not t.is_cuda or tuple(t.shape) != tuple(shape) or t.stride(-1) != 1 \
+            or (t.dim() == 3 and t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be a float32 CUDA tensor {list(shape)} whose rows lie in one piece")
+    return t.stride(0) if t.shape[0] > 1 else math.prod(t.shape[1:])  # a single row's stride is arbitrary
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
+                     residual: torch.Tensor | None = None, sum_out: torch.Tensor | None = None,
+                     y_out: torch.Tensor | None = None, xq: torch.Tensor | None = None, stream=None):
+    """x fp32 [T][K] (+ residual) -> (r, xq): r = x + residual (in sum_out,
+    allocated when None; x itself without a residual and a sum_out) and the
+    Q8 activation buffer of rmsnorm(r) * weight.  y_out fp32 [T][K], if given,
+    receives the normed rows.  sum_out may be x or residual."""
+    if x.dim() == 1:
+        x = x.view(1, -1)
+    if x.dim() != 2:
+        raise ValueError("x must be a 1-D or 2-D tensor")
+    n_tok, k = x.shape
+    ldx = _rows(x, x.shape, "x")
+    _need(weight, torch.float32, "weight")
+    if weight.numel() != k:
+        raise ValueError("weight must hold one value a column of x")
+    dev = _here(x, weight, residual, sum_out, y_out, xq)
+    if residual is not None and residual.dim() == 1:
+        residual = residual.view(1, -1)
+    ldr = 0 if residual is None else _rows(residual, x.shape, "residual")
+    if sum_out is None and residual is not None:
+        sum_out = _new((n_tok, k), torch.float32, dev, stream)
+    lds = 0 if sum_out is None else _rows(sum_out, x.shape, "sum_out")
+    ldy = 0 if y_out is None else _rows(y_out, x.shape, "y_out")
+    nbytes = act_bytes(n_tok, k)
+    if xq is None:
+        xq = _new(max(nbytes, 1), torch.uint8, dev, stream)
+    _need(xq, torch.uint8, "xq")
+    if xq.numel() < nbytes:
+        raise ValueError("activation buffer too small")
+    _check(lib().qmv_rmsnorm_quantize(_ptr(x), ldx, _ptr(residual), ldr, n_tok, k, _ptr(weight), eps, _ptr(sum_out),
+                                      lds, _ptr(y_out), ldy, _ptr(xq), _stream(stream)), "qmv_rmsnorm_quantize")
+    return (x if sum_out is None else sum_out), xq
+
+
+def _kv(codes, scales, block_table, seq_lens, tok_start, n_tok, max_q, dim) -> _Kv:
+    _need(codes, torch.int8, "codes")
+    _need(scales, torch.float32, "scales")
+    _need(block_table, torch.int32, "block_table")
+    _need(seq_lens, torch.int32, "seq_lens")
+    n_seqs = seq_lens.numel()
+    if codes.dim() != 4 or codes.shape[1] != 2 or codes.shape[3] != KV_BLOCK * dim:
+        raise ValueError(f"codes must be [n_blocks][2][n_kv_heads][{KV_BLOCK} * head_dim]")
+    if scales.shape != codes.shape[:3]:
+        raise ValueError("scales must be [n_blocks][2][n_kv_heads]")
+    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
+        raise ValueError("block_table must be [n_seqs][blocks of a sequence]")
+    if tok_start is not None:
+        _need(tok_start, torch.int32, "tok_start")
+        if tok_start.numel() != n_seqs + 1:
+            raise ValueError("tok_start must hold n_seqs + 1 rows")
+    return _Kv(codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[2], dim, block_table.data_ptr(),
+               block_table.shape[1], seq_lens.data_ptr(), None if tok_start is None else tok_start.data_ptr(),
+               n_seqs, n_tok, max_q)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+              block_table: torch.Tensor, seq_lens: torch.Tensor, tok_start: torch.Tensor | None = None,
+              max_q: int = 1, stream=None) -> None:
+    """Writes keys and values fp32 [T][n_kv_heads][head_dim] (rows may be
+    strided) at the end of their sequences in an 8-bit block cache: codes int8
+    [n_blocks][2][n_kv_heads][64 * head_dim] and scales fp32
+    [n_blocks][2][n_kv_heads], changed in place.  seq_lens (int32) counts the
+    new tokens; block_table int32 [n_seqs][blocks]; tok_start int32
+    [n_seqs + 1] the rows of each sequence, at most max_q (None: max_q each)."""
+    if k.dim() != 3 or k.shape != v.shape:
+        raise ValueError("k and v must be [T][n_kv_heads][head_dim]")
+    if codes.dim() == 4 and codes.shape[2] != k.shape[1]:
+        raise ValueError("k has another number of heads than codes")
+    ldk, ldv = _rows(k, k.shape, "k"), _rows(v, k.shape, "v")
+    _here(k, v, codes, scales, block_table, seq_lens, tok_start)
+    kv = _kv(codes, scales, block_table, seq_lens, tok_start, k.shape[0], max_q, k.shape[2])
+    _check(lib().qmv_kv_append(ctypes.byref(kv), _ptr(k), ldk, _ptr(v), ldv, _stream(stream)), "qmv_kv_append")
+
+
+def kv_attn_workspace_bytes(n_seqs: int, n_tok: int, max_q: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                            table_width: int) -> int:
+    return int(lib().qmv_kv_attn_workspace_bytes(n_seqs, n_tok, max_q, n_heads, n_kv_heads, head_dim, table_width))
+
+
+def kv_attn(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_table: torch.Tensor,
+            seq_lens: torch.Tensor, tok_start: torch.Tensor | None = None, max_q: int = 1,
+            scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+            xq: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of q fp32 [T][n_heads][head_dim] over the cache that
+    kv_append writes (see there), causal, over the last `window` positions if
+    that is not 0; scale None: 1 / sqrt(head_dim).  Returns out fp32
+    [T][n_heads][head_dim] (allocated when None); xq, if given, receives the
+    Q8 blocks of its rows.  ``ws`` (uint8, zero-filled once, of
+    kv_attn_workspace_bytes bytes) lets workgroups share a sequence."""
+    if q.dim() != 3:
+        raise ValueError("q must be [T][n_heads][head_dim]")
+    n_tok, n_heads, dim = q.shape
+    ldq = _rows(q, q.shape, "q")
+    dev = _here(q, codes, scales, block_table, seq_lens, tok_start, out, xq, ws)
+    kv = _kv(codes, scales, block_table, seq_lens, tok_start, n_tok, max_q, dim)
+    if out is None:
+        out = _new(q.shape, torch.float32, dev, stream)
+    ldo = _rows(out, q.shape, "out")
+    if xq is not None:
+        _need(xq, torch.uint8, "xq")
+        if xq.numel() < act_bytes(n_tok, n_heads * dim):
+            raise ValueError("activation buffer too small")
+    if ws is not None:
+        _need(ws, torch.uint8, "ws")
+    _check(lib().qmv_kv_attn(ctypes.byref(kv), _ptr(q), ldq, n_heads, dim ** -0.5 if scale is None else scale, window,
+                             _ptr(out), ldo, _ptr(xq), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)),
+           "qmv_kv_attn")
+    return out
 
 
 def block_dots(fmt: int, w: torch.Tensor, n_rows: int, k: int, xq: torch.Tensor, n_tok: int,

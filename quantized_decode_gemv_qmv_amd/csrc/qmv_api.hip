@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "qmv_attn.h"
 #include "qmv_internal.h"
 #include "qmv_mfma.h"
 #include "qmv.h"
@@ -696,6 +697,155 @@ QMV_API qmv_status qmv_router_topk(const float* x, int64_t ldx, int64_t n_tok, i
                                     const_cast<int8_t*>(xv.qs), const_cast<float*>(xv.d),
                                     const_cast<int32_t*>(xv.s), static_cast<hipStream_t>(stream));
   return hip_status(e);
+}
+
+// ------------------------------------------ norm, cache append, attention
+QMV_API qmv_status qmv_rmsnorm_quantize(const float* x, int64_t ldx, const float* residual, int64_t ldr,
+                                        int64_t n_tok, int64_t k, const float* weight, float eps, float* sum_out,
+                                        int64_t lds, float* y_out, int64_t ldy, void* xq, void* stream) {
+  if (x == nullptr || weight == nullptr || xq == nullptr || n_tok < 1 || k < 1 || k % 32 || ldx < k ||
+      (residual != nullptr && ldr < k) || (sum_out != nullptr && lds < k) || (y_out != nullptr && ldy < k) ||
+      !(eps > 0.f) || !(eps < __builtin_inff()))
+    return QMV_ERR_INVALID_ARG;
+  if (n_tok > QMV_MAX_ACT_ROWS || k > QMV_MAX_NORM_K) return QMV_ERR_UNSUPPORTED;
+  if (!aligned(x, 16) || ldx % 4 || !aligned(weight, 16) || !aligned(xq, 256) ||
+      (residual != nullptr && (!aligned(residual, 16) || ldr % 4)) ||
+      (sum_out != nullptr && (!aligned(sum_out, 16) || lds % 4)) ||
+      (y_out != nullptr && (!aligned(y_out, 16) || ldy % 4)))
+    return QMV_ERR_MISALIGNED;
+  const ActView v = act_view(xq, n_tok, k);
+  NormArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.res = residual;
+  a.ldr = ldr;
+  a.w = weight;
+  a.eps = eps;
+  a.sum = sum_out;
+  a.lds = lds;
+  a.y = y_out;
+  a.ldy = ldy;
+  a.qs = const_cast<int8_t*>(v.qs);
+  a.d = const_cast<float*>(v.d);
+  a.s = const_cast<int32_t*>(v.s);
+  a.rows = static_cast<int>(n_tok);
+  a.k = static_cast<int>(k);
+  return hip_status(launch_rmsnorm(a, device_cus(), static_cast<hipStream_t>(stream)));
+}
+
+// The sizes of a cache and its call, whatever their pointers.
+static qmv_status check_kv_sizes(int64_t n_seqs, int64_t n_tok, int64_t max_q, int64_t kvh, int64_t dim,
+                                 int64_t width) {
+  if (n_seqs < 1 || n_tok < 1 || max_q < 1 || kvh < 1 || dim < 1 || dim % 16 || width < 1) return QMV_ERR_INVALID_ARG;
+  if (n_seqs > QMV_MAX_KV_SEQS || n_tok > QMV_MAX_ACT_ROWS || max_q > QMV_MAX_ACT_ROWS || kvh > QMV_MAX_KV_HEADS ||
+      dim > QMV_MAX_HEAD_DIM || width > (int64_t(1) << 24))
+    return QMV_ERR_UNSUPPORTED;
+  return QMV_OK;
+}
+
+static qmv_status check_kv(const qmv_kv* kv, KvView* out) {
+  if (kv == nullptr || kv->codes == nullptr || kv->scales == nullptr || kv->block_table == nullptr ||
+      kv->seq_lens == nullptr || kv->n_blocks < 1)
+    return QMV_ERR_INVALID_ARG;
+  const qmv_status st =
+      check_kv_sizes(kv->n_seqs, kv->n_tok, kv->max_q, kv->n_kv_heads, kv->head_dim, kv->table_width);
+  if (st != QMV_OK) return st;
+  if (kv->tok_start == nullptr && kv->n_tok != kv->n_seqs * kv->max_q) return QMV_ERR_INVALID_ARG;
+  if (kv->n_blocks > INT32_MAX) return QMV_ERR_UNSUPPORTED;
+  if (!aligned(kv->codes, 16) || !aligned(kv->scales, 4) || !aligned(kv->block_table, 4) ||
+      !aligned(kv->seq_lens, 4) || !aligned(kv->tok_start, 4))
+    return QMV_ERR_MISALIGNED;
+  out->codes = kv->codes;
+  out->scales = kv->scales;
+  out->table = kv->block_table;
+  out->lens = kv->seq_lens;
+  out->start = kv->tok_start;
+  out->n_blocks = kv->n_blocks;
+  out->kvh = static_cast<int>(kv->n_kv_heads);
+  out->dim = static_cast<int>(kv->head_dim);
+  out->width = static_cast<int>(kv->table_width);
+  out->n_seqs = static_cast<int>(kv->n_seqs);
+  out->n_tok = static_cast<int>(kv->n_tok);
+  out->max_q = static_cast<int>(kv->max_q);
+  return QMV_OK;
+}
+
+QMV_API qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const float* v, int64_t ldv,
+                                 void* stream) {
+  AppendArgs a{};
+  const qmv_status st = check_kv(kv, &a.kv);
+  if (st != QMV_OK) return st;
+  const int64_t cols = kv->n_kv_heads * kv->head_dim;
+  if (k == nullptr || v == nullptr || ldk < cols || ldv < cols) return QMV_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || ldk % 4 || ldv % 4) return QMV_ERR_MISALIGNED;
+  a.x[0] = k;
+  a.x[1] = v;
+  a.ld[0] = ldk;
+  a.ld[1] = ldv;
+  return hip_status(launch_kv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+static qmv_status check_heads(int64_t n_heads, int64_t kvh) {
+  if (n_heads < 1 || n_heads % kvh) return QMV_ERR_INVALID_ARG;
+  return n_heads > QMV_MAX_HEADS ? QMV_ERR_UNSUPPORTED : QMV_OK;
+}
+
+QMV_API size_t qmv_kv_attn_workspace_bytes(int64_t n_seqs, int64_t n_tok, int64_t max_q, int64_t n_heads,
+                                           int64_t n_kv_heads, int64_t head_dim, int64_t table_width) {
+  if (check_kv_sizes(n_seqs, n_tok, max_q, n_kv_heads, head_dim, table_width) != QMV_OK ||
+      check_heads(n_heads, n_kv_heads) != QMV_OK)
+    return 0;
+  return static_cast<size_t>(
+      attn_plan(n_seqs, max_q, n_heads, n_kv_heads, head_dim, table_width, device_cus()).ws_bytes);
+}
+
+QMV_API qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, int64_t n_heads, float scale,
+                               int64_t window, float* out, int64_t ldo, void* xq, void* ws, size_t ws_bytes,
+                               void* stream) {
+  AttnArgs a{};
+  qmv_status st = check_kv(kv, &a.kv);
+  if (st != QMV_OK) return st;
+  st = check_heads(n_heads, kv->n_kv_heads);
+  if (st != QMV_OK) return st;
+  const int64_t cols = n_heads * kv->head_dim;
+  if (q == nullptr || (out == nullptr && xq == nullptr) || ldq < cols || (out != nullptr && ldo < cols) || window < 0 ||
+      !(scale > -__builtin_inff() && scale < __builtin_inff()) || (xq != nullptr && kv->head_dim % 32))
+    return QMV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || ldq % 4 || (out != nullptr && (!aligned(out, 16) || ldo % 4)) ||
+      (xq != nullptr && !aligned(xq, 256)))
+    return QMV_ERR_MISALIGNED;
+  const AttnPlan p = attn_plan(kv->n_seqs, kv->max_q, n_heads, kv->n_kv_heads, kv->head_dim, kv->table_width,
+                               device_cus());
+  if (p.groups * p.splits >= int64_t(1) << 24) return QMV_ERR_UNSUPPORTED;  // workgroups of one launch
+  const bool use_ws = ws != nullptr && p.ws_bytes > 0;
+  if (use_ws) {
+    if (ws_bytes < static_cast<size_t>(p.ws_bytes)) return QMV_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return QMV_ERR_MISALIGNED;
+  }
+  a.q = q;
+  a.ldq = ldq;
+  a.group = static_cast<int>(n_heads / kv->n_kv_heads);
+  a.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.window = static_cast<int>(window > INT32_MAX ? INT32_MAX : window);
+  a.out = out;
+  a.ldo = ldo;
+  if (xq != nullptr) {
+    const ActView v = act_view(xq, kv->n_tok, cols);
+    a.qs = const_cast<int8_t*>(v.qs);
+    a.qd = const_cast<float*>(v.d);
+    a.qsum = const_cast<int32_t*>(v.s);
+  }
+  a.wr = p.wr;
+  a.row_blocks = p.row_blocks;
+  a.splits = use_ws ? p.splits : 1;
+  if (use_ws) {
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    const int64_t sums = p.groups * p.splits * p.mr * p.wr * 16;
+    a.cnt = reinterpret_cast<int*>(b);
+    a.part = reinterpret_cast<float*>(b + kAttnCounterBytes);
+    a.ml = reinterpret_cast<float*>(b + kAttnCounterBytes + align256(sums * kv->head_dim * 4));
+  }
+  return hip_status(launch_kv_attn(a, p, static_cast<hipStream_t>(stream)));
 }
 
 // --------------------------------------------------------------- matvec

@@ -1,0 +1,297 @@
+"""qmv_kv_append (bit for bit) and qmv_kv_attn (within the bound of
+kv_ref.attend) against the definitions, at the lengths, masks, tables and
+layouts where they can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+import kv_ref
+import oracle
+from gpu_util import gpu, need_gpu, say, to_dev
+
+pytestmark = gpu
+
+
+class Case:
+    """A pool with scattered blocks, garbage in what no call may read, and the
+    sequences of one call."""
+
+    def __init__(self, seed, lens, counts, heads, dim, *, width=None, spare=3, uniform=None, padded=0):
+        r = self.rng = np.random.default_rng(seed)
+        self.lens = np.array(lens, np.int32)
+        n = len(lens)
+        need = [-(-max(x, 0) // 64) for x in lens]
+        self.width = width or max(max(need), 1)
+        self.n_blocks = sum(min(x, self.width) for x in need) + spare
+        ids = r.permutation(self.n_blocks)
+        self.table = r.choice(np.array([-1, -2**31, 2**31 - 1, 10**6]), (n, self.width)).astype(np.int32)
+        at = 0
+        self.used = np.zeros(self.n_blocks, bool)
+        for s in range(n):
+            m = min(need[s], self.width)
+            self.table[s, :m] = ids[at:at + m]
+            self.used[ids[at:at + m]] = True
+            at += m
+        self.codes = np.clip(np.round(r.standard_normal((self.n_blocks, 2, heads, 64 * dim)) * 35), -127, 127).astype(np.int8)
+        self.scales = (r.uniform(0.5, 1.5, (self.n_blocks, 2, heads)) * 4 / 127).astype(np.float32)
+        self.scales[~self.used] = np.nan
+        self.heads, self.dim = heads, dim
+        self.max_q = uniform or max(max(counts), 1)
+        if uniform:
+            self.start, self.n_tok = None, n * uniform
+        else:
+            self.start = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+            self.n_tok = int(self.start[-1]) + padded
+
+    def rows(self, heads, spread=1.0):
+        return (self.rng.standard_normal((self.n_tok, heads, self.dim)) * spread).astype(np.float32)
+
+    def dev(self):
+        return [to_dev(x) for x in (self.codes, self.scales, self.table, self.lens)] + \
+            [None if self.start is None else to_dev(self.start)]
+
+
+def same_cache(c, codes, scales, what):
+    got_c, got_s = codes.cpu().numpy(), scales.cpu().numpy()
+    assert np.array_equal(got_s, c.scales, equal_nan=True), what
+    bad = np.argwhere(got_c != c.codes)
+    assert len(bad) == 0, (what, len(bad), bad[:3])
+
+
+def run_append(qmv, c, k, v, what, **kw):
+    codes, scales, table, lens, start = c.dev()
+    qmv.kv_append(to_dev(k), to_dev(v), codes, scales, table, lens, tok_start=start, max_q=c.max_q, **kw)
+    kv_ref.append(c.codes, c.scales, c.table, c.lens, c.start, c.max_q, k, v)
+    same_cache(c, codes, scales, what)
+
+
+APPENDS = {  # lengths after, new tokens
+    "one": ([1], [1]),
+    "open block": ([70, 64, 65, 128, 3], [1, 1, 1, 1, 2]),
+    "crosses": ([130, 64, 200, 97], [5, 64, 73, 33]),
+    "many blocks": ([517, 300], [450, 300]),
+    "ragged, empty": ([0, 40, 77, 0, 500], [0, 3, 0, 0, 128]),
+    "more rows than tokens": ([2, 0, 66], [5, 3, 70]),
+    "verify": ([63, 64, 65, 66, 127, 128], [6, 6, 6, 6, 6, 6]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(APPENDS))
+@pytest.mark.parametrize("heads,dim", [(1, 16), (3, 64), (2, 80), (8, 128), (1, 192), (2, 256)])
+def test_append(name, heads, dim):
+    qmv = need_gpu()
+    say(f"append {name} {heads}x{dim}")
+    lens, counts = APPENDS[name]
+    c = Case(3, lens, counts, heads, dim, padded=2)
+    spread = np.float32(1.0 + 3.0 * (c.rng.random() < 0.5))
+    run_append(qmv, c, c.rows(heads) * spread, c.rows(heads) * 2, name)
+
+
+def test_append_blocks_outside():
+    """Table entries outside the pool, and positions past the table: nothing
+    is written there, the rest is."""
+    qmv = need_gpu()
+    c = Case(4, [200, 300, 130], [150, 250, 100], 2, 96, width=3)
+    c.table[0, 1] = -1
+    c.table[2, 2] = c.n_blocks
+    run_append(qmv, c, c.rows(2), c.rows(2), "outside")
+
+
+def test_append_step_by_step():
+    """A block filled token by token: its scale grows, its older codes follow
+    it; then a rollback into it, and a fresh start at its first slot over a
+    scale that is not a number."""
+    qmv = need_gpu()
+    say("append step by step")
+    c = Case(5, [64, 64], [1, 1], 2, 64)
+    c.scales[:] = np.nan
+    codes, scales, table, lens, _ = c.dev()
+    order = list(range(1, 65)) + [40, 41, 42] + [1, 2]
+    for n in order:
+        c.lens[:] = (n, max(n - 3, 0))
+        lens.copy_(torch.from_numpy(c.lens))
+        c.start, c.n_tok, c.max_q = None, 2, 1
+        k, v = c.rows(2, 0.1 * n), c.rows(2, 4.0 / n)
+        k[:, :, :] *= np.float32(0.0) if n in (1, 7) else np.float32(1.0)
+        qmv.kv_append(to_dev(k), to_dev(v), codes, scales, table, lens)
+        kv_ref.append(c.codes, c.scales, c.table, c.lens, None, 1, k, v)
+        same_cache(c, codes, scales, n)
+
+
+def test_append_small_and_large_values():
+    qmv = need_gpu()
+    c = Case(6, [70, 20, 64], [3, 20, 64], 2, 64)
+    k, v = c.rows(2), c.rows(2)
+    k[:3] *= np.float32(1e30)
+    v[3:23] *= np.float32(1e-30)
+    k[23:60] = 0.0
+    v[23:] = 0.0
+    run_append(qmv, c, k, v, "values")
+
+
+ATTNS = {  # lengths, new tokens, query heads a kv head
+    "one token": ([1], [1], 4),
+    "short": ([5, 63, 64, 65, 129], [1, 1, 1, 1, 1], 3),
+    "whole prompt": ([70], [70], 1),
+    "verify": ([300, 64, 66, 1000], [6, 6, 6, 6], 2),
+    "ragged, padded": ([0, 130, 77, 900, 64], [0, 3, 0, 9, 1], 5),
+    "rows before the first token": ([2, 0, 66], [5, 3, 70], 2),
+    "wide group": ([513, 200], [4, 3], 16),
+    "many rows": ([400, 90], [64, 33], 5),
+    "long": ([4001], [1], 8),
+}
+
+
+def check_attn(qmv, c, group, what, window=0, scale=None, ws=True, xq=False, q=None):
+    codes, scales, table, lens, start = c.dev()
+    heads = c.heads * group
+    q = c.rows(heads) if q is None else q
+    need = qmv.kv_attn_workspace_bytes(len(c.lens), c.n_tok, c.max_q, heads, c.heads, c.dim, c.width)
+    w = torch.zeros(need, dtype=torch.uint8, device="cuda") if ws and need else None
+    out = torch.full(q.shape, 5.0, device="cuda")
+    buf = None
+    if xq:
+        buf = torch.full((qmv.act_bytes(c.n_tok, heads * c.dim),), 9, dtype=torch.uint8, device="cuda")
+    kw = dict(tok_start=start, max_q=c.max_q, scale=scale, window=window, ws=w, xq=buf)
+    got = qmv.kv_attn(to_dev(q), codes, scales, table, lens, out=out, **kw)
+    assert got.data_ptr() == out.data_ptr()
+    g = out.cpu().numpy()
+    ref, tol, rows = kv_ref.attend(c.codes, c.scales, c.table, c.lens, c.start, c.max_q, q,
+                                   c.dim ** -0.5 if scale is None else scale, window)
+    err = np.abs(g[rows] - ref[rows])
+    assert np.all(err <= tol[rows]), (what, float((err - tol[rows]).max()), np.argwhere(~(err <= tol[rows]))[:3])
+    assert np.all(g[~rows] == 5.0), what  # rows of no sequence
+    if w is not None:
+        again = qmv.kv_attn(to_dev(q), codes, scales, table, lens, **kw)
+        assert torch.equal(again[torch.from_numpy(rows)], out[torch.from_numpy(rows)]), what
+        assert not w[:65536].any(), what
+    if xq:
+        want = oracle.quantize_act(np.ascontiguousarray(g.reshape(c.n_tok, -1)))
+        for x, y in zip(qmv.act_fields(buf, c.n_tok, heads * c.dim), want):
+            assert np.array_equal(x.cpu().numpy()[rows], y[rows]), what
+    return g
+
+
+@pytest.mark.parametrize("name", sorted(ATTNS))
+@pytest.mark.parametrize("heads,dim", [(1, 16), (2, 64), (1, 80), (2, 128), (1, 192), (1, 256)])
+def test_attn(name, heads, dim):
+    qmv = need_gpu()
+    say(f"attn {name} {heads}x{dim}")
+    lens, counts, group = ATTNS[name]
+    c = Case(7, lens, counts, heads, dim, padded=3 if "padded" in name else 0)
+    for ws in (False, True):
+        check_attn(qmv, c, group, name, ws=ws, xq=dim % 32 == 0)
+
+
+@pytest.mark.parametrize("window", [1, 5, 63, 64, 65, 200, 2**40])
+def test_window(window):
+    qmv = need_gpu()
+    c = Case(8, [700, 64, 30, 1], [7, 4, 30, 1], 2, 64)
+    for ws in (False, True):
+        check_attn(qmv, c, 3, window, window=window, ws=ws)
+
+
+def test_blocks_outside():
+    """Blocks outside the pool and positions past the table are not seen; a
+    sequence with no block in the cache gives zeros."""
+    qmv = need_gpu()
+    c = Case(9, [300, 500, 100, 128], [2, 3, 1, 2], 2, 128, width=5)
+    c.table[0, 2] = -7
+    c.table[2, :] = c.n_blocks
+    c.table[3, 1] = 2**31 - 1
+    for ws in (False, True):
+        g = check_attn(qmv, c, 4, "outside", ws=ws)
+        assert not g[5].any()
+
+
+def test_shared_blocks():
+    """Two sequences with the same first blocks."""
+    qmv = need_gpu()
+    c = Case(10, [200, 330], [1, 2], 2, 64)
+    c.table[1, :3] = c.table[0, :3]
+    check_attn(qmv, c, 2, "shared")
+
+
+def test_scores_far_apart():
+    """Scores of thousands (one key takes all), of nearly nothing, a scale of
+    zero and below it, rows of zeros and of very small values."""
+    qmv = need_gpu()
+    c = Case(11, [200, 200, 200, 200, 200], [1] * 5, 1, 64)
+    q = c.rows(4)
+    q[0] *= np.float32(3e4)
+    q[1] *= np.float32(1e-12)
+    q[2] = 0.0
+    q[3, :, 5:] *= np.float32(1e-9)
+    q[4] *= np.float32(1e-33)
+    check_attn(qmv, c, 4, "spread", q=q)
+    for scale in (0.0, -0.3, 2.5):
+        check_attn(qmv, c, 4, scale, scale=scale)
+
+
+def test_a_row_that_is_not_finite_stays_alone():
+    qmv = need_gpu()
+    say("attn nan rows")
+    c = Case(12, [400, 130], [3, 3], 2, 128)
+    q = c.rows(8)
+    good = check_attn(qmv, c, 4, "finite", q=q)
+    bad = q.copy()
+    bad[1, 2, 7] = np.nan
+    bad[3, 0, 100] = np.inf
+    codes, scales, table, lens, start = c.dev()
+    ws = torch.zeros(qmv.kv_attn_workspace_bytes(2, 6, 3, 8, 2, 128, c.width), dtype=torch.uint8, device="cuda")
+    for w in (None, ws):
+        g = qmv.kv_attn(to_dev(bad), codes, scales, table, lens, tok_start=start, max_q=3, ws=w).cpu().numpy()
+        hit = np.zeros(g.shape[:2], bool)
+        hit[1, 2] = hit[3, 0] = True
+        assert np.isnan(g[hit]).all()
+        assert np.allclose(g[~hit], good[~hit], rtol=1e-5, atol=1e-6)
+
+
+def test_layouts():
+    """Rows in the columns of a projection's output, the output among others'
+    columns, and the output over q itself; on another stream."""
+    qmv = need_gpu()
+    say("attn layouts")
+    c = Case(13, [90, 65], [2, 2], 2, 64)
+    heads, d = 6, 64
+    codes, scales, table, lens, start = c.dev()
+    wide = torch.randn(4, (heads + 4) * d, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    q, k, v = (wide[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in ((0, heads), (heads, heads + 2), (heads + 2, heads + 4)))
+    codes2, scales2 = codes.clone(), scales.clone()
+    qmv.kv_append(k, v, codes, scales, table, lens, tok_start=start, max_q=2)
+    qmv.kv_append(k.contiguous(), v.contiguous(), codes2, scales2, table, lens, tok_start=start, max_q=2)
+    assert torch.equal(codes, codes2)
+    ref = qmv.kv_attn(q.contiguous(), codes, scales, table, lens, tok_start=start, max_q=2)
+    host = torch.full((4, 500), 2.0, device="cuda")
+    out = host[:, 100:100 + heads * d].unflatten(1, (heads, d))
+    qmv.kv_attn(q, codes, scales, table, lens, tok_start=start, max_q=2, out=out)
+    assert torch.equal(out, ref) and (host[:, :100] == 2).all() and (host[:, 100 + heads * d:] == 2).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = qmv.kv_attn(q, codes, scales, table, lens, tok_start=start, max_q=2, stream=side)
+    side.synchronize()
+    assert torch.equal(got, ref)
+    qmv.kv_attn(q, codes, scales, table, lens, tok_start=start, max_q=2, out=q)
+    assert torch.equal(q, ref)
+
+
+def test_far_blocks():
+    """A pool of more than 2^32 bytes: block offsets pass 32 bits."""
+    qmv = need_gpu()
+    heads, dim = 8, 128
+    n_blocks = (5 << 30) // (2 * heads * 64 * dim)
+    c = Case(14, [150, 64], [40, 1], heads, dim)
+    small_codes, small_scales, table, lens, start = c.dev()
+    codes = torch.empty((n_blocks, 2, heads, 64 * dim), dtype=torch.int8, device="cuda")
+    scales = torch.empty((n_blocks, 2, heads), device="cuda")
+    off = n_blocks - c.n_blocks
+    codes[off:], scales[off:] = small_codes, small_scales
+    far = torch.where((table >= 0) & (table < c.n_blocks), table + off, -1).int()
+    near = torch.where((table >= 0) & (table < c.n_blocks), table, -1).int()
+    k, v, q = to_dev(c.rows(heads)), to_dev(c.rows(heads)), to_dev(c.rows(2 * heads))
+    kw = dict(tok_start=start, max_q=40)
+    qmv.kv_append(k, v, codes, scales, far, lens, **kw)
+    qmv.kv_append(k, v, small_codes, small_scales, near, lens, **kw)
+    assert torch.equal(codes[off:], small_codes)
+    assert torch.equal(qmv.kv_attn(q, codes, scales, far, lens, **kw),
+                       qmv.kv_attn(q, small_codes, small_scales, near, lens, **kw))

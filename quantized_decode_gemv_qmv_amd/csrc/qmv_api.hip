@@ -840,7 +840,7 @@ QMV_API qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, in
   a.splits = use_ws ? p.splits : 1;
   if (use_ws) {
     uint8_t* b = static_cast<uint8_t*>(ws);
-    const int64_t sums = p.groups * p.splits * p.mr * p.wr * 16;
+    const int64_t sums = p.groups * p.splits * p.wr * 16;
     a.cnt = reinterpret_cast<int*>(b);
     a.part = reinterpret_cast<float*>(b + kAttnCounterBytes);
     a.ml = reinterpret_cast<float*>(b + kAttnCounterBytes + align256(sums * kv->head_dim * 4));

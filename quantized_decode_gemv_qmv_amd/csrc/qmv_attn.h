@@ -44,15 +44,16 @@ struct AppendArgs {
 };
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t st);
 
-// Launch plan of the attention kernel: mr row tiles of 16 rows per wave, wr
-// of a workgroup's four waves along the rows (the others along the keys),
-// row blocks of one (sequence, kv head), and key splits over workgroups.
+// Launch plan of the attention kernel: nw waves a workgroup, wr of them along
+// the rows (16 each; the others along the cache blocks), row blocks of one
+// (sequence, kv head), and workgroups that share its cache blocks.
 struct AttnPlan {
-  int mr, wr, row_blocks, splits;
+  int nw, wr, row_blocks, splits;
   int64_t groups;    // n_seqs * kvh * row_blocks
   int64_t ws_bytes;  // 0 when not split
 };
 constexpr int64_t kAttnCounterBytes = 64 * 1024;
+constexpr int kAttnMaxSplits = 64;  // one a lane where they are added up
 AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, int64_t dim, int64_t width, int cus);
 
 struct AttnArgs {

@@ -2,6 +2,7 @@
 // gfx950.
 #include "qmv_attn.h"
 #include "qmv_device.h"
+#include <cstdlib>  //TUNE
 
 namespace qmv {
 
@@ -13,6 +14,18 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // base-256 digits all lie within -128..127.
 constexpr float kTop = 8323072.0f;
 constexpr float kNegInf = -__builtin_inff();
+// The weights' units are chosen with one bit to spare above the largest
+// weight of the block; a block whose largest is up to three bits below it or
+// one above uses them too.
+constexpr float kAbove = 1.0f, kBelow = 5.0f, kUnit = 2.0f;
+// Blocks after which the integer sums are added up at the latest: one adds at
+// most 64 * 128 * 127 < 2^20 to a sum.
+constexpr int kMost = 1024;
+
+// Waves of a SIMD that the registers leave room for.
+constexpr int attn_waves(int dt, bool keep) { return keep ? (dt <= 4 ? 3 : 2) : 1; }
+// Partial sums of one output loaded at once.
+constexpr int kBatch = 16;
 
 __device__ __forceinline__ i32x4 mfma(i32x4 a, i32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
@@ -32,9 +45,11 @@ __device__ __forceinline__ float add4(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// The base-256 digits of four whole numbers x (as x + 0x808080 in the low 24
-// bits of u): dword e of d[] gets digit e of all four.  x + 0x808080 has the
-// digits of x, each plus 128, as its bytes; the XOR takes the 128 off again.
+// The base-256 digits -128..127 of four whole numbers x: dword e gets digit e
+// of all four.  u holds x + 0x8080, or x + 0x808080 where x may be below zero
+// (SIGNED), in its low 24 bits: the bytes are then the digits, plus 128 in
+// those that the XOR takes it off again.
+template <bool SIGNED>
 __device__ __forceinline__ void digits4(const uint32_t (&u)[4], int& lo, int& mid, int& hi) {
   const uint32_t a = __builtin_amdgcn_perm(u[1], u[0], 0x05010400);  // u0.b0 u1.b0 u0.b1 u1.b1
   const uint32_t b = __builtin_amdgcn_perm(u[3], u[2], 0x05010400);
@@ -42,7 +57,38 @@ __device__ __forceinline__ void digits4(const uint32_t (&u)[4], int& lo, int& mi
   const uint32_t e = __builtin_amdgcn_perm(u[3], u[2], 0x06020c0c);
   lo = (int)(__builtin_amdgcn_perm(b, a, 0x05040100) ^ 0x80808080u);
   mid = (int)(__builtin_amdgcn_perm(b, a, 0x07060302) ^ 0x80808080u);
-  hi = (int)((c | e) ^ 0x80808080u);
+  hi = (int)(SIGNED ? (c | e) ^ 0x80808080u : c | e);
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  v = max8(v);
+  v = fmaxf(v, dpp_f<DPP_MIRROR>(v));
+  const int b = __float_as_int(v);
+  return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 0)), __int_as_float(__builtin_amdgcn_readlane(b, 16))),
+               fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __int_as_float(__builtin_amdgcn_readlane(b, 48))));
+}
+
+// Two floats at once, device scope.
+__device__ __forceinline__ void store8(float* p, float x, float y) {
+  const uint64_t v = ((uint64_t)__float_as_uint(y) << 32) | __float_as_uint(x);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void load8(const float* p, float& x, float& y) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  x = __uint_as_float((uint32_t)v);
+  y = __uint_as_float((uint32_t)(v >> 32));
+}
+
+// The rows of one (sequence, kv head, row block) and the share of its cache
+// blocks that a workgroup takes.
+// 16 cached bytes of a lane.  Where no other wave reads them they pass the
+// caches by.
+template <bool ONCE>
+__device__ __forceinline__ i32x4 load_codes(const int8_t* p) {
+  if constexpr (ONCE)
+    return __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p));
+  else
+    return *reinterpret_cast<const i32x4*>(p);
 }
 
 struct Group {
@@ -95,13 +141,10 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 //   S = scale dq dk (Q K), P = exp(S - m), O = sum dv (P V)
 //
 // K and V hold int8 codes with one scale a block of 64 tokens.  The other
-// operand of each product is taken in 24 bits: a row of q in units of its
-// largest value / kTop, the weights P of one cache block in units of the
-// row's largest weight in that block / kTop, each as three base-256 digits,
-// so that a product is three exact integer products; their sums meet in fp32.
-// The result is as near as fp32 arithmetic's (2^-24 of the largest value),
-// and no code is ever converted.  The scales of a block are one number for
-// the whole 64-key product, which is what they are chosen for.
+// operand of each product is a whole number of 24 bits, as three base-256
+// digits: a row of q in units of its largest value / kTop, the weights P dv in
+// units that follow the row's largest (below).  A product is then three exact
+// integer products, whose sums meet in fp32; no code is ever converted.
 //
 // v_mfma_i32_16x16x64_i8: lane l supplies 16 bytes of A row l % 16 and of B
 // column l % 16 for k = 16 (l / 16) .., and gets D[4 (l / 16) + r][l % 16].
@@ -113,29 +156,43 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 // in the cache, is loaded 16 bytes a lane.  O^T gives a lane four dims of its
 // row at a time.
 //
-// A wave owns MR tiles of 16 rows; a workgroup's four waves are a.wr along the
-// rows and 4 / a.wr along the cache blocks, and a.splits workgroups share a
-// group's blocks.  The waves' sums meet in LDS in wave order, the workgroups'
-// through the workspace: the last one to arrive adds them in split order, so
-// the result does not depend on timing.  KS: 64-value steps of the head
-// dimension; FULL: the dimension is all of them.  Bound by the cache's bytes for a few rows, by the vector ALU
-// (about 450 instructions a tile of 16 rows and 64 keys at 128 dims) for many.
-template <int KS, int MR, bool FULL>
-__global__ __launch_bounds__(256, KS * MR <= 4 ? 2 : 1) void k_kv_attn(AttnArgs a) {
-  constexpr int DT = 4 * KS;          // 16-dim tiles of the output
-  constexpr int LD = 64 * KS + 4;     // LDS row stride (floats)
-  extern __shared__ float lds[];      // [4 waves][16 rows][LD], then [4][16][2]
-  float* lds_ml = lds + 4 * 16 * LD;
+// The three integer sums of O stay in the matrix registers from block to
+// block, as long as every row's largest weight in the block lies within
+// 2^-kBelow .. 2^kAbove of what the units were chosen by; else they are added
+// to the fp32 sums in LDS and the units chosen anew.  A weight is so held to
+// 2^-(23 - kAbove - kBelow) = 2^-19 of the largest of its block, mostly to
+// 2^-22, and a block costs the vector ALU nothing for O (a multiply-add of
+// every output a block took 160 of 380 instructions at 128 dims).
+//
+// A wave owns MR tiles of 16 rows; of a workgroup's NW waves a.wr lie along
+// the rows and NW / a.wr along the cache blocks, and a.splits workgroups share
+// a group's blocks.  K of the next block is loaded when the scores of this one
+// are done, V when its product is: the loads need no registers of their own
+// and have half a block's work to arrive in.  The waves' sums meet in LDS in
+// wave order, the workgroups' through the workspace: the last one to arrive
+// adds them in split order, so the result does not depend on timing.  KS:
+// 64-value steps of the head dimension; FULL: the dimension is all of them.
+template <int DT, int NW, bool KEEP, bool FULL, bool ONE>
+__global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnArgs a) {
+  constexpr int KS = (DT + 3) / 4;     // 64-value steps of a score
+  constexpr int LD = 16 * DT + 4;      // LDS row stride of the sums (floats)
+  constexpr int QLD = 64 * KS + 16;    // and of q's digits (bytes)
+  constexpr int T = 64 * NW;
+  constexpr bool QREG = KS <= 2;       // q's digits stay in registers
+  extern __shared__ float lds[];       // [NW][16 rows][LD] fp32 sums, [NW][16][2] (maximum, total), digits of q
+  float* lds_ml = lds + NW * 16 * LD;
+  int8_t* lds_q = reinterpret_cast<int8_t*>(lds_ml + NW * 16 * 2);  // [3][16 wr][QLD]
+  __shared__ float s_unit[16 * NW];
   const KvView& kv = a.kv;
-  const int dim = FULL ? 64 * KS : kv.dim;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int dim = FULL ? 16 * DT : kv.dim;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g4 = lane >> 4;
   const int split = blockIdx.x % a.splits, gid = blockIdx.x / a.splits;
   const Group g = group_of(a, gid);
   const int rows = g.n * a.group;
-  const int wr = a.wr, wk = 4 / wr;
-  const int my_r = wave % wr, my_k = wave / wr;
-  const int wg_rows = wr * MR * 16;
+  const int wr = ONE ? 1 : a.wr, wk = NW / wr;
+  const int my_r = ONE ? 0 : wave % wr, my_k = ONE ? wave : wave / wr;
+  const int wg_rows = wr * 16;
   const int r0 = g.rb * wg_rows;
   if (r0 >= rows) return;
   const int base = g.len - g.n;  // position of the sequence's first new token
@@ -151,162 +208,280 @@ __global__ __launch_bounds__(256, KS * MR <= 4 ? 2 : 1) void k_kv_attn(AttnArgs 
   if (split >= active) return;
   const int from = b_lo + split * per, to = min(b_hi, from + per);
 
-  // this wave's rows of q, in digits
-  i32x4 qd[MR][3][KS];
-  float cs[MR];   // factor of the integer scores, without the block's scale
-  int pos[MR];
+  // q: 16 lanes a row, four rows a wave at a time
+  constexpr int QJ = ONE ? 1 : 4;
+  const int n_rows = min(rows - r0, wg_rows);
+  f32x4 qv[QJ][KS];
 #pragma unroll
-  for (int m = 0; m < MR; ++m) {
-    const int row = r0 + (my_r * MR + m) * 16 + c16;
-    const bool valid = row < rows;
-    pos[m] = valid ? base + row / a.group : -1;
-    const float* qp = a.q + (int64_t)(g.t0 + (valid ? row / a.group : 0)) * a.ldq +
-                      (int64_t)(g.head * a.group + (valid ? row % a.group : 0)) * dim;
-    f32x4 v[KS][4];
-    float amax = 0.f;
-    bool finite = true;
+  for (int j = 0; j < QJ; ++j) {
+    const int lr = (j * NW + wave) * 4 + g4;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = 64 * ks + 16 * g4 + 4 * i;
-        v[ks][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (valid && (FULL || d < dim)) v[ks][i] = *reinterpret_cast<const f32x4*>(qp + d);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          finite = finite && fabsf(v[ks][i][c]) < __builtin_inff();
-          amax = fmaxf(amax, fabsf(v[ks][i][c]));
-        }
+    for (int ks = 0; ks < KS; ++ks) {
+      qv[j][ks] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int d = 64 * ks + 4 * c16;
+      if (lr < n_rows && d < dim) {
+        const int row = r0 + lr;
+        qv[j][ks] = *reinterpret_cast<const f32x4*>(a.q + (int64_t)(g.t0 + row / a.group) * a.ldq +
+                                                   (int64_t)(g.head * a.group + row % a.group) * dim + d);
       }
-    amax = max4(amax);
-    const float bad = add4(finite ? 0.f : 1.f);
-    // a row that is not finite gives NaN; one below 1e-30 counts as zero
-    // (its scores are, and kTop / amax stays finite)
-    const float unit = bad == 0.f && amax > 1e-30f ? kTop / amax : 0.f;
-    cs[m] = bad != 0.f ? __builtin_nanf("") : amax / kTop * a.scale;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t u[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float f = unit == 0.f ? 0.f : v[ks][i][c] * unit;
-          u[c] = (uint32_t)((int)rintf(f) + 0x808080);
-        }
-        int lo, mid, hi;
-        digits4(u, lo, mid, hi);
-        qd[m][0][ks][i] = lo;
-        qd[m][1][ks][i] = mid;
-        qd[m][2][ks][i] = hi;
-      }
-  }
-  const int row_lo = r0 + my_r * MR * 16;
-  const int p_lo = base + min(row_lo, rows - 1) / a.group;                  // first row's position
-  const int p_hi = base + min(row_lo + MR * 16 - 1, rows - 1) / a.group;    // last row's
-
-  i32x4 zero = {0, 0, 0, 0};
-  f32x4 acc[MR][DT];
-  float mx[MR], tot[MR];
-#pragma unroll
-  for (int m = 0; m < MR; ++m) {
-    mx[m] = kNegInf;
-    tot[m] = 0.f;
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) acc[m][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  const int32_t* table = kv.table + (int64_t)g.seq * kv.width;
-  const int krow = 16 * (c16 >> 2) + (c16 & 3);  // key of A row c16 in product 0
-  int ids = -1;
-  for (int i = 0, b = from + my_k; b < to; ++i, b += wk) {
-    if ((i & 63) == 0) {  // the next 64 block ids, one a lane
-      const int at = b + wk * lane;
-      ids = at < to ? table[at] : -1;
     }
-    const int id = __builtin_amdgcn_readlane(ids, i & 63);
-    if (id < 0 || id >= kv.n_blocks) continue;  // not in the cache: not seen
-    const int64_t plane = (int64_t)id * 2 * kv.kvh + g.head;
-    const int8_t* kc = kv.codes + plane * (64 * (int64_t)dim);
-    const int8_t* vc = kc + (int64_t)kv.kvh * (64 * (int64_t)dim);
-    const float dk = kv.scales[plane], dv = kv.scales[plane + kv.kvh];
+  }
 
-    i32x4 kf[4][KS], vf[DT];
+  const i32x4 zero = {0, 0, 0, 0};
+  const int krow = 16 * (c16 >> 2) + (c16 & 3);  // key of A row c16 in product 0
+  const int voff = c16 * 64 + 16 * g4;
+  i32x4 kf[4][KS], vf[DT];
+  // Past the head dimension q's digits are zero, whatever K's are: such lanes
+  // read bytes that others read too.
+  auto load_k = [&](int64_t plane) {
+    const int8_t* kc = kv.codes + plane * (64 * (int64_t)dim);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        kf[t][ks] = zero;
-        const int d = 64 * ks + 16 * g4;
-        if (FULL || d < dim) kf[t][ks] = *reinterpret_cast<const i32x4*>(kc + (krow + 4 * t) * dim + d);
+        const int d = FULL && DT % 4 == 0 ? 64 * ks + 16 * g4 : min(64 * ks + 16 * g4, dim - 16);
+        kf[t][ks] = load_codes<ONE>(kc + (uint32_t)((krow + 4 * t) * dim + d));
       }
+  };
+  auto load_v = [&](int64_t plane) {
+    const int8_t* vc = kv.codes + (plane + kv.kvh) * (64 * (int64_t)dim);
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      vf[dt] = zero;
-      if (FULL || 16 * dt < dim) vf[dt] = *reinterpret_cast<const i32x4*>(vc + (16 * dt + c16) * 64 + 16 * g4);
+    for (int dt = 0; dt < DT; ++dt)
+      if (FULL || 16 * dt < dim) vf[dt] = load_codes<ONE>(vc + (uint32_t)(voff + 1024 * dt));
+  };
+  // Ids and scales of 64 blocks at a time, one a lane; blocks that are not in
+  // the cache are left out.  todo: the lanes whose blocks are still to be
+  // loaded, cur the one that is in the registers.
+  const int32_t* table = kv.table + (int64_t)g.seq * kv.width;
+  int c0 = from + my_k - 64 * wk, ids = -1, cur = 0;
+  float dks = 0.f, dvs = 0.f;
+  uint64_t todo = 0;
+  int64_t plane = 0;
+  auto take = [&]() {
+    cur = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    plane = (int64_t)__builtin_amdgcn_readlane(ids, cur) * 2 * kv.kvh + g.head;
+  };
+  auto open = [&]() -> bool {
+    for (c0 += 64 * wk; c0 < to; c0 += 64 * wk) {
+      const int at = c0 + wk * lane;
+      ids = at < to ? table[at] : -1;
+      const bool in = ids >= 0 && ids < kv.n_blocks;
+      const float* sp = kv.scales + (in ? (int64_t)ids * 2 * kv.kvh + g.head : 0);
+      dks = in ? sp[0] : 0.f;
+      dvs = in ? sp[kv.kvh] : 0.f;
+      todo = __ballot(in);
+      if (todo == 0) continue;
+      take();
+      load_k(plane);
+      load_v(plane);
+      return true;
     }
-    const bool edge = 64 * b + 63 > p_lo || (a.window > 0 && 64 * b <= p_hi - a.window);
+    return false;
+  };
+  bool more = open();
 
+  // q in digits, while the first block arrives.  A row below 1e-30 counts as
+  // zero (its scores are, and kTop / amax stays finite), as does one that is
+  // not finite, whose total becomes NaN; the sign of the scale is q's, so that
+  // factors of the integer scores are not below zero.
 #pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      float s[4][4];
-      const float c = cs[m] * dk;
+  for (int j = 0; j < QJ; ++j) {
+    const int lr = (j * NW + wave) * 4 + g4;
+    if (j * NW * 4 >= wg_rows) continue;
+    float amax = 0.f, odd = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        i32x4 h = zero, l = zero;
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          h = mfma(kf[t][ks], qd[m][2][ks], h);
-          l = mfma(kf[t][ks], qd[m][1][ks], l);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) l[r] <<= 8;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) l = mfma(kf[t][ks], qd[m][0][ks], l);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[t][r] = fmaf((float)h[r], 65536.f, (float)l[r]) * c;
+      for (int c = 0; c < 4; ++c) {
+        amax = fmaxf(amax, fabsf(qv[j][ks][c]));
+        odd += qv[j][ks][c] * 0.f;  // NaN if it is not finite
       }
-      if (edge) {
-        const int key = 64 * b + 16 * g4;
+    amax = max8(amax);
+    amax = fmaxf(amax, dpp_f<DPP_MIRROR>(amax));
+    odd = sum8(odd);
+    odd += dpp_f<DPP_MIRROR>(odd);
+    float unit = odd == 0.f && amax > 1e-30f ? kTop / amax : 0.f;
+    if (a.scale < 0.f) unit = -unit;
+    if (c16 == 0 && lr < wg_rows) s_unit[lr] = odd == 0.f ? (unit == 0.f ? 0.f : amax / kTop * fabsf(a.scale)) : odd;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t u[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = key + 4 * t + r;
-            const bool seen = j <= pos[m] && (a.window == 0 || j > pos[m] - a.window);
-            s[t][r] = seen ? s[t][r] : kNegInf;
-          }
+      for (int c = 0; c < 4; ++c) {
+        const float f = unit == 0.f ? 0.f : qv[j][ks][c] * unit;
+        u[c] = (uint32_t)((int)rintf(f) + 0x808080);
       }
-      float bm = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+      int x[3];
+      digits4<true>(u, x[0], x[1], x[2]);
+      if (lr < wg_rows)
 #pragma unroll
-      for (int t = 1; t < 4; ++t)
-        bm = fmaxf(bm, fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])));
-      bm = max4(bm);
-      const float nm = fmaxf(mx[m], bm);
-      const float off = bm == kNegInf ? 0.f : bm;
-      const float noff = nm == kNegInf ? 0.f : nm;
-      const float alpha = __builtin_amdgcn_exp2f(mx[m] - noff), beta = __builtin_amdgcn_exp2f(bm - noff);
-      mx[m] = nm;
-      i32x4 ph, pm, pl;
-      float sum = 0.f;
+        for (int e = 0; e < 3; ++e)
+          *reinterpret_cast<int*>(lds_q + (e * wg_rows + lr) * QLD + 64 * ks + 4 * c16) = x[e];
+    }
+  }
+  __syncthreads();
+  const int8_t* my_q = lds_q + (my_r * 16 + c16) * QLD + 16 * g4;
+  auto q_of = [&](int e, int ks) {
+    return *reinterpret_cast<const i32x4*>(my_q + e * wg_rows * QLD + 64 * ks);
+  };
+  i32x4 qd[3][QREG ? KS : 1];
+  if constexpr (QREG)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        uint32_t u[4];
+    for (int e = 0; e < 3; ++e)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) qd[e][ks] = q_of(e, ks);
+  const float cs = s_unit[my_r * 16 + c16];  // factor of the integer scores, without the block's; NaN: the row is
+  const float csf = cs == cs ? cs : 0.f;
+  const int row = r0 + my_r * 16 + c16;
+  const int pos = row < rows ? base + row / a.group : -1;
+  const int row_lo = r0 + my_r * 16;
+  const int p_lo = base + min(row_lo, rows - 1) / a.group;        // first row's position
+  const int p_hi = base + min(row_lo + 15, rows - 1) / a.group;   // last row's
+
+  // sums of O^T: fp32, or (KEEP) one integer sum a digit, fp32 ones in LDS
+  constexpr int NI = KEEP ? DT : 1, NF = KEEP ? 1 : DT;
+  i32x4 oh[NI], om[NI], ol[NI];
+  f32x4 of[NF];
+  float mx = kNegInf, total = 0.f;  // of the fp32 sums: what weights are relative to (log2), and their total
+  float ref = kNegInf, tot = 0.f;   // the same of the integer sums
+  float dref = 1.f;                 // value scale that the units were chosen by
+  int since = 0;                    // blocks in the integer sums
+  bool fresh = true;                // nothing is in the fp32 sums
+  float* mine = lds + (wave * 16 + c16) * LD + 4 * g4;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) {
+    if constexpr (KEEP)
+      oh[dt] = om[dt] = ol[dt] = zero;
+    else
+      of[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // the integer sums into the fp32 ones
+  auto add_up = [&]() {
+    const float nm = fmaxf(mx, ref);
+    const float keep = mx == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mx - nm);
+    const float w = ref == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ref - nm);
+    const float f = w * (dref * (kUnit / kTop));
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        if (!FULL && 16 * dt >= dim) continue;
+        f32x4* at = reinterpret_cast<f32x4*>(mine + 16 * dt);
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        if (!fresh) s = *at;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float p = __builtin_amdgcn_exp2f(s[t][r] - off);
-          sum += p;
-          // 2^23 + p kTop, rounded: its low 24 bits are the whole number
-          u[r] = __float_as_uint(fmaf(p, kTop, 8388608.f)) + 0x808080u;
+          const float x = fmaf((float)oh[dt][r], 65536.f, fmaf((float)om[dt][r], 256.f, (float)ol[dt][r]));
+          s[r] = fmaf(x, f, s[r] * keep);
         }
-        int lo, mid, hi;
-        digits4(u, lo, mid, hi);
-        pl[t] = lo;
-        pm[t] = mid;
-        ph[t] = hi;
+        *at = s;
+        oh[dt] = om[dt] = ol[dt] = zero;
       }
-      tot[m] = fmaf(tot[m], alpha, sum * beta);
-      const float f = beta * dv * (1.f / kTop);
+    }
+    total = fmaf(total, keep, tot * w);
+    tot = 0.f;
+    mx = nm;
+    since = 0;
+    fresh = false;
+  };
+
+  while (more) {
+    const int b = c0 + wk * cur;
+    const float dk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dks), cur));
+    const float dv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dvs), cur));
+    float s[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      i32x4 h = zero, l = zero;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        l = mfma(kf[t][ks], QREG ? qd[1][QREG ? ks : 0] : q_of(1, ks), l);
+        h = mfma(kf[t][ks], QREG ? qd[2][QREG ? ks : 0] : q_of(2, ks), h);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) l[r] <<= 8;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) l = mfma(kf[t][ks], QREG ? qd[0][QREG ? ks : 0] : q_of(0, ks), l);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[t][r] = fmaf((float)h[r], 65536.f, (float)l[r]);
+    }
+    const bool next = todo != 0;
+    if (next) {
+      take();
+      load_k(plane);
+    }
+    float c = csf * dk;
+    if (64 * b + 63 > p_lo || (a.window > 0 && 64 * b <= p_hi - a.window)) {
+      const int key = 64 * b + 16 * g4;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = key + 4 * t + r;
+          const bool seen = j <= pos && (a.window == 0 || j > pos - a.window);
+          s[t][r] = seen ? s[t][r] * c : kNegInf;
+        }
+      c = 1.f;
+    }
+    float bm = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+#pragma unroll
+    for (int t = 1; t < 4; ++t) bm = fmaxf(bm, fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])));
+    bm = max4(bm) * c;
+    const float dvz = dv > 0.f ? dv : dref;
+    if constexpr (KEEP) {
+      // log2 of the largest weight times value scale over what the units were chosen by
+      const float lr = __builtin_amdgcn_logf(dvz / dref);
+      const float rel = bm - ref, x = rel + lr;
+      const bool anew = bm > kNegInf && !(x <= kAbove && x >= -kBelow && rel <= 30.f);
+      if (__any(anew) || since >= kMost) {
+        if (since > 0) add_up();
+        ref = anew ? bm + (kAbove + lr) : ref;
+        if (fabsf(lr) > 8.f) {  // units by this block's value scale
+          ref = bm + kAbove;
+          dref = dvz;
+        }
+      }
+    } else {
+      ref = bm;
+      dref = dvz;
+    }
+    const float cw = dv / dref * (kTop / kUnit);
+    const float off = ref == kNegInf ? 0.f : ref;
+    i32x4 ph, pm, pl;
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t u[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[t][r], c, -off));
+        sum += p;
+        // 2^23 + 0x8080 + the whole number, rounded, in the low 24 bits
+        u[r] = __float_as_uint(fmaf(p, cw, 8388608.f + 32896.f));
+      }
+      int lo, mid, hi;
+      digits4<false>(u, lo, mid, hi);
+      pl[t] = lo;
+      pm[t] = mid;
+      ph[t] = hi;
+    }
+    if constexpr (KEEP) {
+      tot += sum;
+      ++since;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        if (!FULL && 16 * dt >= dim) continue;
+        oh[dt] = mfma(vf[dt], ph, oh[dt]);
+        om[dt] = mfma(vf[dt], pm, om[dt]);
+        ol[dt] = mfma(vf[dt], pl, ol[dt]);
+      }
+    } else {
+      const float nm = fmaxf(mx, bm);
+      const float keep = mx == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mx - nm);
+      const float w = bm == kNegInf ? 0.f : __builtin_amdgcn_exp2f(bm - nm);
+      const float f = w * (dref * (kUnit / kTop));
+      total = fmaf(total, keep, sum * w);
+      mx = nm;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
         if (!FULL && 16 * dt >= dim) continue;
@@ -316,58 +491,55 @@ __global__ __launch_bounds__(256, KS * MR <= 4 ? 2 : 1) void k_kv_attn(AttnArgs 
         for (int r = 0; r < 4; ++r) l[r] <<= 8;
         l = mfma(vf[dt], pl, l);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[m][dt][r] = fmaf(fmaf((float)h[r], 65536.f, (float)l[r]), f, acc[m][dt][r] * alpha);
+        for (int r = 0; r < 4; ++r) of[dt][r] = fmaf(fmaf((float)h[r], 65536.f, (float)l[r]), f, of[dt][r] * keep);
       }
     }
+    if (next)
+      load_v(plane);
+    else
+      more = open();
   }
-
-  // the waves' sums, row tile by row tile
-  const int quads = dim / 4;
-  const bool whole = active == 1;
-#pragma unroll
-  for (int m = 0; m < MR; ++m) {
-    if (m > 0) __syncthreads();
-    const float t = add4(tot[m]);
+  if constexpr (KEEP) {
+    if (since > 0 || fresh) add_up();
+  } else {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
-      if (FULL || 16 * dt < dim) *reinterpret_cast<f32x4*>(lds + (wave * 16 + c16) * LD + 16 * dt + 4 * g4) = acc[m][dt];
-    if (g4 == 0) {
-      lds_ml[(wave * 16 + c16) * 2] = mx[m];
-      lds_ml[(wave * 16 + c16) * 2 + 1] = t;
+      if (FULL || 16 * dt < dim) *reinterpret_cast<f32x4*>(mine + 16 * dt) = of[dt];
+  }
+
+  // the waves' sums, then the workgroups'
+  total = add4(total);
+  if (g4 == 0) {
+    lds_ml[(wave * 16 + c16) * 2] = mx;
+    lds_ml[(wave * 16 + c16) * 2 + 1] = cs != cs && total > 0.f ? cs : total;
+  }
+  __syncthreads();
+  const int quads = dim / 4;
+  const bool whole = active == 1;
+  for (int f = threadIdx.x; f < n_rows * quads; f += T) {
+    const int lr = f / quads, d = 4 * (f % quads);  // row of the workgroup
+    const int w0 = lr / 16, tr = lr % 16;
+    float top_m = kNegInf;
+    for (int w = w0; w < NW; w += wr) top_m = fmaxf(top_m, lds_ml[(w * 16 + tr) * 2]);
+    const float o = top_m == kNegInf ? 0.f : top_m;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+    for (int w = w0; w < NW; w += wr) {
+      const float e = __builtin_amdgcn_exp2f(lds_ml[(w * 16 + tr) * 2] - o);
+      sum = fmaf(lds_ml[(w * 16 + tr) * 2 + 1], e, sum);
+      const f32x4 x = *reinterpret_cast<const f32x4*>(lds + (w * 16 + tr) * LD + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(x[i], e, v[i]);
     }
-    __syncthreads();
-    for (int f = threadIdx.x; f < wr * 16 * quads; f += 256) {
-      const int lr = f / quads, d = 4 * (f % quads);  // row of the workgroup's wr * 16
-      const int w0 = lr >> 4, cr = lr & 15;
-      const int row = r0 + (w0 * MR + m) * 16 + cr;
-      if (row >= rows) continue;
-      float top_m = kNegInf;
-      for (int w = w0; w < 4; w += wr) top_m = fmaxf(top_m, lds_ml[(w * 16 + cr) * 2]);
-      const float o = top_m == kNegInf ? 0.f : top_m;
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      float total = 0.f;
-      for (int w = w0; w < 4; w += wr) {
-        const float e = __builtin_amdgcn_exp2f(lds_ml[(w * 16 + cr) * 2] - o);
-        total = fmaf(lds_ml[(w * 16 + cr) * 2 + 1], e, total);
-        const f32x4 p = *reinterpret_cast<const f32x4*>(lds + (w * 16 + cr) * LD + d);
+    if (whole) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees nothing is zero
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sum[c] = fmaf(p[c], e, sum[c]);
-      }
-      if (whole) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;  // a row that sees nothing is zero
-        const float v[4] = {sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv};
-        store4(a, g, row, d, v);
-      } else {
-        const int64_t at = ((int64_t)gid * a.splits + split) * (wg_rows) + (w0 * MR + m) * 16 + cr;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          __hip_atomic_store(a.part + at * dim + d + c, sum[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (d == 0) {
-          __hip_atomic_store(a.ml + at * 2, top_m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          __hip_atomic_store(a.ml + at * 2 + 1, total, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-      }
+      for (int i = 0; i < 4; ++i) v[i] *= inv;
+      store4(a, g, r0 + lr, d, v);
+    } else {
+      const int64_t at = ((int64_t)gid * a.splits + split) * wg_rows + lr;
+      store8(a.part + at * dim + d, v[0], v[1]);
+      store8(a.part + at * dim + d + 2, v[2], v[3]);
+      if (d == 0) store8(a.ml + at * 2, top_m, sum);
     }
   }
   if (whole) return;
@@ -381,47 +553,77 @@ __global__ __launch_bounds__(256, KS * MR <= 4 ? 2 : 1) void k_kv_attn(AttnArgs 
   if (threadIdx.x == 0) s_last = atomicAdd(&a.cnt[gid], 1) == active - 1;
   __syncthreads();
   if (!s_last) return;
-  for (int f = threadIdx.x; f < wg_rows * quads; f += 256) {
-    const int lr = f / quads, d = 4 * (f % quads);
-    const int row = r0 + lr;
-    if (row >= rows) break;
-    const int64_t at0 = (int64_t)gid * a.splits * wg_rows + lr;
-    float top_m = kNegInf;
-    for (int sp = 0; sp < active; ++sp)
-      top_m = fmaxf(top_m, __hip_atomic_load(a.ml + (at0 + (int64_t)sp * wg_rows) * 2, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT));
-    const float o = top_m == kNegInf ? 0.f : top_m;
-    float v[4] = {0.f, 0.f, 0.f, 0.f}, total = 0.f;
-    for (int sp = 0; sp < active; ++sp) {
-      const int64_t at = at0 + (int64_t)sp * wg_rows;
-      const float e = __builtin_amdgcn_exp2f(
-          __hip_atomic_load(a.ml + at * 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) - o);
-      total = fmaf(__hip_atomic_load(a.ml + at * 2 + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), e, total);
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        v[c] = fmaf(__hip_atomic_load(a.part + at * dim + d + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), e,
-                    v[c]);
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] *= inv;
-    store4(a, g, row, d, v);
+  // every split's factor of every row, one split a lane (at most 64)
+  const int64_t at0 = (int64_t)gid * a.splits * wg_rows;
+  for (int lr = wave; lr < n_rows; lr += NW) {
+    float m = kNegInf, l = 0.f;
+    if (lane < active) load8(a.ml + (at0 + (int64_t)lane * wg_rows + lr) * 2, m, l);
+    const float top_m = wave_max(m);
+    const float e = top_m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top_m);
+    const float sum = wave_sum(l * e);
+    if (lane < active) lds[lr * a.splits + lane] = sum == 0.f ? 0.f : e / sum;
   }
   if (threadIdx.x == 0) atomicExch(&a.cnt[gid], 0);
+  __syncthreads();
+  const int items = n_rows * quads;
+  // with few outputs, several threads share one along the splits
+  const int sub = items >= T ? 1 : T / items;
+  const int share = (active + sub - 1) / sub;
+  float* meet = lds + n_rows * a.splits;
+  for (int f0 = 0; f0 < items; f0 += T) {
+    const int f = sub == 1 ? f0 + (int)threadIdx.x : (int)threadIdx.x % items;
+    const int part = sub == 1 ? 0 : (int)threadIdx.x / items;
+    const int lr = f / quads, d = 4 * (f % quads);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (f < items && part < sub) {
+      const int s1 = min(active, (part + 1) * share);
+      const float* src = a.part + (at0 + lr) * dim + d;
+      for (int sp = part * share; sp < s1; sp += kBatch) {
+        float x[kBatch][4];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int64_t k = (int64_t)min(sp + j, s1 - 1) * wg_rows * dim;
+          load8(src + k, x[j][0], x[j][1]);
+          load8(src + k + 2, x[j][2], x[j][3]);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const float e = sp + j < s1 ? lds[lr * a.splits + sp + j] : 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = fmaf(x[j][i], e, v[i]);
+        }
+      }
+    }
+    if (sub > 1) {
+      if (part > 0 && part < sub) *reinterpret_cast<f32x4*>(meet + ((part - 1) * items + f) * 4) = f32x4{v[0], v[1], v[2], v[3]};
+      __syncthreads();
+      if (part > 0) return;
+      for (int p = 1; p < sub; ++p) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(meet + ((p - 1) * items + f) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += x[i];
+      }
+    }
+    if (f < items) store4(a, g, r0 + lr, d, v);
+  }
 }
 
 AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, int64_t dim, int64_t width, int cus) {
   AttnPlan p{};
-  const int64_t rows = max_q * (n_heads / kvh);
-  p.mr = rows <= 16 ? 1 : 2;
-  p.wr = rows <= 16 * p.mr ? 1 : rows <= 32 * p.mr ? 2 : 4;
-  const int64_t wg_rows = 16 * p.mr * p.wr;
+  auto env = [](const char* n, int64_t d) { const char* v = getenv(n); return v ? (int64_t)atoll(v) : d; };  //TUNE
+  const int64_t rows = max_q * (n_heads / kvh), tiles = (rows + 15) / 16;
+  const int nw = dim <= 128 ? (int)env("T_NW", 8) : 4;  //TUNE
+  p.nw = nw;
+  p.wr = 1;
+  while (p.wr < p.nw && p.wr < tiles && p.wr < env("T_WR", 4)) p.wr *= 2;
+  const int64_t wg_rows = 16 * p.wr, wk = p.nw / p.wr;
   p.row_blocks = static_cast<int>((rows + wg_rows - 1) / wg_rows);
   p.groups = n_seqs * kvh * p.row_blocks;
-  // two workgroups a compute unit, at least one cache block a wave
-  const int64_t most = (width + 4 / p.wr - 1) / (4 / p.wr);
-  int64_t s = 2 * (int64_t)cus / p.groups;
+  const int64_t mt = env("T_MIN", 2);  //TUNE
+  const int64_t most = (width + mt * wk - 1) / (mt * wk);
+  int64_t s = env("T_TGT", 2) * (int64_t)cus * 4 / p.nw / p.groups;
   s = s > most ? most : s;
+  s = s > kAttnMaxSplits ? kAttnMaxSplits : s;
   p.splits = s < 2 ? 1 : static_cast<int>(s);
   if (p.splits > 1) {
     const int64_t sums = p.groups * p.splits * wg_rows;
@@ -432,38 +634,37 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, 
 
 namespace {
 
-template <int KS, int MR, bool FULL>
-hipError_t launch_full(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const size_t lds = (4 * 16 * (64 * KS + 4) + 4 * 16 * 2) * sizeof(float);
-  if (lds > 64 * 1024) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_attn<KS, MR, FULL>),
+template <int DT, int NW, bool KEEP, bool FULL, bool ONE>
+hipError_t launch_one(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  const size_t lds = NW * 16 * ((16 * DT + 4) + 2) * sizeof(float) + 3 * 16 * p.wr * (64 * ((DT + 3) / 4) + 16);
+  if (lds > 60 * 1024) {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_attn<DT, NW, KEEP, FULL, ONE>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_kv_attn<KS, MR, FULL>), dim3((unsigned)(p.groups * a.splits)), dim3(256), lds, st, a);
+  hipLaunchKernelGGL((k_kv_attn<DT, NW, KEEP, FULL, ONE>), dim3((unsigned)(p.groups * a.splits)), dim3(64 * NW), lds,
+                     st, a);
   return hipGetLastError();
 }
 
-template <int KS, int MR>
+template <int DT, int NW, bool KEEP>
 hipError_t launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  return a.kv.dim == 64 * KS ? launch_full<KS, MR, true>(a, p, st) : launch_full<KS, MR, false>(a, p, st);
-}
-
-template <int KS>
-hipError_t launch_mr(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  return p.mr == 1 ? launch<KS, 1>(a, p, st) : launch<KS, 2>(a, p, st);
+  const bool full = a.kv.dim == 16 * DT;
+  if (p.wr == 1)
+    return full ? launch_one<DT, NW, KEEP, true, true>(a, p, st) : launch_one<DT, NW, KEEP, false, true>(a, p, st);
+  return full ? launch_one<DT, NW, KEEP, true, false>(a, p, st) : launch_one<DT, NW, KEEP, false, false>(a, p, st);
 }
 
 }  // namespace
 
 hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  switch ((a.kv.dim + 63) / 64) {
-    case 1: return launch_mr<1>(a, p, st);
-    case 2: return launch_mr<2>(a, p, st);
-    case 3: return launch_mr<3>(a, p, st);
-    case 4: return launch_mr<4>(a, p, st);
-    default: return hipErrorInvalidValue;
-  }
+  const int dt = a.kv.dim / 16;
+  if (dt <= 4) return p.nw == 4 ? launch<4, 4, true>(a, p, st) : launch<4, 8, true>(a, p, st);
+  if (dt <= 6) return p.nw == 4 ? launch<6, 4, true>(a, p, st) : launch<6, 8, true>(a, p, st);
+  if (dt <= 8) return p.nw == 4 ? launch<8, 4, true>(a, p, st) : launch<8, 8, true>(a, p, st);
+  if (dt <= 12) return launch<12, 4, false>(a, p, st);
+  if (dt <= 16) return launch<16, 4, false>(a, p, st);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace qmv

@@ -491,8 +491,8 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  * A row that sees nothing gives zeros; a row of q that is not finite gives
  * NaN in that row.  Sums are fp32 or exact in integers, maxima and totals
  * fp32; the cached codes enter the products as they are, q rounded to 2^-24 of
- * its row's largest value, the softmax weights to 2^-18 of the largest that
- * the row has in the same block (mostly to 2^-21).
+ * its row's largest value, the softmax weights to 2^-19 of the largest that
+ * the row has in the same block (mostly to 2^-22).
  * q    : fp32 [n_tok][ldq] (device), 16-byte aligned, head h of a row at
  *        columns h * head_dim ..; ldq a multiple of 4, at least
  *        n_heads * head_dim.

@@ -12,6 +12,7 @@ If the library has not been built, importing works but the first call raises
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -131,8 +132,15 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it (0.1 us
+# against 3 us for torch.cuda.current_stream())
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -154,10 +162,12 @@ def row_bytes(fmt: int, k: int) -> int:
     return int(lib().qmv_row_bytes(fmt, k))
 
 
+@functools.lru_cache(maxsize=4096)
 def act_bytes(n_tok: int, k: int) -> int:
     return int(lib().qmv_act_bytes(n_tok, k))
 
 
+@functools.lru_cache(maxsize=4096)
 def act_offsets(n_tok: int, k: int) -> tuple[int, int]:
     L = lib()
     return int(L.qmv_act_offset_d(n_tok, k)), int(L.qmv_act_offset_s(n_tok, k))
@@ -168,6 +178,14 @@ def act_fields(xq: torch.Tensor, n_tok: int, k: int):
     activation buffer."""
     od, os_ = act_offsets(n_tok, k)
     nb = k // 32
+    if xq.numel() < act_bytes(n_tok, k):
+        raise ValueError("activation buffer too small")
+    if xq.numel() % 4 == 0 and xq.storage_offset() % 4 == 0 and xq.dim() == 1 and xq.stride(0) == 1:
+        # two tensor operations a field
+        d, s = xq.view(torch.float32), xq.view(torch.int32)
+        at, shape, st = d.storage_offset(), (n_tok, nb), (nb, 1)
+        return (xq.view(torch.int8).as_strided((n_tok, k), (k, 1)), d.as_strided(shape, st, at + od // 4),
+                s.as_strided(shape, st, at + os_ // 4))
     qs = xq[: n_tok * k].view(torch.int8).view(n_tok, k)
     d = xq[od: od + 4 * n_tok * nb].view(torch.float32).view(n_tok, nb)
     s = xq[os_: os_ + 4 * n_tok * nb].view(torch.int32).view(n_tok, nb)
@@ -413,30 +431,38 @@ def moe_matvec_noalloc(fmt: int, w: torch.Tensor, n_experts: int, n_rows: int, k
 
 
 # ------------------------------------- norm, cache append and attention
-def _here(*tensors) -> torch.device:
+def _here(*tensors) -> int:
     """The current device, on which every tensor has to be: the call is
     enqueued on one of its streams."""
-    dev = torch.cuda.current_device()
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device (cuda:{dev})")
-    return torch.device("cuda", dev)
+            raise ValueError("every tensor must be on the current CUDA device")
+    return dev
 
 
-def _new(shape, dtype, dev, stream) -> torch.Tensor:
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     """A tensor for a call on `stream` to write, of that stream's memory."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _rows(t: torch.Tensor, shape, name: str) -> int:
     """Checks an fp32 row array and gives its row stride."""
-    if t.dtype != torch.float32 or not t.is_cuda or tuple(t.shape) != tuple(shape) or t.stride(-1) != 1 \
-            or (t.dim() == 3 and t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name} must be a float32 CUDA tensor {list(shape)} whose rows lie in one piece")
-    return t.stride(0) if t.shape[0] > 1 else math.prod(t.shape[1:])  # a single row's stride is arbitrary
+    st = t.stride()
+    if t.dtype != torch.float32 or t.shape != shape or st[-1] != 1 \
+            or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
+        raise ValueError(f"{name} must be a float32 tensor {list(shape)} whose rows lie in one piece")
+    return st[0] if shape[0] > 1 else math.prod(shape[1:])  # a single row's stride is arbitrary
+
+
+def _whole(t: torch.Tensor, dtype, name: str) -> int:
+    """Checks a tensor that the call takes in one piece and gives its address."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor")
+    return t.data_ptr()
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
@@ -450,49 +476,54 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
         x = x.view(1, -1)
     if x.dim() != 2:
         raise ValueError("x must be a 1-D or 2-D tensor")
-    n_tok, k = x.shape
-    ldx = _rows(x, x.shape, "x")
-    _need(weight, torch.float32, "weight")
+    _here(x, weight, residual, sum_out, y_out, xq)
+    shape = x.shape
+    n_tok, k = shape
+    ldx = _rows(x, shape, "x")
+    wp = _whole(weight, torch.float32, "weight")
     if weight.numel() != k:
         raise ValueError("weight must hold one value a column of x")
-    dev = _here(x, weight, residual, sum_out, y_out, xq)
-    if residual is not None and residual.dim() == 1:
-        residual = residual.view(1, -1)
-    ldr = 0 if residual is None else _rows(residual, x.shape, "residual")
-    if sum_out is None and residual is not None:
-        sum_out = _new((n_tok, k), torch.float32, dev, stream)
-    lds = 0 if sum_out is None else _rows(sum_out, x.shape, "sum_out")
-    ldy = 0 if y_out is None else _rows(y_out, x.shape, "y_out")
+    rp = sp = yp = None
+    ldr = lds = ldy = 0
+    if residual is not None:
+        if residual.dim() == 1:
+            residual = residual.view(1, -1)
+        ldr, rp = _rows(residual, shape, "residual"), residual.data_ptr()
+        if sum_out is None:
+            sum_out = _new(x, shape, torch.float32, stream)
+    if sum_out is not None:
+        lds, sp = _rows(sum_out, shape, "sum_out"), sum_out.data_ptr()
+    if y_out is not None:
+        ldy, yp = _rows(y_out, shape, "y_out"), y_out.data_ptr()
     nbytes = act_bytes(n_tok, k)
     if xq is None:
-        xq = _new(max(nbytes, 1), torch.uint8, dev, stream)
-    _need(xq, torch.uint8, "xq")
+        xq = _new(x, (max(nbytes, 1),), torch.uint8, stream)
+    qp = _whole(xq, torch.uint8, "xq")
     if xq.numel() < nbytes:
         raise ValueError("activation buffer too small")
-    _check(lib().qmv_rmsnorm_quantize(_ptr(x), ldx, _ptr(residual), ldr, n_tok, k, _ptr(weight), eps, _ptr(sum_out),
-                                      lds, _ptr(y_out), ldy, _ptr(xq), _stream(stream)), "qmv_rmsnorm_quantize")
+    _check(lib().qmv_rmsnorm_quantize(x.data_ptr(), ldx, rp, ldr, n_tok, k, wp, eps, sp, lds, yp, ldy, qp,
+                                      _stream(stream)), "qmv_rmsnorm_quantize")
     return (x if sum_out is None else sum_out), xq
 
 
 def _kv(codes, scales, block_table, seq_lens, tok_start, n_tok, max_q, dim) -> _Kv:
-    _need(codes, torch.int8, "codes")
-    _need(scales, torch.float32, "scales")
-    _need(block_table, torch.int32, "block_table")
-    _need(seq_lens, torch.int32, "seq_lens")
     n_seqs = seq_lens.numel()
-    if codes.dim() != 4 or codes.shape[1] != 2 or codes.shape[3] != KV_BLOCK * dim:
+    cs = codes.shape
+    if len(cs) != 4 or cs[1] != 2 or cs[3] != KV_BLOCK * dim:
         raise ValueError(f"codes must be [n_blocks][2][n_kv_heads][{KV_BLOCK} * head_dim]")
-    if scales.shape != codes.shape[:3]:
+    if scales.shape != cs[:3]:
         raise ValueError("scales must be [n_blocks][2][n_kv_heads]")
-    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
+    ts = block_table.shape
+    if len(ts) != 2 or ts[0] != n_seqs:
         raise ValueError("block_table must be [n_seqs][blocks of a sequence]")
+    start = None
     if tok_start is not None:
-        _need(tok_start, torch.int32, "tok_start")
+        start = _whole(tok_start, torch.int32, "tok_start")
         if tok_start.numel() != n_seqs + 1:
             raise ValueError("tok_start must hold n_seqs + 1 rows")
-    return _Kv(codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[2], dim, block_table.data_ptr(),
-               block_table.shape[1], seq_lens.data_ptr(), None if tok_start is None else tok_start.data_ptr(),
-               n_seqs, n_tok, max_q)
+    return _Kv(_whole(codes, torch.int8, "codes"), _whole(scales, torch.float32, "scales"), cs[0], cs[2], dim,
+               _whole(block_table, torch.int32, "block_table"), ts[1], _whole(seq_lens, torch.int32, "seq_lens"),
+               start, n_seqs, n_tok, max_q)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -504,14 +535,15 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: tor
     [n_blocks][2][n_kv_heads], changed in place.  seq_lens (int32) counts the
     new tokens; block_table int32 [n_seqs][blocks]; tok_start int32
     [n_seqs + 1] the rows of each sequence, at most max_q (None: max_q each)."""
-    if k.dim() != 3 or k.shape != v.shape:
+    shape = k.shape
+    if len(shape) != 3:
         raise ValueError("k and v must be [T][n_kv_heads][head_dim]")
-    if codes.dim() == 4 and codes.shape[2] != k.shape[1]:
-        raise ValueError("k has another number of heads than codes")
-    ldk, ldv = _rows(k, k.shape, "k"), _rows(v, k.shape, "v")
     _here(k, v, codes, scales, block_table, seq_lens, tok_start)
-    kv = _kv(codes, scales, block_table, seq_lens, tok_start, k.shape[0], max_q, k.shape[2])
-    _check(lib().qmv_kv_append(ctypes.byref(kv), _ptr(k), ldk, _ptr(v), ldv, _stream(stream)), "qmv_kv_append")
+    kv = _kv(codes, scales, block_table, seq_lens, tok_start, shape[0], max_q, shape[2])
+    if kv.n_kv_heads != shape[1]:
+        raise ValueError("k has another number of heads than codes")
+    _check(lib().qmv_kv_append(ctypes.byref(kv), k.data_ptr(), _rows(k, shape, "k"), v.data_ptr(),
+                               _rows(v, shape, "v"), _stream(stream)), "qmv_kv_append")
 
 
 def kv_attn_workspace_bytes(n_seqs: int, n_tok: int, max_q: int, n_heads: int, n_kv_heads: int, head_dim: int,
@@ -529,24 +561,26 @@ def kv_attn(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_ta
     [T][n_heads][head_dim] (allocated when None); xq, if given, receives the
     Q8 blocks of its rows.  ``ws`` (uint8, zero-filled once, of
     kv_attn_workspace_bytes bytes) lets workgroups share a sequence."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [T][n_heads][head_dim]")
-    n_tok, n_heads, dim = q.shape
-    ldq = _rows(q, q.shape, "q")
-    dev = _here(q, codes, scales, block_table, seq_lens, tok_start, out, xq, ws)
+    n_tok, n_heads, dim = shape
+    _here(q, codes, scales, block_table, seq_lens, tok_start, out, xq, ws)
     kv = _kv(codes, scales, block_table, seq_lens, tok_start, n_tok, max_q, dim)
+    ldq = _rows(q, shape, "q")
     if out is None:
-        out = _new(q.shape, torch.float32, dev, stream)
-    ldo = _rows(out, q.shape, "out")
+        out = _new(q, shape, torch.float32, stream)
+    ldo = _rows(out, shape, "out")
+    qp = wp = None
+    ws_bytes = 0
     if xq is not None:
-        _need(xq, torch.uint8, "xq")
+        qp = _whole(xq, torch.uint8, "xq")
         if xq.numel() < act_bytes(n_tok, n_heads * dim):
             raise ValueError("activation buffer too small")
     if ws is not None:
-        _need(ws, torch.uint8, "ws")
-    _check(lib().qmv_kv_attn(ctypes.byref(kv), _ptr(q), ldq, n_heads, dim ** -0.5 if scale is None else scale, window,
-                             _ptr(out), ldo, _ptr(xq), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)),
-           "qmv_kv_attn")
+        wp, ws_bytes = _whole(ws, torch.uint8, "ws"), ws.numel()
+    _check(lib().qmv_kv_attn(ctypes.byref(kv), q.data_ptr(), ldq, n_heads, dim ** -0.5 if scale is None else scale,
+                             window, out.data_ptr(), ldo, qp, wp, ws_bytes, _stream(stream)), "qmv_kv_attn")
     return out
 
 

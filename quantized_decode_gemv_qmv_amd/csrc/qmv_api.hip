@@ -730,7 +730,7 @@ QMV_API qmv_status qmv_rmsnorm_quantize(const float* x, int64_t ldx, const float
   a.s = const_cast<int32_t*>(v.s);
   a.rows = static_cast<int>(n_tok);
   a.k = static_cast<int>(k);
-  return hip_status(launch_rmsnorm(a, device_cus(), static_cast<hipStream_t>(stream)));
+  return hip_status(launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
 }
 
 // The sizes of a cache and its call, whatever their pointers.
@@ -816,7 +816,7 @@ QMV_API qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, in
     return QMV_ERR_MISALIGNED;
   const AttnPlan p = attn_plan(kv->n_seqs, kv->max_q, n_heads, kv->n_kv_heads, kv->head_dim, kv->table_width,
                                device_cus());
-  if (p.groups * p.splits >= int64_t(1) << 24) return QMV_ERR_UNSUPPORTED;  // workgroups of one launch
+  if (p.groups >= int64_t(1) << 24) return QMV_ERR_UNSUPPORTED;  // workgroups of one launch
   const bool use_ws = ws != nullptr && p.ws_bytes > 0;
   if (use_ws) {
     if (ws_bytes < static_cast<size_t>(p.ws_bytes)) return QMV_ERR_WORKSPACE;
@@ -840,7 +840,9 @@ QMV_API qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, in
   a.splits = use_ws ? p.splits : 1;
   if (use_ws) {
     uint8_t* b = static_cast<uint8_t*>(ws);
-    const int64_t sums = p.groups * p.splits * p.wr * 16;
+    const int64_t sums = p.grid * p.wr * 16;
+    a.shares = p.shares;
+    a.least = p.least;
     a.cnt = reinterpret_cast<int*>(b);
     a.part = reinterpret_cast<float*>(b + kAttnCounterBytes);
     a.ml = reinterpret_cast<float*>(b + kAttnCounterBytes + align256(sums * kv->head_dim * 4));

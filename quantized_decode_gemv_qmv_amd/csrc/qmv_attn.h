@@ -24,7 +24,7 @@ struct NormArgs {
   int32_t* s;
   int rows, k;
 };
-hipError_t launch_rmsnorm(const NormArgs& a, int cus, hipStream_t st);
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
 
 // The 8-bit cache and the sequences of one call (qmv_kv of the ABI).
 struct KvView {
@@ -46,11 +46,14 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t st);
 
 // Launch plan of the attention kernel: nw waves a workgroup, wr of them along
 // the rows (16 each; the others along the cache blocks), row blocks of one
-// (sequence, kv head), and workgroups that share its cache blocks.
+// (sequence, kv head), and the workgroups that share its cache blocks: splits
+// for every group, or by length, as many as come to shares in all with parts
+// of at least `least` blocks.
 struct AttnPlan {
-  int nw, wr, row_blocks, splits;
+  int nw, wr, row_blocks, splits, shares, least;
   int64_t groups;    // n_seqs * kvh * row_blocks
-  int64_t ws_bytes;  // 0 when not split
+  int64_t grid;      // workgroups with a workspace
+  int64_t ws_bytes;  // 0: none is used
 };
 constexpr int64_t kAttnCounterBytes = 64 * 1024;
 constexpr int kAttnMaxSplits = 64;  // one a lane where they are added up
@@ -68,9 +71,9 @@ struct AttnArgs {
   int8_t* qs;       // NULL, or the Q8 blocks of the output rows
   float* qd;
   int32_t* qsum;
-  int wr, row_blocks, splits;
-  float* part;      // [group][split][row][dim] unnormalized sums, then the
-  float* ml;        // [group][split][row][2] maxima and totals
+  int wr, row_blocks, splits, shares, least;
+  float* part;      // [workgroup][row][dim] unnormalized sums, then the
+  float* ml;        // [workgroup][row][2] maxima and totals
   int* cnt;         // one arrival counter per group
 };
 hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st);

@@ -2,7 +2,6 @@
 // gfx950.
 #include "qmv_attn.h"
 #include "qmv_device.h"
-#include <cstdlib>  //TUNE
 
 namespace qmv {
 
@@ -15,9 +14,9 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr float kTop = 8323072.0f;
 constexpr float kNegInf = -__builtin_inff();
 // The weights' units are chosen with one bit to spare above the largest
-// weight of the block; a block whose largest is up to three bits below it or
+// weight of the block; a block whose largest is up to four bits below it or
 // one above uses them too.
-constexpr float kAbove = 1.0f, kBelow = 5.0f, kUnit = 2.0f;
+constexpr float kAbove = 1.0f, kBelow = 4.0f, kUnit = 2.0f;
 // Blocks after which the integer sums are added up at the latest: one adds at
 // most 64 * 128 * 127 < 2^20 to a sum.
 constexpr int kMost = 1024;
@@ -92,25 +91,92 @@ __device__ __forceinline__ i32x4 load_codes(const int8_t* p) {
 }
 
 struct Group {
-  int seq, head, rb;  // sequence, kv head, row block
-  int t0, n, len;     // first token, new tokens, length
+  int seq, head, rb;   // sequence, kv head, row block
+  int t0, n, len;      // first row, new tokens, length
+  int splits, split;   // workgroups that may share it, and which this is
+  int slot;            // the first one's slot in the workspace
 };
 
-__device__ __forceinline__ Group group_of(const AttnArgs& a, int id) {
-  Group g;
-  g.rb = id % a.row_blocks;
-  const int z = id / a.row_blocks;
-  g.head = z % a.kv.kvh;
-  g.seq = z / a.kv.kvh;
-  g.t0 = g.seq * a.kv.max_q;
-  g.n = a.kv.max_q;
-  if (a.kv.start != nullptr) {
-    g.t0 = min(max(a.kv.start[g.seq], 0), a.kv.n_tok);
-    g.n = min(max(a.kv.start[g.seq + 1], g.t0), a.kv.n_tok) - g.t0;
-    g.n = min(g.n, a.kv.max_q);
+// Rows of a sequence, clamped to what the call has.
+__device__ __forceinline__ void rows_of(const KvView& kv, int seq, int& t0, int& n, int& len) {
+  t0 = seq * kv.max_q;
+  n = kv.max_q;
+  if (kv.start != nullptr) {
+    t0 = min(max(kv.start[seq], 0), kv.n_tok);
+    n = min(max(kv.start[seq + 1], t0), kv.n_tok) - t0;
+    n = min(n, kv.max_q);
   }
-  g.len = max(a.kv.lens[g.seq], 0);
-  return g;
+  len = max(kv.lens[seq], 0);
+}
+
+// Cache blocks [lo, hi) that the rows at positions first .. last see.
+__device__ __forceinline__ void blocks_of(const AttnArgs& a, int first, int last, int& lo, int& hi) {
+  hi = last < 0 ? 0 : min(last / 64 + 1, a.kv.width);
+  lo = a.window > 0 ? max(first - a.window + 1, 0) / 64 : 0;
+}
+
+__device__ __forceinline__ int wave_add(int v) {
+  v = sum8(v);
+  v += dpp_i<DPP_MIRROR>(v);
+  return (__builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16)) +
+         (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
+}
+
+// What workgroup w does; false: nothing.  With a.shares (at most 64 sequences,
+// no more groups than a.shares) sequences are split by their lengths: a lane
+// takes a sequence, and the workgroups of a group are as many as parts of at
+// most q cache blocks need, q the smallest of a geometric series for which all
+// parts are at most a.shares.  Else every group has a.splits workgroups.
+__device__ __forceinline__ bool group_of(const AttnArgs& a, int w, int wg_rows, int wk, Group& g) {
+  if (a.shares == 0) {
+    const int gid = w / a.splits;
+    g.split = w - gid * a.splits;
+    g.splits = a.splits;
+    g.slot = gid * a.splits;
+    g.rb = gid % a.row_blocks;
+    g.head = gid / a.row_blocks % a.kv.kvh;
+    g.seq = gid / a.row_blocks / a.kv.kvh;
+    rows_of(a.kv, g.seq, g.t0, g.n, g.len);
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  int t0 = 0, n = 0, len = 0, run = 0;
+  if (lane < a.kv.n_seqs) {
+    rows_of(a.kv, lane, t0, n, len);
+    int lo, hi;
+    blocks_of(a, len - n, len - 1, lo, hi);
+    run = max(hi - lo, 1);
+  }
+  const int rbs = (n * a.group + wg_rows - 1) / wg_rows;  // 0 without rows
+  const int times = a.kv.kvh * rbs;
+  int q = max((wave_add(run * times) + a.shares - 1) / a.shares, 2 * wk);
+  q = max(q, a.least);
+  int parts = (run + q - 1) / q;
+  while (wave_add(parts * times) > a.shares) {
+    q += q / 8 + 1;
+    parts = (run + q - 1) / q;
+  }
+  int x = parts * times;
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const int y = __shfl_up(x, k, 64);
+    if (lane >= k) x += y;
+  }
+  const uint64_t hit = __ballot(w < x);  // the sequences that end behind w
+  if (hit == 0) return false;
+  const int s = __builtin_ctzll(hit);
+  auto of = [&](int v) { return __builtin_amdgcn_readlane(v, s); };
+  g.seq = s;
+  g.t0 = of(t0);
+  g.n = of(n);
+  g.len = of(len);
+  g.splits = of(parts);
+  const int rel = w - (of(x) - g.splits * of(times)), i = rel / g.splits;
+  g.split = rel - i * g.splits;
+  g.slot = w - g.split;
+  g.head = i / of(rbs);
+  g.rb = i - g.head * of(rbs);
+  return true;
 }
 
 // Stores four values of one output row, and their Q8 block with the eight
@@ -159,19 +225,27 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 // The three integer sums of O stay in the matrix registers from block to
 // block, as long as every row's largest weight in the block lies within
 // 2^-kBelow .. 2^kAbove of what the units were chosen by; else they are added
-// to the fp32 sums in LDS and the units chosen anew.  A weight is so held to
-// 2^-(23 - kAbove - kBelow) = 2^-19 of the largest of its block, mostly to
-// 2^-22, and a block costs the vector ALU nothing for O (a multiply-add of
-// every output a block took 160 of 380 instructions at 128 dims).
+// to the fp32 sums in LDS and the units chosen anew.  A weight is so rounded
+// to half a unit, 2^-19 of the largest of its block or less, mostly 2^-22, and
+// a block costs the vector ALU nothing for O (KEEP; above 128 dims the integer
+// sums do not fit the registers, and fp32 sums take a block's products: 160 of
+// 380 instructions at 128 dims).
 //
-// A wave owns MR tiles of 16 rows; of a workgroup's NW waves a.wr lie along
-// the rows and NW / a.wr along the cache blocks, and a.splits workgroups share
-// a group's blocks.  K of the next block is loaded when the scores of this one
-// are done, V when its product is: the loads need no registers of their own
-// and have half a block's work to arrive in.  The waves' sums meet in LDS in
-// wave order, the workgroups' through the workspace: the last one to arrive
-// adds them in split order, so the result does not depend on timing.  KS:
-// 64-value steps of the head dimension; FULL: the dimension is all of them.
+// A wave owns 16 rows; of a workgroup's NW waves a.wr lie along the rows (ONE:
+// one does) and NW / a.wr along the cache blocks, and several workgroups share
+// a group's blocks (group_of).  K of the next block is loaded when the scores
+// of this one are done, V when its product is: the loads need no registers of
+// their own and have half a block's work to arrive in.  q's digits are made
+// once a workgroup, through LDS.  The waves' sums meet in LDS in wave order, the
+// workgroups' through the workspace: the last one to arrive adds them in split
+// order, so the result does not depend on timing.  DT: 16-dim tiles of the
+// head dimension; FULL: it is all of them.
+//
+// Bound by the cache's bytes where a wave's rows are few: 131072 tokens, 8
+// heads, 128 dims in 53.5 us, of which 40 stream the cache at 6.7 TB/s and the
+// rest is the start (ids, then blocks, then q: 3 us), the waves' unequal ends
+// (5), the joins (4) and the launch.  48 sequences of up to 12000: 123 us, 4.8
+// TB/s.
 template <int DT, int NW, bool KEEP, bool FULL, bool ONE>
 __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnArgs a) {
   constexpr int KS = (DT + 3) / 4;     // 64-value steps of a score
@@ -187,26 +261,24 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   const int dim = FULL ? 16 * DT : kv.dim;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g4 = lane >> 4;
-  const int split = blockIdx.x % a.splits, gid = blockIdx.x / a.splits;
-  const Group g = group_of(a, gid);
-  const int rows = g.n * a.group;
   const int wr = ONE ? 1 : a.wr, wk = NW / wr;
   const int my_r = ONE ? 0 : wave % wr, my_k = ONE ? wave : wave / wr;
   const int wg_rows = wr * 16;
+  Group g;
+  if (!group_of(a, blockIdx.x, wg_rows, wk, g)) return;
+  const int rows = g.n * a.group;
   const int r0 = g.rb * wg_rows;
   if (r0 >= rows) return;
   const int base = g.len - g.n;  // position of the sequence's first new token
 
   // cache blocks that some row of the workgroup sees, and this split's share
-  const int top = base + (min(rows, r0 + wg_rows) - 1) / a.group;  // position of the last row
-  const int b_hi = top < 0 ? 0 : min(top / 64 + 1, kv.width);
-  const int low = base + r0 / a.group;
-  const int b_lo = a.window > 0 ? max(low - a.window + 1, 0) / 64 : 0;
+  int b_lo, b_hi;
+  blocks_of(a, base + r0 / a.group, base + (min(rows, r0 + wg_rows) - 1) / a.group, b_lo, b_hi);
   const int nb = max(b_hi - b_lo, 0);
-  const int per = max((nb + a.splits - 1) / a.splits, wk);
+  const int per = max((nb + g.splits - 1) / g.splits, wk);
   const int active = max((nb + per - 1) / per, 1);
-  if (split >= active) return;
-  const int from = b_lo + split * per, to = min(b_hi, from + per);
+  if (g.split >= active) return;
+  const int from = b_lo + g.split * per, to = min(b_hi, from + per);
 
   // q: 16 lanes a row, four rows a wave at a time
   constexpr int QJ = ONE ? 1 : 4;
@@ -435,9 +507,9 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
       const bool anew = bm > kNegInf && !(x <= kAbove && x >= -kBelow && rel <= 30.f);
       if (__any(anew) || since >= kMost) {
         if (since > 0) add_up();
-        ref = anew ? bm + (kAbove + lr) : ref;
+        ref = anew ? bm + lr : ref;
         if (fabsf(lr) > 8.f) {  // units by this block's value scale
-          ref = bm + kAbove;
+          ref = bm;
           dref = dvz;
         }
       }
@@ -536,7 +608,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
       for (int i = 0; i < 4; ++i) v[i] *= inv;
       store4(a, g, r0 + lr, d, v);
     } else {
-      const int64_t at = ((int64_t)gid * a.splits + split) * wg_rows + lr;
+      const int64_t at = (int64_t)(g.slot + g.split) * wg_rows + lr;
       store8(a.part + at * dim + d, v[0], v[1]);
       store8(a.part + at * dim + d + 2, v[2], v[3]);
       if (d == 0) store8(a.ml + at * 2, top_m, sum);
@@ -550,26 +622,26 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   __shared__ int s_last;
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(&a.cnt[gid], 1) == active - 1;
+  if (threadIdx.x == 0) s_last = atomicAdd(&a.cnt[g.slot], 1) == active - 1;
   __syncthreads();
   if (!s_last) return;
   // every split's factor of every row, one split a lane (at most 64)
-  const int64_t at0 = (int64_t)gid * a.splits * wg_rows;
+  const int64_t at0 = (int64_t)g.slot * wg_rows;
   for (int lr = wave; lr < n_rows; lr += NW) {
     float m = kNegInf, l = 0.f;
     if (lane < active) load8(a.ml + (at0 + (int64_t)lane * wg_rows + lr) * 2, m, l);
     const float top_m = wave_max(m);
     const float e = top_m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top_m);
     const float sum = wave_sum(l * e);
-    if (lane < active) lds[lr * a.splits + lane] = sum == 0.f ? 0.f : e / sum;
+    if (lane < active) lds[lr * active + lane] = sum == 0.f ? 0.f : e / sum;
   }
-  if (threadIdx.x == 0) atomicExch(&a.cnt[gid], 0);
+  if (threadIdx.x == 0) atomicExch(&a.cnt[g.slot], 0);
   __syncthreads();
   const int items = n_rows * quads;
   // with few outputs, several threads share one along the splits
   const int sub = items >= T ? 1 : T / items;
   const int share = (active + sub - 1) / sub;
-  float* meet = lds + n_rows * a.splits;
+  float* meet = lds + n_rows * active;
   for (int f0 = 0; f0 < items; f0 += T) {
     const int f = sub == 1 ? f0 + (int)threadIdx.x : (int)threadIdx.x % items;
     const int part = sub == 1 ? 0 : (int)threadIdx.x / items;
@@ -588,7 +660,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const float e = sp + j < s1 ? lds[lr * a.splits + sp + j] : 0.f;
+          const float e = sp + j < s1 ? lds[lr * active + sp + j] : 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = fmaf(x[j][i], e, v[i]);
         }
@@ -610,23 +682,39 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
 
 AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, int64_t dim, int64_t width, int cus) {
   AttnPlan p{};
-  auto env = [](const char* n, int64_t d) { const char* v = getenv(n); return v ? (int64_t)atoll(v) : d; };  //TUNE
   const int64_t rows = max_q * (n_heads / kvh), tiles = (rows + 15) / 16;
-  const int nw = dim <= 128 ? (int)env("T_NW", 8) : 4;  //TUNE
-  p.nw = nw;
+  // Workgroups of eight waves make fewer partial sums of one sequence, those of
+  // four are more alike in length where sequences share the device (us, four /
+  // eight waves, 128 dims: one sequence of 131072 tokens and eight heads 57.0 /
+  // 53.5, of 700 12.9 / 11.1; 48 of up to 12000 126 / 153, 16 of up to 8000
+  // 37.7 / 41.1).
+  const bool small = dim <= 128;
+  p.nw = small && (n_seqs * kvh * tiles <= cus / 4 || tiles >= 4) ? 8 : 4;
   p.wr = 1;
-  while (p.wr < p.nw && p.wr < tiles && p.wr < env("T_WR", 4)) p.wr *= 2;
+  while (p.wr < 4 && p.wr < tiles) p.wr *= 2;
   const int64_t wg_rows = 16 * p.wr, wk = p.nw / p.wr;
   p.row_blocks = static_cast<int>((rows + wg_rows - 1) / wg_rows);
   p.groups = n_seqs * kvh * p.row_blocks;
-  const int64_t mt = env("T_MIN", 2);  //TUNE
-  const int64_t most = (width + mt * wk - 1) / (mt * wk);
-  int64_t s = env("T_TGT", 2) * (int64_t)cus * 4 / p.nw / p.groups;
+  // Workgroups that the device holds at once: their registers leave room for
+  // eight waves a compute unit, four above 128 dims.  More at a time would
+  // start one after the other, each with its own start and end.
+  const int64_t slots = (int64_t)cus * (small ? 8 : 4) / p.nw;
+  // at least two cache blocks a wave
+  const int64_t most = (width + 2 * wk - 1) / (2 * wk);
+  int64_t s = slots / p.groups;
   s = s > most ? most : s;
   s = s > kAttnMaxSplits ? kAttnMaxSplits : s;
   p.splits = s < 2 ? 1 : static_cast<int>(s);
-  if (p.splits > 1) {
-    const int64_t sums = p.groups * p.splits * wg_rows;
+  p.grid = p.groups * p.splits;
+  p.least = static_cast<int>((width + kAttnMaxSplits - 1) / kAttnMaxSplits);
+  if (n_seqs > 1 && n_seqs <= 64 && most > 1 && p.groups <= 2 * slots) {
+    // twice the slots where there are nearly as many groups already (64
+    // sequences of up to 8000 tokens, eight heads: 117 us against 129)
+    p.shares = static_cast<int>(5 * p.groups <= 4 * slots ? slots : 2 * slots);
+    p.grid = p.shares;
+  }
+  if (p.splits > 1 || p.shares > 0) {
+    const int64_t sums = p.grid * wg_rows;
     p.ws_bytes = kAttnCounterBytes + ((sums * dim * 4 + 255) & ~int64_t(255)) + sums * 8;
   }
   return p;
@@ -642,8 +730,8 @@ hipError_t launch_one(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_kv_attn<DT, NW, KEEP, FULL, ONE>), dim3((unsigned)(p.groups * a.splits)), dim3(64 * NW), lds,
-                     st, a);
+  hipLaunchKernelGGL((k_kv_attn<DT, NW, KEEP, FULL, ONE>), dim3((unsigned)(a.part != nullptr ? p.grid : p.groups)),
+                     dim3(64 * NW), lds, st, a);
   return hipGetLastError();
 }
 
@@ -662,6 +750,7 @@ hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) 
   if (dt <= 4) return p.nw == 4 ? launch<4, 4, true>(a, p, st) : launch<4, 8, true>(a, p, st);
   if (dt <= 6) return p.nw == 4 ? launch<6, 4, true>(a, p, st) : launch<6, 8, true>(a, p, st);
   if (dt <= 8) return p.nw == 4 ? launch<8, 4, true>(a, p, st) : launch<8, 8, true>(a, p, st);
+  // above 128 dims the integer sums do not fit the registers
   if (dt <= 12) return launch<12, 4, false>(a, p, st);
   if (dt <= 16) return launch<16, 4, false>(a, p, st);
   return hipErrorInvalidValue;

@@ -56,7 +56,6 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
   const int lo = max(first, 64 * b), hi = min(len, 64 * b + 64);
   if (lo >= hi) return;
   const int id = kv.table[(int64_t)seq * kv.width + b];
-  if (id < 0 || id >= kv.n_blocks) return;
   const int s0 = lo - 64 * b, s1 = hi - 64 * b;  // slots [s0, s1) are new
   const int dim = kv.dim, qd = dim / 4;
   // x of slot j: token t0 + (64 b + j) - (len - n)
@@ -79,14 +78,18 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
     }
     v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (slot >= s0 && slot < s1 && quad < qd) v[i] = *reinterpret_cast<const f32x4*>(x + (tok0 + slot) * ld + 4 * quad);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) amax = fmaxf(amax, fabsf(v[i][c]));
   }
-  __shared__ float part_max[4];
-  amax = wave_max(amax);
-  if ((threadIdx.x & 63) == 0) part_max[threadIdx.x >> 6] = amax;
+  // the id's load was issued before the values'
+  if (id < 0 || id >= kv.n_blocks) return;
   const int64_t plane = ((int64_t)id * 2 + part) * kv.kvh + head;
   const float old = s0 > 0 ? kv.scales[plane] : 0.f;
+  __shared__ float part_max[4];
+#pragma unroll
+  for (int i = 0; i < 4 * NI; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) amax = fmaxf(amax, fabsf(v[i][c]));
+  amax = wave_max(amax);
+  if ((threadIdx.x & 63) == 0) part_max[threadIdx.x >> 6] = amax;
   __syncthreads();  // also: every thread has read the old scale before one writes the new one
   amax = fmaxf(fmaxf(part_max[0], part_max[1]), fmaxf(part_max[2], part_max[3]));
   const float d = fmaxf(old, amax / 127.0f);

@@ -34,7 +34,8 @@ __device__ __forceinline__ double row_sum(double v) {
 // r = x + res, y = (r * inv) * w with inv = 1 / sqrt(mean r^2 + eps), then the
 // Q8 blocks of y as k_quantize makes them.  TPR threads hold one row in
 // registers, NV 16-byte vectors each, so that x, res and w are read once and r
-// and the blocks written once: 13.25 bytes a value, which bounds the kernel.
+// and the blocks written once: 13.25 bytes a value, which bounds the kernel
+// (8192 x 14336: 275 us, 5.66 TB/s; one row of 4096: 3.2 us, all latency).
 // Eight neighbouring lanes hold a block of 32 (q8_block8).  The squares are
 // summed in fp64 (they are exact there, and the card's fp64 rate leaves the
 // sum hidden behind the loads): inv then does not depend on the order of the
@@ -103,6 +104,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int i = tid + TPR * j;
+    if constexpr (!EARLY) __builtin_amdgcn_sched_barrier(0);  // one at a time: the registers hold the row
     if (i < nv) {  // all eight lanes of a block together: k is a multiple of 32
       float v[4];
       f32x4 wj;
@@ -137,23 +139,39 @@ hipError_t launch(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int TPR>
-hipError_t launch_nv(const NormArgs& a, hipStream_t st) {
-  const int nv = (a.k / 4 + TPR - 1) / TPR;
-  if (nv <= 1) return launch<TPR, 1>(a, st);
-  if (nv <= 2) return launch<TPR, 2>(a, st);
-  if (nv <= 4) return launch<TPR, 4>(a, st);
-  if (nv <= 8) return launch<TPR, 8>(a, st);
-  if (nv <= 16) return launch<TPR, 16>(a, st);
-  return hipErrorInvalidValue;
-}
-
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& a, int cus, hipStream_t st) {
-  if (a.rows >= 4 * cus && a.k <= 4096) return launch_nv<64>(a, st);
-  if (a.k <= 4096 || (a.rows >= 2 * cus && a.k <= 16384)) return launch_nv<256>(a, st);
-  return launch_nv<1024>(a, st);
+// Threads of a row by its length: the fewest that hold it in two 16-byte
+// vectors each, up to a whole workgroup.  Us at 1 / 64 / 2048 rows with a
+// residual (256, 512, 1024 threads): 1024 values 2.1 / 2.4 / 7.8, 2.1 / 2.4 /
+// 7.6, 2.2 / 2.4 / 9.0; 4096 values 4.0 / 4.4 / 25.9, 3.2 / 3.5 / 22.4, 3.3 /
+// 3.7 / 23.5; 8192 values 11.8 / 12.7 / 89.7, 5.0 / 5.5 / 44.4, 4.6 / 5.1 /
+// 43.8.  One wave a row saves the barrier where two vectors a lane hold it.
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
+  const int nv = a.k / 4;
+  if (nv <= 64) return launch<64, 1>(a, st);
+  if (nv <= 128) return launch<64, 2>(a, st);
+  if (nv <= 256) return launch<256, 1>(a, st);
+  if (nv <= 512) return launch<256, 2>(a, st);
+  if (nv <= 1024) return launch<512, 2>(a, st);
+  switch ((nv + 1023) / 1024) {
+    case 2: return launch<1024, 2>(a, st);
+    case 3: return launch<1024, 3>(a, st);
+    case 4: return launch<1024, 4>(a, st);
+    case 5:
+    case 6:
+    case 7:
+    case 8: return launch<1024, 8>(a, st);
+    case 9:
+    case 10:
+    case 11:
+    case 12: return launch<1024, 12>(a, st);
+    case 13:
+    case 14:
+    case 15:
+    case 16: return launch<1024, 16>(a, st);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace qmv

@@ -73,8 +73,8 @@ def attend(codes, scales, table, lens, start, max_q, q, scale, window):
     their fma, the factors dq dk scale log2(e), the difference from the
     maximum) and the exponential by 2.  A weight is rounded to half a unit:
     units are 2/8323072 of what p dv may be 2^1 above and, at the largest of
-    its block, 2^-5 below, so half of one is at most 2^5/8323072 < 2^-17.98
-    < 65 u of the block's largest.  The sums over T blocks, and the joins of up
+    its block, 2^-4 below, so half of one is at most 2^4/8323072 < 2^-18.98
+    < 33 u of the block's largest.  The sums over T blocks, and the joins of up
     to 68 partial sums, are off by 4 (T + 72) roundings."""
     n_blocks, _, heads, _ = codes.shape
     n_tok, n_heads, dim = q.shape
@@ -114,5 +114,5 @@ def attend(codes, scales, table, lens, start, max_q, q, scale, window):
                 big = np.zeros(inv.max() + 1)
                 np.maximum.at(big, inv, w)
                 a = np.abs(vx)
-                tol[t0 + i, h] = (w * (ds + w @ ds)) @ a + 4 * u * (inv.max() + 73) * (w @ a) + 65 * u * (big[inv] @ a)
+                tol[t0 + i, h] = (w * (ds + w @ ds)) @ a + 4 * u * (inv.max() + 73) * (w @ a) + 33 * u * (big[inv] @ a)
     return out, tol, rows

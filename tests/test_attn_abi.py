@@ -92,7 +92,8 @@ def test_attn_refusals(change, status):
 def test_workspace_sizes():
     f = q.kv_attn_workspace_bytes
     assert f(1, 1, 1, 32, 8, 128, 64) > 65536
-    assert f(64, 64, 1, 64, 8, 128, 64) == 0  # enough sequences: none is shared
+    assert f(48, 48, 1, 64, 8, 128, 64) > 65536  # shared by length
+    assert f(200, 200, 1, 64, 8, 128, 64) == 0   # enough sequences: none is shared
     assert f(1, 1, 1, 32, 8, 128, 1) == 0     # one block has nothing to share
     for bad in ((0, 1, 1, 32, 8, 128, 64), (1, 0, 1, 32, 8, 128, 64), (1, 1, 0, 32, 8, 128, 64),
                 (1, 1, 1, 33, 8, 128, 64), (1, 1, 1, 32, 0, 128, 64), (1, 1, 1, 32, 8, 100, 64),

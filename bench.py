@@ -245,6 +245,115 @@ class MoeRing:
         return u * self.bytes_per_expert + self.wr.numel() * 4, u
 
 
+# the attention half of a decode layer: hidden size, query heads, kv heads,
+# head dimension, tokens in the cache, layers in the ring (their q4_K weights
+# and caches, 40 MB each, together exceed the 256 MB Infinity Cache)
+ATTN = {"name": "attn_half_q4_k_4096", "hidden": 4096, "heads": 32, "kv_heads": 8, "dim": 128, "context": 8192,
+        "layers": 10}
+
+
+class AttnRing:
+    """Device-resident inputs of the attention half of a decode layer: q4_K
+    projections and an 8-bit block cache for each layer of the ring."""
+
+    def __init__(self, torch, qmv, t):
+        from synth import make_x
+        from synth.device import make_weights_t
+
+        c = ATTN
+        h, d = c["hidden"], c["dim"]
+        self.t, self.nq, self.nkv = t, c["heads"] * d, c["kv_heads"] * d
+        blocks = -(-c["context"] // qmv.KV_BLOCK)
+        dev = "cuda"
+        gen = torch.Generator(device=dev).manual_seed(0)
+        self.layers = []
+        for i in range(c["layers"]):
+            w = {n: make_weights_t(1, rows, k, f"{c['name']}/{i}/{n}", device=dev)
+                 for n, rows, k in (("q", self.nq, h), ("k", self.nkv, h), ("v", self.nkv, h), ("o", h, self.nq))}
+            codes = (torch.randn(blocks, 2, c["kv_heads"], qmv.KV_BLOCK * d, generator=gen, device=dev) * 32)
+            w["codes"] = codes.round_().clamp_(-127, 127).to(torch.int8)
+            w["scales"] = torch.full((blocks, 2, c["kv_heads"]), 1 / 32, device=dev)
+            w["table"] = torch.randperm(blocks, generator=gen, device=dev).int().view(1, blocks)
+            w["norm"] = torch.ones(h, device=dev)
+            self.layers.append(w)
+        self.weight_bytes = sum(self.layers[0][n].numel() for n in "qkvo")
+        self.cache_bytes = self.layers[0]["codes"].numel()
+        self.x = torch.from_numpy(make_x(t, h, f"{c['name']}/x")).to(dev)
+        self.res = torch.from_numpy(make_x(t, h, f"{c['name']}/res")).to(dev)
+        self.lens = torch.full((1,), c["context"], dtype=torch.int32, device=dev)
+        self.r = torch.empty(t, h, device=dev)
+        self.y = torch.empty(t, h, device=dev)
+        self.q, self.k, self.v = (torch.empty(t, n, device=dev) for n in (self.nq, self.nkv, self.nkv))
+        self.out = torch.empty(t, c["heads"], d, device=dev)
+        self.xq = torch.empty(qmv.act_bytes(t, h), dtype=torch.uint8, device=dev)
+        self.oq = torch.empty(qmv.act_bytes(t, self.nq), dtype=torch.uint8, device=dev)
+        self.ws = torch.zeros(qmv.kv_attn_workspace_bytes(1, t, t, c["heads"], c["kv_heads"], d, blocks),
+                              dtype=torch.uint8, device=dev)
+
+    def norm(self, qmv, i):
+        qmv.rmsnorm_quantize(self.x, self.layers[i % len(self.layers)]["norm"], residual=self.res, sum_out=self.r,
+                             xq=self.xq)
+
+    def attn(self, qmv, i):
+        c, w = ATTN, self.layers[i % len(self.layers)]
+        kv = (w["codes"], w["scales"], w["table"], self.lens)
+        q, k, v = (a.unflatten(1, (-1, c["dim"])) for a in (self.q, self.k, self.v))
+        qmv.kv_append(k, v, *kv, max_q=self.t)
+        qmv.kv_attn(q, *kv, max_q=self.t, out=self.out, xq=self.oq, ws=self.ws)
+
+    def step(self, qmv, i):
+        """Residual + norm + Q8, q/k/v projections, append, attention + Q8,
+        output projection + residual."""
+        w, h = self.layers[i % len(self.layers)], ATTN["hidden"]
+        self.norm(qmv, i)
+        qmv.matvec_batch(1, [(w["q"], self.nq, self.q, None), (w["k"], self.nkv, self.k, None),
+                             (w["v"], self.nkv, self.v, None)], h, self.xq, self.t)
+        self.attn(qmv, i)
+        qmv.matvec_batch(1, [(w["o"], h, self.y, self.r)], self.nq, self.oq, self.t)
+
+
+def bench_attn(args, torch, qmv):
+    t = args.tokens
+    log(f"bench: attention half T={t}: generating inputs")
+    ring = AttnRing(torch, qmv, t)
+    ring.step(qmv, 0)
+    torch.cuda.synchronize()
+    if args.profile_launches > 0:
+        for i in range(2 * args.profile_launches):
+            ring.step(qmv, i)
+        torch.cuda.synchronize()
+        log(f"bench: {args.profile_launches} profiled steps after as many warmup steps")
+        return 0
+    per = ATTN["layers"]
+    step = lambda i: ring.step(qmv, i)  # noqa: E731
+    g_full = capture(torch, step, per)
+    tails = [capture(torch, step, n % per) if n % per else None for n in (args.warmup, args.steps)]
+    run_steps(torch, (g_full, per, tails[0]), args.warmup)
+    torch.cuda.synchronize()
+    log(f"bench: timing {args.steps} steps")
+    t0 = time.perf_counter()
+    run_steps(torch, (g_full, per, tails[1]), args.steps)
+    torch.cuda.synchronize()
+    ms = (time.perf_counter() - t0) * 1e3 / args.steps
+    step_bytes = ring.weight_bytes + ring.cache_bytes
+    value = step_bytes / (ms * 1e-3) / 1e9
+    norm_us = timed_replays(torch, lambda i: ring.norm(qmv, i), per)
+    attn_us = timed_replays(torch, lambda i: ring.attn(qmv, i), per)
+    c = ATTN
+    print(json.dumps({
+        "metric": "weight and cache GB/s, attention half of a decode layer", "value": round(value, 1), "unit": "GB/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(ms, 6),
+        "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "int8", "data": "synthetic",
+        "config": {"workload": f"attention half of a decode layer, hidden {c['hidden']}, {c['heads']} query and "
+                               f"{c['kv_heads']} kv heads of {c['dim']}, q4_K projections, {c['context']} tokens "
+                               f"in an 8-bit cache, {t} new token(s)", "tokens": t,
+                   "weight_bytes_per_step": ring.weight_bytes, "cache_bytes_per_step": ring.cache_bytes,
+                   "step": "residual + norm + Q8, q/k/v matvecs, append, attention + Q8, output matvec + residual"},
+        "hbm_frac_step": round(value / HBM_PEAK_GBS, 4),
+        "norm_us": round(norm_us, 3), "append_and_attention_us": round(attn_us, 3)}), flush=True)
+    return 0
+
+
 def capture(torch, fn, count, start=0):
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -735,7 +844,7 @@ def main() -> int:
                     help="untimed steps before the timed ones (the default is about 0.2 s of the one-token "
                          "q4_K step: the GPU's clocks settle in about 0.1 s of continuous work)")
     ap.add_argument("--workload", default="q4_k_14336x4096",
-                    choices=sorted(WORKLOADS) + [MOE["name"], MOE["ffn_name"]])
+                    choices=sorted(WORKLOADS) + [MOE["name"], MOE["ffn_name"], ATTN["name"]])
     ap.add_argument("--tokens", type=int, default=1)
     ap.add_argument("--all-tokens", action="store_true",
                     help="also time the matvec at every token count of the workload")
@@ -798,6 +907,11 @@ def main() -> int:
             print("--tokens must be 1..64 for the MoE workload", file=sys.stderr)
             return 2
         return bench_moe(args, torch, qmv, ffn=args.workload == MOE["ffn_name"])
+    if args.workload == ATTN["name"]:
+        if not 1 <= args.tokens <= 16:
+            print("--tokens must be 1..16", file=sys.stderr)
+            return 2
+        return bench_attn(args, torch, qmv)
     fmt, n, k, token_list, *rest = WORKLOADS[args.workload]
     mats = rest[0] if rest else 1
     t = args.tokens

@@ -1,6 +1,8 @@
 // qmv_attn.hip -- attention of new tokens over the 8-bit block cache, for
 // gfx950.
 #include "qmv_attn.h"
+#include <type_traits>
+
 #include "qmv_device.h"
 
 namespace qmv {
@@ -23,8 +25,6 @@ constexpr int kMost = 1024;
 
 // Waves of a SIMD that the registers leave room for.
 constexpr int attn_waves(int dt, bool keep) { return keep ? (dt <= 4 ? 3 : 2) : 1; }
-// Partial sums of one output loaded at once.
-constexpr int kBatch = 16;
 
 __device__ __forceinline__ i32x4 mfma(i32x4 a, i32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
@@ -149,12 +149,13 @@ __device__ __forceinline__ bool group_of(const AttnArgs& a, int w, int wg_rows, 
   }
   const int rbs = (n * a.group + wg_rows - 1) / wg_rows;  // 0 without rows
   const int times = a.kv.kvh * rbs;
-  int q = max((wave_add(run * times) + a.shares - 1) / a.shares, 2 * wk);
+  int q = max((wave_add(run * times) + a.shares - 1) / a.shares, wk);
   q = max(q, a.least);
-  int parts = (run + q - 1) / q;
+  auto parts_of = [&]() { return run <= 2 * wk ? 1 : (run + q - 1) / q; };
+  int parts = parts_of();
   while (wave_add(parts * times) > a.shares) {
     q += q / 8 + 1;
-    parts = (run + q - 1) / q;
+    parts = parts_of();
   }
   int x = parts * times;
 #pragma unroll
@@ -650,21 +651,25 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
     if (f < items && part < sub) {
       const int s1 = min(active, (part + 1) * share);
       const float* src = a.part + (at0 + lr) * dim + d;
-      for (int sp = part * share; sp < s1; sp += kBatch) {
-        float x[kBatch][4];
+      auto add = [&](int sp, auto batch) {  // so many at once
+        constexpr int B = decltype(batch)::value;
+        float x[B][4];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
+        for (int j = 0; j < B; ++j) {
           const int64_t k = (int64_t)min(sp + j, s1 - 1) * wg_rows * dim;
           load8(src + k, x[j][0], x[j][1]);
           load8(src + k + 2, x[j][2], x[j][3]);
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
+        for (int j = 0; j < B; ++j) {
           const float e = sp + j < s1 ? lds[lr * active + sp + j] : 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = fmaf(x[j][i], e, v[i]);
         }
-      }
+      };
+      int sp = part * share;
+      for (; sp + 4 < s1; sp += 16) add(sp, std::integral_constant<int, 16>());
+      if (sp < s1) add(sp, std::integral_constant<int, 4>());
     }
     if (sub > 1) {
       if (part > 0 && part < sub) *reinterpret_cast<f32x4*>(meet + ((part - 1) * items + f) * 4) = f32x4{v[0], v[1], v[2], v[3]};
@@ -699,8 +704,11 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, 
   // eight waves a compute unit, four above 128 dims.  More at a time would
   // start one after the other, each with its own start and end.
   const int64_t slots = (int64_t)cus * (small ? 8 : 4) / p.nw;
-  // at least two cache blocks a wave
-  const int64_t most = (width + 2 * wk - 1) / (2 * wk);
+  // Up to two cache blocks a wave are not shared, which costs a join through
+  // the workspace; more are, down to one a wave (one sequence, eight heads, us
+  // against at least two a wave: 700 tokens 11.2 unshared, 12.0 shared; 2000
+  // tokens 12.7 / 15.6, 8192 14.4 / 18.2).
+  const int64_t most = width <= 2 * wk ? 1 : (width + wk - 1) / wk;
   int64_t s = slots / p.groups;
   s = s > most ? most : s;
   s = s > kAttnMaxSplits ? kAttnMaxSplits : s;

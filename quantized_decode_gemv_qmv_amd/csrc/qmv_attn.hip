@@ -151,11 +151,18 @@ __device__ __forceinline__ bool group_of(const AttnArgs& a, int w, int wg_rows, 
   const int times = a.kv.kvh * rbs;
   int q = max((wave_add(run * times) + a.shares - 1) / a.shares, wk);
   q = max(q, a.least);
-  auto parts_of = [&]() { return run <= 2 * wk ? 1 : (run + q - 1) / q; };
-  int parts = parts_of();
-  while (wave_add(parts * times) > a.shares) {
+  // A run of up to two blocks a wave has one part.  No lane may leave the loop
+  // or take another way through it than the others: wave_add reads them all.
+  // (So no condition on run inside it, which the compiler made two loops of,
+  // the second without the lanes that the sum is read from; and a bound that
+  // q, which passes any run long before it, cannot reach.)
+  const int whole = run <= 2 * wk ? max(run, 1) : 1;
+  int parts = 0;
+  for (int i = 0; i < 256; ++i) {
+    const int each = max(q, whole);
+    parts = (run + each - 1) / each;
+    if (wave_add(parts * times) <= a.shares) break;
     q += q / 8 + 1;
-    parts = parts_of();
   }
   int x = parts * times;
 #pragma unroll
@@ -629,8 +636,10 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   // every split's factor of every row, one split a lane (at most 64)
   const int64_t at0 = (int64_t)g.slot * wg_rows;
   for (int lr = wave; lr < n_rows; lr += NW) {
-    float m = kNegInf, l = 0.f;
-    if (lane < active) load8(a.ml + (at0 + (int64_t)lane * wg_rows + lr) * 2, m, l);
+    float m, l;
+    load8(a.ml + (at0 + (int64_t)min(lane, active - 1) * wg_rows + lr) * 2, m, l);
+    m = lane < active ? m : kNegInf;
+    l = lane < active ? l : 0.f;
     const float top_m = wave_max(m);
     const float e = top_m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top_m);
     const float sum = wave_sum(l * e);

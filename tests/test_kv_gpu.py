@@ -295,3 +295,19 @@ def test_far_blocks():
     assert torch.equal(codes[off:], small_codes)
     assert torch.equal(qmv.kv_attn(q, codes, scales, far, lens, **kw),
                        qmv.kv_attn(q, small_codes, small_scales, near, lens, **kw))
+
+
+@pytest.mark.parametrize("heads,dim,group,tokens", [(4, 256, 8, 1), (2, 128, 8, 1), (4, 64, 2, 3), (1, 16, 4, 16)])
+def test_many_sequences_shared_by_length(heads, dim, group, tokens):
+    """Sequences of no token to many, their workgroups counted by length: some
+    short enough for one, some not, lanes without a sequence."""
+    qmv = need_gpu()
+    for n in (2, 48, 63, 64, 65):
+        say(f"attn {n} sequences {heads}x{dim}")
+        r = np.random.default_rng(n)
+        lens = r.integers(0, 700, n)
+        lens[: min(n, 3)] = (0, 2500, 1)[: min(n, 3)]
+        counts = r.integers(0, tokens + 1, n)
+        counts[1] = tokens
+        c = Case(20 + n, lens.tolist(), counts.tolist(), heads, dim)
+        check_attn(qmv, c, group, (n, dim))

@@ -261,7 +261,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   constexpr int QLD = 64 * KS + 16;    // and of q's digits (bytes)
   constexpr int T = 64 * NW;
   constexpr bool QREG = KS <= 2;       // q's digits stay in registers
-  extern __shared__ float lds[];       // [NW][16 rows][LD] fp32 sums, [NW][16][2] (maximum, total), digits of q
+  extern __shared__ __align__(16) float lds[];       // [NW][16 rows][LD] fp32 sums, [NW][16][2] (maximum, total), digits of q
   float* lds_ml = lds + NW * 16 * LD;
   int8_t* lds_q = reinterpret_cast<int8_t*>(lds_ml + NW * 16 * 2);  // [3][16 wr][QLD]
   __shared__ float s_unit[16 * NW];

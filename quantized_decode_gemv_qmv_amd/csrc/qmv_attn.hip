@@ -19,6 +19,8 @@ constexpr float kNegInf = -__builtin_inff();
 // weight of the block; a block whose largest is up to four bits below it or
 // one above uses them too.
 constexpr float kAbove = 1.0f, kBelow = 4.0f, kUnit = 2.0f;
+// Value scales below it count in its units.
+constexpr float kTiny = 1e-30f;
 // Blocks after which the integer sums are added up at the latest: one adds at
 // most 64 * 128 * 127 < 2^20 to a sum.
 constexpr int kMost = 1024;
@@ -44,6 +46,12 @@ __device__ __forceinline__ float add4(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // The base-256 digits -128..127 of four whole numbers x: dword e gets digit e
 // of all four.  u holds x + 0x8080, or x + 0x808080 where x may be below zero
 // (SIGNED), in its low 24 bits: the bytes are then the digits, plus 128 in
@@ -66,6 +74,9 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 0)), __int_as_float(__builtin_amdgcn_readlane(b, 16))),
                fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __int_as_float(__builtin_amdgcn_readlane(b, 48))));
 }
+
+// A value that all lanes have, in a scalar register.
+__device__ __forceinline__ float scalar(float v) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))); }
 
 // Two floats at once, device scope.
 __device__ __forceinline__ void store8(float* p, float x, float y) {
@@ -254,8 +265,9 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 // rest is the start (ids, then blocks, then q: 3 us), the waves' unequal ends
 // (5), the joins (4) and the launch.  48 sequences of up to 12000: 123 us, 4.8
 // TB/s.
-template <int DT, int NW, bool KEEP, bool FULL, bool ONE>
+template <int DT, int NW, bool KEEP, bool FULL, int WR>
 __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnArgs a) {
+  constexpr bool ONE = WR == 1;
   constexpr int KS = (DT + 3) / 4;     // 64-value steps of a score
   constexpr int LD = 16 * DT + 4;      // LDS row stride of the sums (floats)
   constexpr int QLD = 64 * KS + 16;    // and of q's digits (bytes)
@@ -269,9 +281,8 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   const int dim = FULL ? 16 * DT : kv.dim;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g4 = lane >> 4;
-  const int wr = ONE ? 1 : a.wr, wk = NW / wr;
-  const int my_r = ONE ? 0 : wave % wr, my_k = ONE ? wave : wave / wr;
-  const int wg_rows = wr * 16;
+  constexpr int wr = WR, wk = NW / WR, wg_rows = 16 * WR;
+  const int my_r = wave % wr, my_k = wave / wr;
   Group g;
   if (!group_of(a, blockIdx.x, wg_rows, wk, g)) return;
   const int rows = g.n * a.group;
@@ -289,7 +300,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   const int from = b_lo + g.split * per, to = min(b_hi, from + per);
 
   // q: 16 lanes a row, four rows a wave at a time
-  constexpr int QJ = ONE ? 1 : 4;
+  constexpr int QJ = 4 * WR > NW ? 4 * WR / NW : 1;  // passes
   const int n_rows = min(rows - r0, wg_rows);
   f32x4 qv[QJ][KS];
 #pragma unroll
@@ -368,7 +379,6 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
 #pragma unroll
   for (int j = 0; j < QJ; ++j) {
     const int lr = (j * NW + wave) * 4 + g4;
-    if (j * NW * 4 >= wg_rows) continue;
     float amax = 0.f, odd = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
@@ -425,9 +435,10 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   f32x4 of[NF];
   float mx = kNegInf, total = 0.f;  // of the fp32 sums: what weights are relative to (log2), and their total
   float ref = kNegInf, tot = 0.f;   // the same of the integer sums
-  float dref = 1.f;                 // value scale that the units were chosen by
+  float dref = 1.f, lref = 0.f, per_dref = kTop / kUnit;  // value scale that the units were chosen by
   int since = 0;                    // blocks in the integer sums
   bool fresh = true;                // nothing is in the fp32 sums
+  float mean = kNegInf;             // of the blocks' largest weights times value scale (log2), the last ones count most
   float* mine = lds + (wave * 16 + c16) * LD + 4 * g4;
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) {
@@ -503,29 +514,35 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
         }
       c = 1.f;
     }
-    float bm = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+    float bm = max3(s[0][0], s[0][1], s[0][2]);
 #pragma unroll
-    for (int t = 1; t < 4; ++t) bm = fmaxf(bm, fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])));
+    for (int i = 3; i < 15; i += 2) bm = max3(bm, s[i / 4][i % 4], s[(i + 1) / 4][(i + 1) % 4]);
+    bm = fmaxf(bm, s[3][3]);
     bm = max4(bm) * c;
-    const float dvz = dv > 0.f ? dv : dref;
     if constexpr (KEEP) {
-      // log2 of the largest weight times value scale over what the units were chosen by
-      const float lr = __builtin_amdgcn_logf(dvz / dref);
+      // x: log2 of the largest weight times value scale over what the units were
+      // chosen by.  They follow the mean of the blocks so far.
+      const float dvu = fmaxf(dv, kTiny);
+      const float lr = dv > 0.f ? __builtin_amdgcn_logf(dvu) - lref : 0.f;
       const float rel = bm - ref, x = rel + lr;
-      const bool anew = bm > kNegInf && !(x <= kAbove && x >= -kBelow && rel <= 30.f);
+      const bool any = bm > kNegInf, anew = any && !(x <= kAbove && x >= -kBelow && rel <= 30.f);
+      const float top = bm + lr + lref;
+      mean = !any ? mean : mean == kNegInf ? top : fmaf(top - mean, 0.125f, mean);
       if (__any(anew) || since >= kMost) {
         if (since > 0) add_up();
-        ref = anew ? bm + lr : ref;
         if (fabsf(lr) > 8.f) {  // units by this block's value scale
-          ref = bm;
-          dref = dvz;
+          dref = scalar(dvu);
+          lref = scalar(lref + lr);
+          per_dref = scalar(kTop / kUnit / dvu);
         }
+        const float r = fminf(fmaxf(mean + 0.5f * (kBelow - kAbove), top - kAbove), top + kBelow) - lref;
+        ref = any ? r : ref;
       }
     } else {
       ref = bm;
-      dref = dvz;
+      dref = dv > 0.f ? dv : 1.f;
     }
-    const float cw = dv / dref * (kTop / kUnit);
+    const float cw = KEEP ? dv * per_dref : dv / dref * (kTop / kUnit);
     const float off = ref == kNegInf ? 0.f : ref;
     i32x4 ph, pm, pl;
     float sum = 0.f;
@@ -739,25 +756,29 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, 
 
 namespace {
 
-template <int DT, int NW, bool KEEP, bool FULL, bool ONE>
+template <int DT, int NW, bool KEEP, bool FULL, int WR>
 hipError_t launch_one(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const size_t lds = NW * 16 * ((16 * DT + 4) + 2) * sizeof(float) + 3 * 16 * p.wr * (64 * ((DT + 3) / 4) + 16);
+  constexpr int lds = NW * 16 * ((16 * DT + 4) + 2) * 4 + 3 * 16 * WR * (64 * ((DT + 3) / 4) + 16);
   if (lds > 60 * 1024) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_attn<DT, NW, KEEP, FULL, ONE>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_attn<DT, NW, KEEP, FULL, WR>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_kv_attn<DT, NW, KEEP, FULL, ONE>), dim3((unsigned)(a.part != nullptr ? p.grid : p.groups)),
+  hipLaunchKernelGGL((k_kv_attn<DT, NW, KEEP, FULL, WR>), dim3((unsigned)(a.part != nullptr ? p.grid : p.groups)),
                      dim3(64 * NW), lds, st, a);
   return hipGetLastError();
 }
 
+template <int DT, int NW, bool KEEP, int WR>
+hipError_t launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  return a.kv.dim == 16 * DT ? launch_one<DT, NW, KEEP, true, WR>(a, p, st) : launch_one<DT, NW, KEEP, false, WR>(a, p, st);
+}
+
 template <int DT, int NW, bool KEEP>
 hipError_t launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const bool full = a.kv.dim == 16 * DT;
-  if (p.wr == 1)
-    return full ? launch_one<DT, NW, KEEP, true, true>(a, p, st) : launch_one<DT, NW, KEEP, false, true>(a, p, st);
-  return full ? launch_one<DT, NW, KEEP, true, false>(a, p, st) : launch_one<DT, NW, KEEP, false, false>(a, p, st);
+  if (p.wr == 1) return launch_rows<DT, NW, KEEP, 1>(a, p, st);
+  if (p.wr == 2) return launch_rows<DT, NW, KEEP, 2>(a, p, st);
+  return launch_rows<DT, NW, KEEP, 4>(a, p, st);
 }
 
 }  // namespace

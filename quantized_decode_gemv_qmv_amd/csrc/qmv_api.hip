@@ -835,7 +835,6 @@ QMV_API qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, in
     a.qd = const_cast<float*>(v.d);
     a.qsum = const_cast<int32_t*>(v.s);
   }
-  a.wr = p.wr;
   a.row_blocks = p.row_blocks;
   a.splits = use_ws ? p.splits : 1;
   if (use_ws) {

@@ -71,7 +71,7 @@ struct AttnArgs {
   int8_t* qs;       // NULL, or the Q8 blocks of the output rows
   float* qd;
   int32_t* qsum;
-  int wr, row_blocks, splits, shares, least;
+  int row_blocks, splits, shares, least;
   float* part;      // [workgroup][row][dim] unnormalized sums, then the
   float* ml;        // [workgroup][row][2] maxima and totals
   int* cnt;         // one arrival counter per group

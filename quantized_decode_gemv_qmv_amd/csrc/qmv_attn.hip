@@ -133,11 +133,55 @@ __device__ __forceinline__ int wave_add(int v) {
          (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
 }
 
-// What workgroup w does; false: nothing.  With a.shares (at most 64 sequences,
-// no more groups than a.shares) sequences are split by their lengths: a lane
-// takes a sequence, and the workgroups of a group are as many as parts of at
-// most q cache blocks need, q the smallest of a geometric series for which all
-// parts are at most a.shares.  Else every group has a.splits workgroups.
+// With a.shares (at most 64 sequences, no more groups than a.shares) sequences
+// are split by their lengths: a lane takes a sequence, and the workgroups of a
+// group are as many as parts of at most q cache blocks need, q the smallest of
+// a geometric series for which all parts are at most a.shares.
+struct Lengths {
+  int t0, n, len;       // of this lane's sequence
+  int parts, rbs, end;  // workgroups of a group, row blocks, where its last group's workgroups end
+};
+
+__device__ __forceinline__ Lengths lengths_of(const AttnArgs& a, int wg_rows, int wk) {
+  const int lane = threadIdx.x & 63;
+  Lengths s{};
+  int run = 0;
+  if (lane < a.kv.n_seqs) {
+    rows_of(a.kv, lane, s.t0, s.n, s.len);
+    int lo, hi;
+    blocks_of(a, s.len - s.n, s.len - 1, lo, hi);
+    run = max(hi - lo, 1);
+  }
+  s.rbs = (s.n * a.group + wg_rows - 1) / wg_rows;  // 0 without rows
+  const int times = a.kv.kvh * s.rbs;
+  int q = max((wave_add(run * times) + a.shares - 1) / a.shares, wk);
+  q = max(q, a.least);
+  // A run of up to two blocks a wave has one part.  No lane may leave the loop
+  // or take another way through it than the others: wave_add reads them all.
+  // (So no condition on run inside it, which the compiler made two loops of,
+  // the second without the lanes that the sum is read from; and a bound that
+  // q, which passes any run long before it, cannot reach.)
+  const int whole = run <= 2 * wk ? max(run, 1) : 1;
+  s.parts = 0;
+  for (int i = 0; i < 256; ++i) {
+    const int each = max(q, whole);
+    s.parts = (run + each - 1) / each;
+    if (wave_add(s.parts * times) <= a.shares) break;
+    q += q / 8 + 1;
+  }
+  s.end = s.parts * times;
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const int y = __shfl_up(s.end, k, 64);
+    if (lane >= k) s.end += y;
+  }
+  return s;
+}
+
+__device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// What workgroup w does; false: nothing.  Without a.shares every group has
+// a.splits workgroups.
 __device__ __forceinline__ bool group_of(const AttnArgs& a, int w, int wg_rows, int wk, Group& g) {
   if (a.shares == 0) {
     const int gid = w / a.splits;
@@ -150,52 +194,47 @@ __device__ __forceinline__ bool group_of(const AttnArgs& a, int w, int wg_rows, 
     rows_of(a.kv, g.seq, g.t0, g.n, g.len);
     return true;
   }
-  const int lane = threadIdx.x & 63;
-  int t0 = 0, n = 0, len = 0, run = 0;
-  if (lane < a.kv.n_seqs) {
-    rows_of(a.kv, lane, t0, n, len);
-    int lo, hi;
-    blocks_of(a, len - n, len - 1, lo, hi);
-    run = max(hi - lo, 1);
-  }
-  const int rbs = (n * a.group + wg_rows - 1) / wg_rows;  // 0 without rows
-  const int times = a.kv.kvh * rbs;
-  int q = max((wave_add(run * times) + a.shares - 1) / a.shares, wk);
-  q = max(q, a.least);
-  // A run of up to two blocks a wave has one part.  No lane may leave the loop
-  // or take another way through it than the others: wave_add reads them all.
-  // (So no condition on run inside it, which the compiler made two loops of,
-  // the second without the lanes that the sum is read from; and a bound that
-  // q, which passes any run long before it, cannot reach.)
-  const int whole = run <= 2 * wk ? max(run, 1) : 1;
-  int parts = 0;
-  for (int i = 0; i < 256; ++i) {
-    const int each = max(q, whole);
-    parts = (run + each - 1) / each;
-    if (wave_add(parts * times) <= a.shares) break;
-    q += q / 8 + 1;
-  }
-  int x = parts * times;
-#pragma unroll
-  for (int k = 1; k < 64; k *= 2) {
-    const int y = __shfl_up(x, k, 64);
-    if (lane >= k) x += y;
-  }
-  const uint64_t hit = __ballot(w < x);  // the sequences that end behind w
+  const Lengths s = lengths_of(a, wg_rows, wk);
+  const uint64_t hit = __ballot(w < s.end);  // the sequences that end behind w
   if (hit == 0) return false;
-  const int s = __builtin_ctzll(hit);
-  auto of = [&](int v) { return __builtin_amdgcn_readlane(v, s); };
-  g.seq = s;
-  g.t0 = of(t0);
-  g.n = of(n);
-  g.len = of(len);
-  g.splits = of(parts);
-  const int rel = w - (of(x) - g.splits * of(times)), i = rel / g.splits;
+  g.seq = __builtin_ctzll(hit);
+  g.t0 = lane_of(s.t0, g.seq);
+  g.n = lane_of(s.n, g.seq);
+  g.len = lane_of(s.len, g.seq);
+  g.splits = lane_of(s.parts, g.seq);
+  const int rbs = lane_of(s.rbs, g.seq);
+  const int rel = w - (lane_of(s.end, g.seq) - g.splits * a.kv.kvh * rbs), i = rel / g.splits;
   g.split = rel - i * g.splits;
   g.slot = w - g.split;
-  g.head = i / of(rbs);
-  g.rb = i - g.head * of(rbs);
+  g.head = i / rbs;
+  g.rb = i - g.head * rbs;
   return true;
+}
+
+// Cache blocks [lo, hi) of a group, and how many of its workgroups have a
+// share of them, `per` blocks each; false: it has no rows.
+__device__ __forceinline__ bool blocks_of(const AttnArgs& a, const Group& g, int wg_rows, int wk, int& lo, int& hi,
+                                          int& per, int& active) {
+  const int rows = g.n * a.group, r0 = g.rb * wg_rows, base = g.len - g.n;
+  if (r0 >= rows) return false;
+  blocks_of(a, base + r0 / a.group, base + (min(rows, r0 + wg_rows) - 1) / a.group, lo, hi);
+  const int nb = max(hi - lo, 0);
+  per = max((nb + g.splits - 1) / g.splits, wk);
+  active = max((nb + per - 1) / per, 1);
+  return true;
+}
+
+// Factors of the n parts of row lr of a group, one part a lane (at most 64).
+__device__ __forceinline__ float factor_of(const AttnArgs& a, int64_t slot, int wg_rows, int lr, int n) {
+  const int lane = threadIdx.x & 63;
+  float m, l;
+  load8(a.ml + ((slot + min(lane, n - 1)) * wg_rows + lr) * 2, m, l);
+  m = lane < n ? m : kNegInf;
+  l = lane < n ? l : 0.f;
+  const float top = wave_max(m);
+  const float e = top == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top);
+  const float sum = wave_sum(l * e);
+  return sum == 0.f ? 0.f : e / sum;
 }
 
 // Stores four values of one output row, and their Q8 block with the eight
@@ -285,18 +324,12 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   const int my_r = wave % wr, my_k = wave / wr;
   Group g;
   if (!group_of(a, blockIdx.x, wg_rows, wk, g)) return;
+  int b_lo, b_hi, per, active;
+  if (!blocks_of(a, g, wg_rows, wk, b_lo, b_hi, per, active)) return;
+  if (g.split >= active) return;
   const int rows = g.n * a.group;
   const int r0 = g.rb * wg_rows;
-  if (r0 >= rows) return;
   const int base = g.len - g.n;  // position of the sequence's first new token
-
-  // cache blocks that some row of the workgroup sees, and this split's share
-  int b_lo, b_hi;
-  blocks_of(a, base + r0 / a.group, base + (min(rows, r0 + wg_rows) - 1) / a.group, b_lo, b_hi);
-  const int nb = max(b_hi - b_lo, 0);
-  const int per = max((nb + g.splits - 1) / g.splits, wk);
-  const int active = max((nb + per - 1) / per, 1);
-  if (g.split >= active) return;
   const int from = b_lo + g.split * per, to = min(b_hi, from + per);
 
   // q: 16 lanes a row, four rows a wave at a time
@@ -634,11 +667,16 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
       store4(a, g, r0 + lr, d, v);
     } else {
       const int64_t at = (int64_t)(g.slot + g.split) * wg_rows + lr;
-      store8(a.part + at * dim + d, v[0], v[1]);
-      store8(a.part + at * dim + d + 2, v[2], v[3]);
+      if constexpr (!ONE) {
+        *reinterpret_cast<f32x4*>(a.part + at * dim + d) = f32x4{v[0], v[1], v[2], v[3]};
+      } else {
+        store8(a.part + at * dim + d, v[0], v[1]);
+        store8(a.part + at * dim + d + 2, v[2], v[3]);
+      }
       if (d == 0) store8(a.ml + at * 2, top_m, sum);
     }
   }
+  if constexpr (!ONE) return;  // k_kv_join
   if (whole) return;
 
   // Partial sums are device-scope atomic accesses (written through and
@@ -650,17 +688,10 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   if (threadIdx.x == 0) s_last = atomicAdd(&a.cnt[g.slot], 1) == active - 1;
   __syncthreads();
   if (!s_last) return;
-  // every split's factor of every row, one split a lane (at most 64)
   const int64_t at0 = (int64_t)g.slot * wg_rows;
   for (int lr = wave; lr < n_rows; lr += NW) {
-    float m, l;
-    load8(a.ml + (at0 + (int64_t)min(lane, active - 1) * wg_rows + lr) * 2, m, l);
-    m = lane < active ? m : kNegInf;
-    l = lane < active ? l : 0.f;
-    const float top_m = wave_max(m);
-    const float e = top_m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top_m);
-    const float sum = wave_sum(l * e);
-    if (lane < active) lds[lr * active + lane] = sum == 0.f ? 0.f : e / sum;
+    const float f = factor_of(a, g.slot, wg_rows, lr, active);
+    if (lane < active) lds[lr * active + lane] = f;
   }
   if (threadIdx.x == 0) atomicExch(&a.cnt[g.slot], 0);
   __syncthreads();
@@ -711,6 +742,62 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   }
 }
 
+// The join of groups of more than 16 rows, as a launch of its own over all of
+// the device: a workgroup alone reads partial sums at some 60 GB/s (8 heads, 64
+// rows each, 128 dims, us joined by the last workgroup / by this: 700 tokens
+// 25.7 / 16.1, 8000 tokens 39.8 / 23.0; 8 rows and 131072 tokens 52.7 / 53.8,
+// 48 sequences of up to 12000 122 / 129).  A thread joins four values of a row,
+// `chunks` workgroups a group; bound by the launch and two loads in a row.
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int wg_rows, int wk, int chunks) {
+  __shared__ float fac[66 * kAttnMaxSplits];  // rows of 256 threads, at least four threads a row
+  const int gid = blockIdx.x / chunks, chunk = blockIdx.x - gid * chunks;
+  Group g;
+  g.rb = gid % a.row_blocks;
+  g.head = gid / a.row_blocks % a.kv.kvh;
+  g.seq = gid / a.row_blocks / a.kv.kvh;
+  rows_of(a.kv, g.seq, g.t0, g.n, g.len);
+  g.splits = a.splits;
+  g.slot = gid * a.splits;
+  if (a.shares > 0) {
+    const Lengths s = lengths_of(a, wg_rows, wk);
+    const int rbs = lane_of(s.rbs, g.seq);
+    g.splits = lane_of(s.parts, g.seq);
+    g.slot = lane_of(s.end, g.seq) - g.splits * (a.kv.kvh * rbs - g.head * rbs - g.rb);
+  }
+  int lo, hi, per, active;
+  if (!blocks_of(a, g, wg_rows, wk, lo, hi, per, active) || active == 1) return;
+  const int r0 = g.rb * wg_rows, n_rows = min(g.n * a.group - r0, wg_rows);
+  const int quads = a.kv.dim / 4, items = n_rows * quads, f0 = chunk * 256;
+  if (f0 >= items) return;
+  const int lr0 = f0 / quads, lr1 = min(n_rows, (f0 + 255) / quads + 1);
+  const int lane = threadIdx.x & 63;
+  for (int lr = lr0 + (int)(threadIdx.x >> 6); lr < lr1; lr += 4) {
+    const float f = factor_of(a, g.slot, wg_rows, lr, active);
+    if (lane < active) fac[(lr - lr0) * active + lane] = f;
+  }
+  __syncthreads();
+  const int f = f0 + (int)threadIdx.x;
+  if (f >= items) return;
+  const int lr = f / quads, d = 4 * (f % quads);
+  const float* src = a.part + ((int64_t)g.slot * wg_rows + lr) * a.kv.dim + d;
+  const float* fs = fac + (lr - lr0) * active;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int B = 16;  // so many at once
+  for (int sp = 0; sp < active; sp += B) {
+    f32x4 x[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      x[j] = *reinterpret_cast<const f32x4*>(src + (int64_t)min(sp + j, active - 1) * wg_rows * a.kv.dim);
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const float e = sp + j < active ? fs[sp + j] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(x[j][i], e, v[i]);
+    }
+  }
+  store4(a, g, r0 + lr, d, v);
+}
+
 AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, int64_t dim, int64_t width, int cus) {
   AttnPlan p{};
   const int64_t rows = max_q * (n_heads / kvh), tiles = (rows + 15) / 16;
@@ -720,9 +807,15 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, 
   // 53.5, of 700 12.9 / 11.1; 48 of up to 12000 126 / 153, 16 of up to 8000
   // 37.7 / 41.1).
   const bool small = dim <= 128;
-  p.nw = small && (n_seqs * kvh * tiles <= cus / 4 || tiles >= 4) ? 8 : 4;
+  const int64_t all = n_seqs * kvh * tiles;
+  p.nw = small && (all <= (tiles > 1 ? cus : cus / 4) || tiles >= 4) ? 8 : 4;
+  // Rows beyond 16: waves along the rows share a cache block's way from L2, those
+  // along the blocks make runs shorter, which counts while the device is not full
+  // of row tiles (us, at most two / four waves along the rows, 128 dims, 8 heads
+  // with 8 query heads: one sequence of 8000 with 8 new tokens 19.8 / 22.9, four
+  // with 16 60.8 / 62.6; 16 of 4000 with 8 77.1 / 67.0).
   p.wr = 1;
-  while (p.wr < 4 && p.wr < tiles) p.wr *= 2;
+  while (p.wr < (all <= cus ? 2 : 4) && p.wr < tiles) p.wr *= 2;
   const int64_t wg_rows = 16 * p.wr, wk = p.nw / p.wr;
   p.row_blocks = static_cast<int>((rows + wg_rows - 1) / wg_rows);
   p.groups = n_seqs * kvh * p.row_blocks;
@@ -783,7 +876,7 @@ hipError_t launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+static hipError_t launch_sums(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   const int dt = a.kv.dim / 16;
   if (dt <= 4) return p.nw == 4 ? launch<4, 4, true>(a, p, st) : launch<4, 8, true>(a, p, st);
   if (dt <= 6) return p.nw == 4 ? launch<6, 4, true>(a, p, st) : launch<6, 8, true>(a, p, st);
@@ -792,6 +885,14 @@ hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) 
   if (dt <= 12) return launch<12, 4, false>(a, p, st);
   if (dt <= 16) return launch<16, 4, false>(a, p, st);
   return hipErrorInvalidValue;
+}
+
+hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  const hipError_t e = launch_sums(a, p, st);
+  if (e != hipSuccess || a.part == nullptr || p.wr == 1) return e;
+  const int wg_rows = 16 * p.wr, chunks = (wg_rows * (a.kv.dim / 4) + 255) / 256;
+  hipLaunchKernelGGL(k_kv_join, dim3((unsigned)(p.groups * chunks)), dim3(256), 0, st, a, wg_rows, p.nw / p.wr, chunks);
+  return hipGetLastError();
 }
 
 }  // namespace qmv

@@ -18,7 +18,7 @@ constexpr float kNegInf = -__builtin_inff();
 // The weights' units are chosen with one bit to spare above the largest
 // weight of the block; a block whose largest is up to four bits below it or
 // one above uses them too.
-constexpr float kAbove = 1.0f, kBelow = 4.0f, kUnit = 2.0f;
+constexpr float kAbove = 1.0f, kBelow = 4.0f, kUnit = 2.0f, kRoom = 1.0f;
 // Value scales below it count in its units.
 constexpr float kTiny = 1e-30f;
 // Blocks after which the integer sums are added up at the latest: one adds at
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
           lref = scalar(lref + lr);
           per_dref = scalar(kTop / kUnit / dvu);
         }
-        const float r = fminf(fmaxf(mean + 0.5f * (kBelow - kAbove), top - kAbove), top + kBelow) - lref;
+        const float r = fminf(fmaxf(mean + (ref == kNegInf ? 0.f : kRoom), top - kAbove), top + kBelow) - lref;
         ref = any ? r : ref;
       }
     } else {

@@ -854,6 +854,8 @@ namespace {
 template <int DT, int NW, bool KEEP, bool FULL, int WR>
 hipError_t launch_one(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   constexpr int lds = NW * 16 * ((16 * DT + 4) + 2) * 4 + 3 * 16 * WR * (64 * ((DT + 3) / 4) + 16);
+  // the join's factors, and the sums that meet (WR 1)
+  static_assert(WR > 1 || lds >= (16 * kAttnMaxSplits + 4 * 64 * NW) * 4);
   if (lds > 60 * 1024) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_attn<DT, NW, KEEP, FULL, WR>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -864,30 +866,36 @@ hipError_t launch_one(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int DT, int NW, bool KEEP, int WR>
-hipError_t launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  return a.kv.dim == 16 * DT ? launch_one<DT, NW, KEEP, true, WR>(a, p, st) : launch_one<DT, NW, KEEP, false, WR>(a, p, st);
+template <int DT, int NW, bool KEEP, bool FULL>
+hipError_t launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  if (p.wr == 1) return launch_one<DT, NW, KEEP, FULL, 1>(a, p, st);
+  if (p.wr == 2) return launch_one<DT, NW, KEEP, FULL, 2>(a, p, st);
+  return launch_one<DT, NW, KEEP, FULL, 4>(a, p, st);
 }
 
-template <int DT, int NW, bool KEEP>
-hipError_t launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  if (p.wr == 1) return launch_rows<DT, NW, KEEP, 1>(a, p, st);
-  if (p.wr == 2) return launch_rows<DT, NW, KEEP, 2>(a, p, st);
-  return launch_rows<DT, NW, KEEP, 4>(a, p, st);
+// Up to 128 dims every multiple of 16 has its own kernel (80 dims: the one for
+// 96 with a bound on the tiles spilled registers); above, the integer sums do
+// not fit the registers.
+hipError_t launch_sums(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+#define QMV_DT(n) \
+  case n: return p.nw == 4 ? launch<n, 4, true, true>(a, p, st) : launch<n, 8, true, true>(a, p, st)
+  switch (a.kv.dim / 16) {
+    QMV_DT(1);
+    QMV_DT(2);
+    QMV_DT(3);
+    QMV_DT(4);
+    QMV_DT(5);
+    QMV_DT(6);
+    QMV_DT(7);
+    QMV_DT(8);
+    case 12: return launch<12, 4, false, true>(a, p, st);
+    case 16: return launch<16, 4, false, true>(a, p, st);
+  }
+#undef QMV_DT
+  return a.kv.dim < 192 ? launch<12, 4, false, false>(a, p, st) : launch<16, 4, false, false>(a, p, st);
 }
 
 }  // namespace
-
-static hipError_t launch_sums(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  const int dt = a.kv.dim / 16;
-  if (dt <= 4) return p.nw == 4 ? launch<4, 4, true>(a, p, st) : launch<4, 8, true>(a, p, st);
-  if (dt <= 6) return p.nw == 4 ? launch<6, 4, true>(a, p, st) : launch<6, 8, true>(a, p, st);
-  if (dt <= 8) return p.nw == 4 ? launch<8, 4, true>(a, p, st) : launch<8, 8, true>(a, p, st);
-  // above 128 dims the integer sums do not fit the registers
-  if (dt <= 12) return launch<12, 4, false>(a, p, st);
-  if (dt <= 16) return launch<16, 4, false>(a, p, st);
-  return hipErrorInvalidValue;
-}
 
 hipError_t launch_kv_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   const hipError_t e = launch_sums(a, p, st);

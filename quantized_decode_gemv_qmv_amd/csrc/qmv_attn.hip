@@ -26,7 +26,7 @@ constexpr float kTiny = 1e-30f;
 constexpr int kMost = 1024;
 
 // Waves of a SIMD that the registers leave room for.
-constexpr int attn_waves(int dt, bool keep) { return keep ? (dt <= 4 ? 3 : 2) : 1; }
+constexpr int attn_waves(int dt) { return dt <= 4 ? 3 : dt <= 8 ? 2 : 1; }
 
 __device__ __forceinline__ i32x4 mfma(i32x4 a, i32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
@@ -89,8 +89,6 @@ __device__ __forceinline__ void load8(const float* p, float& x, float& y) {
   y = __uint_as_float((uint32_t)(v >> 32));
 }
 
-// The rows of one (sequence, kv head, row block) and the share of its cache
-// blocks that a workgroup takes.
 // 16 cached bytes of a lane.  Where no other wave reads them they pass the
 // caches by.
 template <bool ONCE>
@@ -101,6 +99,8 @@ __device__ __forceinline__ i32x4 load_codes(const int8_t* p) {
     return *reinterpret_cast<const i32x4*>(p);
 }
 
+// The rows of one (sequence, kv head, row block) and the share of its cache
+// blocks that a workgroup takes.
 struct Group {
   int seq, head, rb;   // sequence, kv head, row block
   int t0, n, len;      // first row, new tokens, length
@@ -297,15 +297,16 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 // once a workgroup, through LDS.  The waves' sums meet in LDS in wave order, the
 // workgroups' through the workspace: the last one to arrive adds them in split
 // order, so the result does not depend on timing.  DT: 16-dim tiles of the
-// head dimension; FULL: it is all of them.
+// head dimension.
 //
 // Bound by the cache's bytes where a wave's rows are few: 131072 tokens, 8
 // heads, 128 dims in 53.5 us, of which 40 stream the cache at 6.7 TB/s and the
 // rest is the start (ids, then blocks, then q: 3 us), the waves' unequal ends
 // (5), the joins (4) and the launch.  48 sequences of up to 12000: 123 us, 4.8
 // TB/s.
-template <int DT, int NW, bool KEEP, bool FULL, int WR>
-__global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnArgs a) {
+template <int DT, int NW, int WR>
+__global__ __launch_bounds__(64 * NW, attn_waves(DT)) void k_kv_attn(AttnArgs a) {
+  constexpr bool KEEP = DT <= 8;
   constexpr bool ONE = WR == 1;
   constexpr int KS = (DT + 3) / 4;     // 64-value steps of a score
   constexpr int LD = 16 * DT + 4;      // LDS row stride of the sums (floats)
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
   int8_t* lds_q = reinterpret_cast<int8_t*>(lds_ml + NW * 16 * 2);  // [3][16 wr][QLD]
   __shared__ float s_unit[16 * NW];
   const KvView& kv = a.kv;
-  const int dim = FULL ? 16 * DT : kv.dim;
+  constexpr int dim = 16 * DT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g4 = lane >> 4;
   constexpr int wr = WR, wk = NW / WR, wg_rows = 16 * WR;
@@ -363,15 +364,14 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const int d = FULL && DT % 4 == 0 ? 64 * ks + 16 * g4 : min(64 * ks + 16 * g4, dim - 16);
+        const int d = DT % 4 == 0 ? 64 * ks + 16 * g4 : min(64 * ks + 16 * g4, dim - 16);
         kf[t][ks] = load_codes<ONE>(kc + (uint32_t)((krow + 4 * t) * dim + d));
       }
   };
   auto load_v = [&](int64_t plane) {
     const int8_t* vc = kv.codes + (plane + kv.kvh) * (64 * (int64_t)dim);
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-      if (FULL || 16 * dt < dim) vf[dt] = load_codes<ONE>(vc + (uint32_t)(voff + 1024 * dt));
+    for (int dt = 0; dt < DT; ++dt) vf[dt] = load_codes<ONE>(vc + (uint32_t)(voff + 1024 * dt));
   };
   // Ids and scales of 64 blocks at a time, one a lane; blocks that are not in
   // the cache are left out.  todo: the lanes whose blocks are still to be
@@ -489,7 +489,6 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
     if constexpr (KEEP) {
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        if (!FULL && 16 * dt >= dim) continue;
         f32x4* at = reinterpret_cast<f32x4*>(mine + 16 * dt);
         f32x4 s = {0.f, 0.f, 0.f, 0.f};
         if (!fresh) s = *at;
@@ -600,7 +599,6 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
       ++since;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        if (!FULL && 16 * dt >= dim) continue;
         oh[dt] = mfma(vf[dt], ph, oh[dt]);
         om[dt] = mfma(vf[dt], pm, om[dt]);
         ol[dt] = mfma(vf[dt], pl, ol[dt]);
@@ -614,7 +612,6 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
       mx = nm;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        if (!FULL && 16 * dt >= dim) continue;
         const i32x4 h = mfma(vf[dt], ph, zero);
         i32x4 l = mfma(vf[dt], pm, zero);
 #pragma unroll
@@ -633,8 +630,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT, KEEP)) void k_kv_attn(AttnA
     if (since > 0 || fresh) add_up();
   } else {
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-      if (FULL || 16 * dt < dim) *reinterpret_cast<f32x4*>(mine + 16 * dt) = of[dt];
+    for (int dt = 0; dt < DT; ++dt) *reinterpret_cast<f32x4*>(mine + 16 * dt) = of[dt];
   }
 
   // the waves' sums, then the workgroups'
@@ -851,48 +847,58 @@ AttnPlan attn_plan(int64_t n_seqs, int64_t max_q, int64_t n_heads, int64_t kvh, 
 
 namespace {
 
-template <int DT, int NW, bool KEEP, bool FULL, int WR>
+template <int DT, int NW, int WR>
 hipError_t launch_one(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   constexpr int lds = NW * 16 * ((16 * DT + 4) + 2) * 4 + 3 * 16 * WR * (64 * ((DT + 3) / 4) + 16);
   // the join's factors, and the sums that meet (WR 1)
   static_assert(WR > 1 || lds >= (16 * kAttnMaxSplits + 4 * 64 * NW) * 4);
   if (lds > 60 * 1024) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_attn<DT, NW, KEEP, FULL, WR>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_kv_attn<DT, NW, WR>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_kv_attn<DT, NW, KEEP, FULL, WR>), dim3((unsigned)(a.part != nullptr ? p.grid : p.groups)),
-                     dim3(64 * NW), lds, st, a);
+  hipLaunchKernelGGL((k_kv_attn<DT, NW, WR>), dim3((unsigned)(a.part != nullptr ? p.grid : p.groups)), dim3(64 * NW),
+                     lds, st, a);
   return hipGetLastError();
 }
 
-template <int DT, int NW, bool KEEP, bool FULL>
-hipError_t launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-  if (p.wr == 1) return launch_one<DT, NW, KEEP, FULL, 1>(a, p, st);
-  if (p.wr == 2) return launch_one<DT, NW, KEEP, FULL, 2>(a, p, st);
-  return launch_one<DT, NW, KEEP, FULL, 4>(a, p, st);
+template <int DT, int NW>
+hipError_t launch_rows(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  if (p.wr == 1) return launch_one<DT, NW, 1>(a, p, st);
+  if (p.wr == 2) return launch_one<DT, NW, 2>(a, p, st);
+  return launch_one<DT, NW, 4>(a, p, st);
 }
 
-// Up to 128 dims every multiple of 16 has its own kernel (80 dims: the one for
-// 96 with a bound on the tiles spilled registers); above, the integer sums do
-// not fit the registers.
+template <int DT>
+hipError_t launch(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+  if constexpr (DT <= 8)
+    if (p.nw == 8) return launch_rows<DT, 8>(a, p, st);
+  return launch_rows<DT, 4>(a, p, st);
+}
+
+// Every multiple of 16 dims has its own kernel: one for the next multiple of 32
+// or 64, with a bound on its tiles, spilled registers (8 x 8 new tokens of
+// 8000, 160 dims: 138 us, 86 with its own).
 hipError_t launch_sums(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-#define QMV_DT(n) \
-  case n: return p.nw == 4 ? launch<n, 4, true, true>(a, p, st) : launch<n, 8, true, true>(a, p, st)
   switch (a.kv.dim / 16) {
-    QMV_DT(1);
-    QMV_DT(2);
-    QMV_DT(3);
-    QMV_DT(4);
-    QMV_DT(5);
-    QMV_DT(6);
-    QMV_DT(7);
-    QMV_DT(8);
-    case 12: return launch<12, 4, false, true>(a, p, st);
-    case 16: return launch<16, 4, false, true>(a, p, st);
+    case 1: return launch<1>(a, p, st);
+    case 2: return launch<2>(a, p, st);
+    case 3: return launch<3>(a, p, st);
+    case 4: return launch<4>(a, p, st);
+    case 5: return launch<5>(a, p, st);
+    case 6: return launch<6>(a, p, st);
+    case 7: return launch<7>(a, p, st);
+    case 8: return launch<8>(a, p, st);
+    case 9: return launch<9>(a, p, st);
+    case 10: return launch<10>(a, p, st);
+    case 11: return launch<11>(a, p, st);
+    case 12: return launch<12>(a, p, st);
+    case 13: return launch<13>(a, p, st);
+    case 14: return launch<14>(a, p, st);
+    case 15: return launch<15>(a, p, st);
+    case 16: return launch<16>(a, p, st);
+    default: return hipErrorInvalidValue;
   }
-#undef QMV_DT
-  return a.kv.dim < 192 ? launch<12, 4, false, false>(a, p, st) : launch<16, 4, false, false>(a, p, st);
 }
 
 }  // namespace

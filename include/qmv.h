@@ -415,7 +415,8 @@ qmv_status qmv_rmsnorm_quantize(const float* x, int64_t ldx, const float* residu
  *            [head_dim][64 slots];
  *   scales : fp32 [n_blocks][2][n_kv_heads] (keys, then values).
  * Neither needs to be initialized: a block's codes and scale count from the
- * first token on that qmv_kv_append writes into its slot 0.
+ * first token on that qmv_kv_append writes into its slot 0.  Scales of blocks
+ * that a query sees are finite and not below zero.
  *
  * Sequence s of n_seqs has seq_lens[s] tokens, the new ones of the call among
  * them (at its end).  Its token at position p lies in slot p % 64 of block
@@ -492,7 +493,8 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  * NaN in that row.  Sums are fp32 or exact in integers, maxima and totals
  * fp32; the cached codes enter the products as they are, q rounded to 2^-24 of
  * its row's largest value, the softmax weights to 2^-19 of the largest that
- * the row has in the same block (mostly to 2^-22).
+ * the row has in the same block (mostly to 2^-22; up to 128 dims a value scale
+ * below 1e-30 counts in units of 1e-30).
  * q    : fp32 [n_tok][ldq] (device), 16-byte aligned, head h of a row at
  *        columns h * head_dim ..; ldq a multiple of 4, at least
  *        n_heads * head_dim.
@@ -509,7 +511,9 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  *        lets workgroups share a sequence's blocks, which calls with few
  *        sequences and heads need for speed.  NULL runs without.  One
  *        workspace may serve calls of different shapes that do not overlap
- *        in time.  The result with a workspace is the same on every call
+ *        in time.  Calls of more than 16 rows (new tokens x query heads of a
+ *        kv head) that use it take two launches.
+ *        The result with a workspace is the same on every call
  *        with the same arguments, and differs from the one without in
  *        rounding only.
  * n_heads a positive multiple of n_kv_heads of at most QMV_MAX_HEADS, window

@@ -123,7 +123,7 @@ __device__ __forceinline__ void rows_of(const KvView& kv, int seq, int& t0, int&
 // Cache blocks [lo, hi) that the rows at positions first .. last see.
 __device__ __forceinline__ void blocks_of(const AttnArgs& a, int first, int last, int& lo, int& hi) {
   hi = last < 0 ? 0 : min(last / 64 + 1, a.kv.width);
-  lo = a.window > 0 ? max(first - a.window + 1, 0) / 64 : 0;
+  lo = a.window > 0 ? max(max(first, 0) - a.window + 1, 0) / 64 : 0;  // positions below zero see nothing
 }
 
 __device__ __forceinline__ int wave_add(int v) {
@@ -457,10 +457,10 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT)) void k_kv_attn(AttnArgs a)
   const float cs = s_unit[my_r * 16 + c16];  // factor of the integer scores, without the block's; NaN: the row is
   const float csf = cs == cs ? cs : 0.f;
   const int row = r0 + my_r * 16 + c16;
-  const int pos = row < rows ? base + row / a.group : -1;
+  const int pos = row < rows ? max(base + row / a.group, -1) : -1;
   const int row_lo = r0 + my_r * 16;
   const int p_lo = base + min(row_lo, rows - 1) / a.group;        // first row's position
-  const int p_hi = base + min(row_lo + 15, rows - 1) / a.group;   // last row's
+  const int p_hi = max(base + min(row_lo + 15, rows - 1) / a.group, -1);  // last row's
 
   // sums of O^T: fp32, or (KEEP) one integer sum a digit, fp32 ones in LDS
   constexpr int NI = KEEP ? DT : 1, NF = KEEP ? 1 : DT;

@@ -311,3 +311,72 @@ def test_many_sequences_shared_by_length(heads, dim, group, tokens):
         counts[1] = tokens
         c = Case(20 + n, lens.tolist(), counts.tolist(), heads, dim)
         check_attn(qmv, c, group, (n, dim))
+
+
+@pytest.mark.parametrize("dim", [32, 48, 96, 112, 144, 160, 176, 208, 224, 240])
+def test_other_dims(dim):
+    """Each multiple of 16, with few rows, more than 16 and more than 32."""
+    qmv = need_gpu()
+    for lens, counts, group in (([200, 65], [1, 3], 2), ([900, 130], [9, 4], 3), ([700, 90], [64, 20], 2)):
+        c = Case(dim, lens, counts, 2, dim)
+        for ws in (False, True):
+            check_attn(qmv, c, group, (dim, group), ws=ws, xq=dim % 32 == 0)
+
+
+@pytest.mark.parametrize("lens,counts,group", [
+    ([9000], [3], 8),            # 24 rows, one sequence: every group the same parts
+    ([5000, 64, 0, 1300], [9, 9, 0, 2], 8),  # up to 72 rows, parts by length, some one part
+    ([2500], [80], 4),           # row blocks of one sequence
+])
+def test_rows_joined_by_a_second_launch(lens, counts, group):
+    """More than 16 rows over many blocks: the sums of several workgroups, the
+    output over q itself, and a captured call replayed with others between."""
+    qmv = need_gpu()
+    say(f"attn joined {lens} {counts}")
+    c = Case(31, lens, counts, 2, 64)
+    q = c.rows(2 * group)
+    for window in (0, 700):
+        check_attn(qmv, c, group, (lens, window), window=window, xq=True, q=q)
+    codes, scales, table, seq, start = c.dev()
+    need = qmv.kv_attn_workspace_bytes(len(lens), c.n_tok, c.max_q, 2 * group, 2, 64, c.width)
+    assert need > 0
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    kw = dict(tok_start=start, max_q=c.max_q, ws=ws)
+    x = to_dev(q)
+    want = qmv.kv_attn(x, codes, scales, table, seq, **kw)
+    over = x.clone()
+    qmv.kv_attn(over, codes, scales, table, seq, out=over, **kw)
+    assert torch.equal(over, want)
+    out = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        qmv.kv_attn(x, codes, scales, table, seq, out=out, **kw)
+    for _ in range(3):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert torch.equal(qmv.kv_attn(x, codes, scales, table, seq, **kw), want)
+
+
+@pytest.mark.parametrize("dim", [64, 192])
+def test_value_scales_far_apart(dim):
+    """Blocks whose values differ by many powers of two, and blocks of zeros."""
+    qmv = need_gpu()
+    c = Case(33, [1500, 900], [2, 20], 2, dim)
+    c.scales[:, 1] *= np.float32(2.0) ** c.rng.integers(-60, 40, c.scales[:, 1].shape).astype(np.float32)
+    c.scales[:, 1][c.rng.random(c.scales[:, 1].shape) < 0.2] = 0.0
+    for ws in (False, True):
+        check_attn(qmv, c, 3, dim, ws=ws)
+
+
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 40, 2**33])
+def test_the_widest_windows(window):
+    """Windows about the largest whole number, rows before the first token in
+    the same call: those see nothing, the others all of theirs."""
+    qmv = need_gpu()
+    c = Case(34, [3, 130, 70], [10, 5, 70], 2, 64)
+    for ws in (False, True):
+        check_attn(qmv, c, 2, window, window=window, ws=ws)

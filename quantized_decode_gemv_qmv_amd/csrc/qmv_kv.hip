@@ -9,9 +9,24 @@ namespace {
 
 // Whole number nearest to x, halves away from zero, within +-127.
 __device__ __forceinline__ int code_of(float x) {
-  const int r = static_cast<int>(roundf(x));
+  // plus the number below a half, towards zero: below 2^22 a sum that should
+  // not reach the next whole number does not round to it
+  const int r = static_cast<int>(x + copysignf(0.49999997f, x));
   return r > 127 ? 127 : (r < -127 ? -127 : r);
 }
+
+// y / d, correctly rounded: from the reciprocal and, by Markstein's theorem, one
+// step with the exact remainder (a third of a division's instructions, which
+// had bounded the append of many tokens).  d within 2^-100 .. 2^100.
+struct Quotient {
+  float d, inv;
+  bool near;
+  __device__ __forceinline__ explicit Quotient(float x) : d(x), inv(1.f / x), near(x > 1e-30f && x < 1e30f) {}
+  __device__ __forceinline__ float operator()(float y) const {
+    const float q = y * inv;
+    return fmaf(fmaf(-q, d, y), inv, q);
+  }
+};
 
 __device__ __forceinline__ float wave_max(float v) {
   v = max8(v);
@@ -47,8 +62,9 @@ constexpr int kFew = 16;
 // with / without: 16 sequences, 8 heads, 128 dims, one new token 3.2 / 5.6, 256
 // dims 4.1 / 8.9; 8 sequences of 16 3.9 / 6.4).
 // Bound: with few tokens by the launch and two loads in a row (id and length,
-// then the values); 4 sequences of 2000 new tokens, 8 heads, 128 dims: 19.5 us,
-// 4.2 TB/s of the values and codes, at the rate of a large copy (4.9).
+// then the values; 16 x 1: 2.8 us); many by bytes (4 sequences of 2000, 8 heads,
+// 128 dims: 16.7 us, 4.9 TB/s of values and codes, the rate of a large copy; with
+// a division a value 19.7).
 template <int NI, bool FEW>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
   const KvView& kv = a.kv;
@@ -107,10 +123,18 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
   int8_t* codes = kv.codes + plane * (64 * (int64_t)dim);
   if (threadIdx.x == 0) kv.scales[plane] = d;
 
+  const Quotient over(d);
+  if (over.near) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[i][c] = d > 0.f ? v[i][c] / d : 0.f;
+      for (int c = 0; c < 4; ++c) v[i][c] = over(v[i][c]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[i][c] = d > 0.f ? v[i][c] / d : 0.f;
+  }
   if (FEW || part == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

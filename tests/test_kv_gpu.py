@@ -380,3 +380,19 @@ def test_the_widest_windows(window):
     c = Case(34, [3, 130, 70], [10, 5, 70], 2, 64)
     for ws in (False, True):
         check_attn(qmv, c, 2, window, window=window, ws=ws)
+
+
+@pytest.mark.parametrize("uniform", [1, 40])
+def test_append_at_half_steps(uniform):
+    """Values at and one step beside the middle between two codes, with scales
+    that are no power of two, very small and very large ones too."""
+    qmv = need_gpu()
+    for e in (0, -3, -98, -103, 98, 103):
+        c = Case(40, [uniform, 64 + uniform], [uniform] * 2, 2, 64, uniform=uniform)
+        d = (np.float32(2.0) ** e * c.rng.uniform(1, 2, (2 * uniform, 2, 64))).astype(np.float32)
+        d[:] = d[:1, :1, :1]
+        n = c.rng.integers(-127, 127, d.shape)
+        k = ((n + np.float32(0.5)) * d).astype(np.float32)
+        k = np.nextafter(k, np.where(c.rng.random(d.shape) < 0.5, k, np.float32(0))).astype(np.float32)
+        k[..., 0] = 127 * d[..., 0]
+        run_append(qmv, c, k, np.ascontiguousarray(k[:, ::-1, ::-1]), e)

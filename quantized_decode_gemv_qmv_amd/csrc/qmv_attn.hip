@@ -15,9 +15,12 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // base-256 digits all lie within -128..127.
 constexpr float kTop = 8323072.0f;
 constexpr float kNegInf = -__builtin_inff();
-// The weights' units are chosen with one bit to spare above the largest
-// weight of the block; a block whose largest is up to four bits below it or
-// one above uses them too.
+// Units of the weights (kUnit / kTop of what they were chosen by) serve every
+// block whose largest weight is up to kAbove bits above it or kBelow below.  They
+// are chosen at the first block's own largest weight, later kRoom bits above the
+// mean of the blocks so far: each bit of room costs one of the weights', and 0 /
+// 1 / 1.5 of them add the sums up in 0.5 / 0.3 / 0.28 of the blocks (16 rows,
+// block scales that vary by a factor of two).
 constexpr float kAbove = 1.0f, kBelow = 4.0f, kUnit = 2.0f, kRoom = 1.0f;
 // Value scales below it count in its units.
 constexpr float kTiny = 1e-30f;
@@ -283,27 +286,32 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 // The three integer sums of O stay in the matrix registers from block to
 // block, as long as every row's largest weight in the block lies within
 // 2^-kBelow .. 2^kAbove of what the units were chosen by; else they are added
-// to the fp32 sums in LDS and the units chosen anew.  A weight is so rounded
-// to half a unit, 2^-19 of the largest of its block or less, mostly 2^-22, and
-// a block costs the vector ALU nothing for O (KEEP; above 128 dims the integer
-// sums do not fit the registers, and fp32 sums take a block's products: 160 of
-// 380 instructions at 128 dims).
+// to the fp32 sums in LDS (280 instructions at 96 dims, against 250 of a block)
+// and the units chosen anew.  A weight is so rounded to half a unit, 2^-19 of the
+// largest of its block or less, mostly 2^-22, and a block costs the vector ALU
+// nothing for O (KEEP; above 128 dims the integer sums do not fit the
+// registers, and fp32 sums take a block's products: 160 of 380 instructions at
+// 128 dims).
 //
-// A wave owns 16 rows; of a workgroup's NW waves a.wr lie along the rows (ONE:
-// one does) and NW / a.wr along the cache blocks, and several workgroups share
+// A wave owns 16 rows; of a workgroup's NW waves WR lie along the rows (ONE:
+// one does) and NW / WR along the cache blocks, and several workgroups share
 // a group's blocks (group_of).  K of the next block is loaded when the scores
 // of this one are done, V when its product is: the loads need no registers of
 // their own and have half a block's work to arrive in.  q's digits are made
 // once a workgroup, through LDS.  The waves' sums meet in LDS in wave order, the
-// workgroups' through the workspace: the last one to arrive adds them in split
-// order, so the result does not depend on timing.  DT: 16-dim tiles of the
-// head dimension.
+// workgroups' through the workspace: the last one to arrive (up to 16 rows, ONE)
+// or a launch of its own (k_kv_join) adds them in split order, so the result does
+// not depend on timing.  DT: 16-dim tiles of the head dimension.
 //
 // Bound by the cache's bytes where a wave's rows are few: 131072 tokens, 8
-// heads, 128 dims in 53.5 us, of which 40 stream the cache at 6.7 TB/s and the
+// heads, 128 dims in 52.6 us, of which 40 stream the cache at 6.7 TB/s and the
 // rest is the start (ids, then blocks, then q: 3 us), the waves' unequal ends
-// (5), the joins (4) and the launch.  48 sequences of up to 12000: 123 us, 4.8
-// TB/s.
+// (5), the joins (4) and the launch.  48 sequences of up to 12000: 122 us, 4.8
+// TB/s.  With many rows by waiting for blocks that the waves along the rows and
+// the row blocks read again from L2 (a third of the waves' time; 2 x 64 new
+// tokens of 16000, 5 x 8 heads, 96 dims: 98 us, of them 54 vector ALU, 22 matrix
+// ALU).  Through LDS once a workgroup they cost more: waves in step do not
+// overlap one's products with another's exponentials (120 to 152 us).
 template <int DT, int NW, int WR>
 __global__ __launch_bounds__(64 * NW, attn_waves(DT)) void k_kv_attn(AttnArgs a) {
   constexpr bool KEEP = DT <= 8;
@@ -766,8 +774,8 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int wg_rows, int wk
   const int quads = a.kv.dim / 4, items = n_rows * quads, f0 = chunk * 256;
   if (f0 >= items) return;
   const int lr0 = f0 / quads, lr1 = min(n_rows, (f0 + 255) / quads + 1);
-  const int lane = threadIdx.x & 63;
-  for (int lr = lr0 + (int)(threadIdx.x >> 6); lr < lr1; lr += 4) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int lr = lr0 + wave; lr < lr1; lr += 4) {
     const float f = factor_of(a, g.slot, wg_rows, lr, active);
     if (lane < active) fac[(lr - lr0) * active + lane] = f;
   }

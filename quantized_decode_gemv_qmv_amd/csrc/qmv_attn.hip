@@ -183,6 +183,16 @@ __device__ __forceinline__ Lengths lengths_of(const AttnArgs& a, int wg_rows, in
 
 __device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
+// The device hands workgroup w to XCD w % 8.  This order gives each XCD, which
+// has an L2 of its own, neighbouring ones: the row blocks that read the same
+// cache blocks (us without / with: a prompt of 2048, 8 heads with 4 query heads,
+// 128 dims 173 / 145, 2 x 64 new tokens of 16000 98.7 / 96.7, 8 x 9 of 5001 with
+// 16 query heads 128.8 / 130.7).
+__device__ __forceinline__ int near_order(int w, int n) {
+  const int xcd = w & 7, at = w >> 3;
+  return xcd * (n >> 3) + min(xcd, n & 7) + at;
+}
+
 // What workgroup w does; false: nothing.  Without a.shares every group has
 // a.splits workgroups.
 __device__ __forceinline__ bool group_of(const AttnArgs& a, int w, int wg_rows, int wk, Group& g) {
@@ -309,7 +319,7 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 // (5), the joins (4) and the launch.  48 sequences of up to 12000: 122 us, 4.8
 // TB/s.  With many rows by waiting for blocks that the waves along the rows and
 // the row blocks read again from L2 (a third of the waves' time; 2 x 64 new
-// tokens of 16000, 5 x 8 heads, 96 dims: 98 us, of them 54 vector ALU, 22 matrix
+// tokens of 16000, 5 x 8 heads, 96 dims: 97 us, of them 52 vector ALU, 22 matrix
 // ALU).  Through LDS once a workgroup they cost more: waves in step do not
 // overlap one's products with another's exponentials (120 to 152 us).
 template <int DT, int NW, int WR>
@@ -332,7 +342,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT)) void k_kv_attn(AttnArgs a)
   constexpr int wr = WR, wk = NW / WR, wg_rows = 16 * WR;
   const int my_r = wave % wr, my_k = wave / wr;
   Group g;
-  if (!group_of(a, blockIdx.x, wg_rows, wk, g)) return;
+  if (!group_of(a, a.row_blocks > 1 ? near_order(blockIdx.x, gridDim.x) : blockIdx.x, wg_rows, wk, g)) return;
   int b_lo, b_hi, per, active;
   if (!blocks_of(a, g, wg_rows, wk, b_lo, b_hi, per, active)) return;
   if (g.split >= active) return;

@@ -492,7 +492,8 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  * A row that sees nothing gives zeros; a row of q that is not finite gives
  * NaN in that row.  Sums are fp32 or exact in integers, maxima and totals
  * fp32; the cached codes enter the products as they are, q rounded to 2^-24 of
- * its row's largest value, the softmax weights to 2^-19 of the largest that
+ * its row's largest value (a row whose largest is below 1e-30 counts as
+ * zero), the softmax weights to 2^-19 of the largest that
  * the row has in the same block (mostly to 2^-22; up to 128 dims a value scale
  * below 1e-30 counts in units of 1e-30).
  * q    : fp32 [n_tok][ldq] (device), 16-byte aligned, head h of a row at

@@ -13,7 +13,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // Largest whole number a 24-bit operand holds: 127 * 2^16, so that its three
 // base-256 digits all lie within -128..127.
-constexpr float kTop = 8323072.0f;
+constexpr float kTop = 127 * 65536;
 constexpr float kNegInf = -__builtin_inff();
 // Units of the weights (kUnit / kTop of what they were chosen by) serve every
 // block whose largest weight is up to kAbove bits above it or kBelow below.  They

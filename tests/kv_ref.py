@@ -68,12 +68,12 @@ def attend(codes, scales, table, lens, start, max_q, q, scale, window):
     belong to a sequence.
 
     With u = 2^-24: an element of q is off by at most 2 u of its row's largest
-    (rounded to half a unit of 1/8323072 of it, and the product before that),
+    (rounded to half a unit of 1/(127 2^16) of it, and the product before that),
     a score besides by 10 roundings of its own size (integer sums to fp32,
     their fma, the factors dq dk scale log2(e), the difference from the
     maximum) and the exponential by 2.  A weight is rounded to half a unit:
-    units are 2/8323072 of what p dv may be 2^1 above and, at the largest of
-    its block, 2^-4 below, so half of one is at most 2^4/8323072 < 2^-18.98
+    units are 2/(127 2^16) of what p dv may be 2^1 above and, at the largest of
+    its block, 2^-4 below, so half of one is at most 2^4/(127 2^16) < 2^-18.98
     < 33 u of the block's largest.  The sums over T blocks, and the joins of up
     to 68 partial sums, are off by 4 (T + 72) roundings."""
     n_blocks, _, heads, _ = codes.shape

@@ -396,3 +396,72 @@ def test_append_at_half_steps(uniform):
         k = np.nextafter(k, np.where(c.rng.random(d.shape) < 0.5, k, np.float32(0))).astype(np.float32)
         k[..., 0] = 127 * d[..., 0]
         run_append(qmv, c, k, np.ascontiguousarray(k[:, ::-1, ::-1]), e)
+
+
+def test_a_run_longer_than_the_integer_sums_hold():
+    """Equal weights over 9375 blocks of the largest codes: nothing but their
+    number makes a wave add its integer sums up."""
+    qmv = need_gpu()
+    say("attn long equal")
+    c = Case(50, [600000], [1], 1, 16)
+    c.codes[:, 1] = np.where(c.codes[:, 1] >= 0, 127, -127)
+    c.codes[:, 1, :, ::3] = 127
+    c.scales[:, 1] = c.scales[0, 1]
+    q = np.zeros((1, 2, 16), np.float32)
+    q[0, 1] = c.rng.standard_normal(16) * 1e-3
+    for ws in (False, True):
+        check_attn(qmv, c, 2, "long", ws=ws, q=q)
+
+
+def test_calls_on_two_streams():
+    """Calls of two shapes at once, each with its own workspace."""
+    qmv = need_gpu()
+    say("attn two streams")
+    jobs = []
+    for seed, lens, counts, group in ((51, [3000, 70, 900], [1, 1, 1], 8), (52, [4000], [12], 4)):
+        c = Case(seed, lens, counts, 4, 128)
+        codes, scales, table, seq, start = c.dev()
+        q = to_dev(c.rows(4 * group))
+        ws = torch.zeros(qmv.kv_attn_workspace_bytes(len(lens), c.n_tok, c.max_q, 4 * group, 4, 128, c.width),
+                         dtype=torch.uint8, device="cuda")
+        args = (q, codes, scales, table, seq)
+        kw = dict(tok_start=start, max_q=c.max_q, ws=ws)
+        jobs.append((args, kw, qmv.kv_attn(*args, **kw), torch.cuda.Stream(), torch.empty_like(q)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, kw, _, stream, out in jobs:
+            qmv.kv_attn(*args, out=out, stream=stream, **kw)
+    torch.cuda.synchronize()
+    for _, _, want, _, out in jobs:
+        assert torch.equal(out, want)
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured calls of two shapes with one workspace, replayed in turn."""
+    qmv = need_gpu()
+    say("attn two graphs")
+    jobs, need = [], 0
+    for seed, lens, group in ((53, [5000], 8), (54, [2000, 10, 600], 4)):
+        c = Case(seed, lens, [1] * len(lens), 2, 128)
+        need = max(need, qmv.kv_attn_workspace_bytes(len(lens), c.n_tok, 1, 2 * group, 2, 128, c.width))
+        jobs.append((c, to_dev(c.rows(2 * group))))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c, q in jobs:
+        codes, scales, table, seq, start = c.dev()
+        want = qmv.kv_attn(q, codes, scales, table, seq, tok_start=start, ws=ws)
+        out = torch.empty_like(q)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+            qmv.kv_attn(q, codes, scales, table, seq, tok_start=start, ws=ws, out=out)
+        graphs.append((graph, out, want, (codes, scales, table, seq, start)))
+    for _ in range(4):
+        for graph, out, _, _ in graphs:
+            out.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _ in graphs:
+            assert torch.equal(out, want)
+        assert not ws[:65536].any()

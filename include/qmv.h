@@ -490,7 +490,9 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  * with the keys and values of kv head h / (n_heads / n_kv_heads).  The row at
  * position p sees the positions j <= p, with window > 0 only j > p - window.
  * A row that sees nothing gives zeros; a row of q that is not finite gives
- * NaN in that row.  Sums are fp32 or exact in integers, maxima and totals
+ * NaN in that row.  Scores are fp32: they are rounded as such however large
+ * they are, and a row with one that (times log2 e) leaves fp32's range has no
+ * defined result; other rows keep theirs.  Sums are fp32 or exact in integers, maxima and totals
  * fp32; the cached codes enter the products as they are, q rounded to 2^-24 of
  * its row's largest value (a row whose largest is below 1e-30 counts as
  * zero), the softmax weights to 2^-19 of the largest that

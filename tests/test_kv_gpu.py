@@ -465,3 +465,89 @@ def test_two_graphs_share_a_workspace():
         for _, out, want, _ in graphs:
             assert torch.equal(out, want)
         assert not ws[:65536].any()
+
+
+def attend_far(c, q, scale):
+    """(out, tol) where scores lie so far apart that the largest take all: the
+    mean of the values of the keys that have it.  Weights of one are rounded
+    to 33 u of the block's largest, sums and joins as in kv_ref.attend."""
+    u = 2.0 ** -24
+    kk, vv = kv_ref.split(c.codes, c.dim)
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    for s, (t0, n) in enumerate(kv_ref.rows_of(c.start, len(c.lens), q.shape[0], c.max_q)):
+        length = int(c.lens[s])
+        ids = c.table[s, :-(-length // 64)]
+        kf = kk[ids] * c.scales[ids].astype(np.float64)[:, 0, :, None, None]
+        vf = vv[ids] * c.scales[ids].astype(np.float64)[:, 1, :, None, None]
+        for i in range(n):
+            for h in range(q.shape[1]):
+                g = h // (q.shape[1] // c.heads)
+                score = (kf[:, g].reshape(-1, c.dim) @ q[t0 + i, h].astype(np.float64)) * scale * np.log2(np.e)
+                score[length - n + i + 1:] = -np.inf
+                top = score.max()
+                won = score >= top - 1e-6 * abs(top)
+                rest = score[~won].max()
+                assert top - rest > 40 + 1e-5 * abs(top), (i, h, top, rest)  # weights below 2^-40 are nothing
+                v = vf[:, g].reshape(-1, c.dim)
+                blocks = np.unique(np.flatnonzero(won) // 64)
+                a = np.abs(v).reshape(-1, 64, c.dim)[blocks].sum((0, 1)) / won.sum()
+                out[t0 + i, h] = v[won].mean(0)
+                tol[t0 + i, h] = 33 * u * a + 4 * (len(ids) + 73) * u * np.abs(v[won]).mean(0)
+    return out, tol
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 1), (128, 3), (192, 1), (256, 3)])
+def test_the_largest_scores(dim, new, order):
+    """Scores up to 1e30 and down to -1e30 over many blocks a wave, where an
+    fp32 step of a score is more than what its weight's field has to spare,
+    later more than the whole field: one key, or a few alike, take all."""
+    qmv = need_gpu()
+    say(f"attn far scores {dim} {new} {order}")
+    c = Case(60, [2500, 1300], [new, 1], 1, dim)
+    kk, _ = kv_ref.split(c.codes, dim)
+    kk[...] = 0
+    kk[..., 0] = c.rng.integers(62, 126, kk.shape[:-1])
+    kk[..., 7, 0], kk[..., 11, 0] = 127, 127
+    kk[..., 5, 0], kk[..., 60, 0] = 60, 60
+    c.scales[:, 1] = 2.0 ** c.rng.uniform(-3, 3, c.scales[:, 1].shape)
+    for s in range(2):
+        n = -(-int(c.lens[s]) // 64)
+        at = {"rising": np.arange(n), "falling": np.arange(n)[::-1], "mixed": c.rng.permutation(n)}[order]
+        c.scales[c.table[s, :n], 0, 0] = 0.02 * (1 + 0.02 * at)
+    scale = dim ** -0.5
+    far = np.array([2e4, 7e4, 2e5, 3e6, 1e9, 1e20, 1e30])
+    q = np.zeros((c.n_tok, 14, dim), np.float32)
+    q[..., 0] = np.concatenate([far, -far]) / (127 * c.scales[:, 0][c.used].max() * scale * np.log2(np.e))
+    codes, scales, table, lens, start = c.dev()
+    ref, tol = attend_far(c, q, scale)
+    need = qmv.kv_attn_workspace_bytes(2, c.n_tok, new, 14, 1, dim, c.width)
+    for ws in (None, torch.zeros(need, dtype=torch.uint8, device="cuda")):
+        got = qmv.kv_attn(to_dev(q), codes, scales, table, lens, tok_start=start, max_q=new, ws=ws).cpu().numpy()
+        bad = np.argwhere(~(np.abs(got - ref) <= tol))
+        assert len(bad) == 0, (len(bad), bad[:3], got[tuple(bad[0])], ref[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 160])
+def test_large_scores_among_others(dim):
+    """Rows with scores of up to 1e5 beside ordinary ones in the same waves,
+    many blocks a wave; and a row whose scores leave fp32, which is not to
+    touch the others."""
+    qmv = need_gpu()
+    c = Case(61, [8000, 700], [2, 1], 1, dim)
+    q = c.rows(8)
+    q[0, 1] *= np.float32(1e4)
+    q[0, 2] *= np.float32(3e4)
+    q[0, 5] *= np.float32(100)
+    q[2, :4] *= np.float32(3e4)
+    for ws in (False, True):
+        good = check_attn(qmv, c, 8, dim, q=q, ws=ws)
+    q[1, 3] = np.float32(3e38)
+    codes, scales, table, lens, start = c.dev()
+    got = qmv.kv_attn(to_dev(q), codes, scales, table, lens, tok_start=start, max_q=2, scale=30.0).cpu().numpy()
+    q[1, 3] = 0.0
+    want = qmv.kv_attn(to_dev(q), codes, scales, table, lens, tok_start=start, max_q=2, scale=30.0).cpu().numpy()
+    keep = np.ones(good.shape[:2], bool)
+    keep[1, 3] = False
+    assert np.isfinite(want).all()
+    assert np.abs(got - want)[keep].max() <= 1e-4 * np.abs(want).max()

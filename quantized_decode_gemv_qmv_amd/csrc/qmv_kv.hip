@@ -170,8 +170,9 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
       }
     }
   }
-  if (!(old > 0.f && d > old)) return;
-  // the scale grew: the codes of slots [0, s0) in units of the new one
+  if (s0 == 0 || !(old >= 0.f && d > old)) return;
+  // the scale grew: the codes of slots [0, s0) in units of the new one; from a
+  // scale of zero they become zeros, whatever they were
   const float ratio = old / d;
   if (part == 0) {
     for (int f = threadIdx.x; f < s0 * qd; f += 256) {

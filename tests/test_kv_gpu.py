@@ -551,3 +551,24 @@ def test_large_scores_among_others(dim):
     keep[1, 3] = False
     assert np.isfinite(want).all()
     assert np.abs(got - want)[keep].max() <= 1e-4 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_append_behind_a_scale_of_zero(new):
+    """Codes under a scale of zero stand for zeros, whatever they are: they
+    are zeros when the scale grows."""
+    qmv = need_gpu()
+    say(f"append behind zero scales {new}")
+    c = Case(62, [50 + new, 9 + new], [new, new], 2, 80)
+    c.scales[c.table[:, 0], 0, 1] = 0.0
+    c.scales[c.table[:, 0], 1, 0] = 0.0
+    k, v = c.rows(2), c.rows(2)
+    before = c.codes.copy()
+    codes, scales, table, lens, start = c.dev()
+    qmv.kv_append(to_dev(k), to_dev(v), codes, scales, table, lens, tok_start=start, max_q=new)
+    kv_ref.append(c.codes, c.scales, c.table, c.lens, c.start, c.max_q, k, v)
+    for part, h in ((0, 1), (1, 0)):
+        for s, old in enumerate((50, 9)):
+            assert kv_ref.split(before, 80)[part][c.table[s, 0], h, :old].any()
+            kv_ref.split(c.codes, 80)[part][c.table[s, 0], h, :old] = 0
+    same_cache(c, codes, scales, new)

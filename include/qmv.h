@@ -520,7 +520,9 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  *        with the same arguments, and differs from the one without in
  *        rounding only.
  * n_heads a positive multiple of n_kv_heads of at most QMV_MAX_HEADS, window
- * >= 0, scale finite.  Asynchronous on `stream`; allocates nothing.
+ * >= 0, scale finite.  A call is one launch over all that max_q allows: below
+ * 2^23 tiles, n_seqs * n_kv_heads * ceil(max_q * n_heads / n_kv_heads / 16),
+ * it always fits, from there on it may be QMV_ERR_UNSUPPORTED.  Asynchronous on `stream`; allocates nothing.
  * qmv_kv_attn_workspace_bytes is host only; 0: the arguments are invalid, or
  * no workspace is used.
  */

@@ -816,7 +816,7 @@ QMV_API qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, in
     return QMV_ERR_MISALIGNED;
   const AttnPlan p = attn_plan(kv->n_seqs, kv->max_q, n_heads, kv->n_kv_heads, kv->head_dim, kv->table_width,
                                device_cus());
-  if (p.groups >= int64_t(1) << 24) return QMV_ERR_UNSUPPORTED;  // workgroups of one launch
+  if (p.groups * (64 * p.nw) > UINT32_MAX) return QMV_ERR_UNSUPPORTED;  // threads of one launch
   const bool use_ws = ws != nullptr && p.ws_bytes > 0;
   if (use_ws) {
     if (ws_bytes < static_cast<size_t>(p.ws_bytes)) return QMV_ERR_WORKSPACE;

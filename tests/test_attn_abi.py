@@ -117,3 +117,9 @@ def test_binding_refuses_host_tensors_and_shapes():
         q.kv_attn(torch.zeros(1, 2, 64), codes, scales, table, lens)
     with pytest.raises(ValueError):
         q.kv_attn(torch.zeros(1, 64), codes, scales, table, lens)
+
+
+def test_more_threads_than_a_launch_has():
+    """Groups of eight waves: 2^23 of them are 2^32 threads."""
+    big = dict(n_seqs=65535, n_tok=65535, max_q=1, n_heads=10240, ldq=10240 * 64, ldo=10240 * 64)
+    assert attn(n_kv_heads=160, **big) == UNSUPPORTED

@@ -178,7 +178,7 @@ def act_fields(xq: torch.Tensor, n_tok: int, k: int):
     activation buffer."""
     od, os_ = act_offsets(n_tok, k)
     nb = k // 32
-    if xq.numel() < act_bytes(n_tok, k):
+    if xq.numel() < os_ + 4 * n_tok * nb:  # the fields' end; what pads the buffer behind it may be missing
         raise ValueError("activation buffer too small")
     if xq.numel() % 4 == 0 and xq.storage_offset() % 4 == 0 and xq.dim() == 1 and xq.stride(0) == 1:
         # two tensor operations a field

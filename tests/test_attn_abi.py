@@ -123,3 +123,17 @@ def test_more_threads_than_a_launch_has():
     """Groups of eight waves: 2^23 of them are 2^32 threads."""
     big = dict(n_seqs=65535, n_tok=65535, max_q=1, n_heads=10240, ldq=10240 * 64, ldo=10240 * 64)
     assert attn(n_kv_heads=160, **big) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("n_tok,k", [(1, 32), (3, 96), (2, 4096)])
+def test_act_fields_of_a_buffer_without_padding(n_tok, k):
+    """The fields end before act_bytes; a buffer that ends with them holds
+    them all, one byte less does not."""
+    _, at = q.act_offsets(n_tok, k)
+    end = at + 4 * n_tok * (k // 32)
+    buf = torch.arange(q.act_bytes(n_tok, k)).to(torch.uint8)
+    want = q.act_fields(buf, n_tok, k)
+    for part in (buf[:end].clone(), buf[:end]):
+        assert all(torch.equal(a.view(torch.int8), b.view(torch.int8)) for a, b in zip(q.act_fields(part, n_tok, k), want))
+    with pytest.raises((ValueError, RuntimeError)):
+        q.act_fields(buf[:end - 1], n_tok, k)

@@ -450,7 +450,9 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
 
 
 def _rows(t: torch.Tensor, shape, name: str) -> int:
-    """Checks an fp32 row array and gives its row stride."""
+    """Checks an fp32 row array and gives its row stride.  A single row may come without its dimension."""
+    if t.dim() == 1 and len(shape) == 2 and shape[0] == 1:
+        t = t.view(1, -1)
     st = t.stride()
     if t.dtype != torch.float32 or t.shape != shape or st[-1] != 1 \
             or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
@@ -471,7 +473,10 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     """x fp32 [T][K] (+ residual) -> (r, xq): r = x + residual (in sum_out,
     allocated when None; x itself without a residual and a sum_out) and the
     Q8 activation buffer of rmsnorm(r) * weight.  y_out fp32 [T][K], if given,
-    receives the normed rows.  sum_out may be x or residual."""
+    receives the normed rows.  sum_out may be x or residual, and so may y_out
+    if sum_out is not the same one (without a residual and a sum_out, a y_out
+    that is x leaves the normed rows in what is returned as r).  A single row
+    may be given as [K], the outputs and the residual too."""
     if x.dim() == 1:
         x = x.view(1, -1)
     if x.dim() != 2:
@@ -486,8 +491,6 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
     rp = sp = yp = None
     ldr = lds = ldy = 0
     if residual is not None:
-        if residual.dim() == 1:
-            residual = residual.view(1, -1)
         ldr, rp = _rows(residual, shape, "residual"), residual.data_ptr()
         if sum_out is None:
             sum_out = _new(x, shape, torch.float32, stream)

@@ -109,3 +109,19 @@ def test_rows_do_not_depend_on_each_other_or_the_split():
             _, one = qmv.rmsnorm_quantize(x[row], w, EPS)
             for a, b in zip(qmv.act_fields(many, t, k), qmv.act_fields(one, 1, k)):
                 assert torch.equal(a[row], b[0]), (k, row)
+
+
+def test_a_row_without_its_dimension():
+    """A 1-D x takes 1-D residuals and outputs, and may be its own output."""
+    qmv = need_gpu()
+    say("norm 1-D")
+    k = 96
+    x, res, w = (to_dev(x_host(1, k, f"norm/1d{i}")[0]) for i in range(3))
+    r0, q0 = qmv.rmsnorm_quantize(x.view(1, k), w, EPS, residual=res.view(1, k), y_out=(y0 := torch.empty(1, k, device="cuda")))
+    s, y = torch.empty(k, device="cuda"), torch.empty(k, device="cuda")
+    r, q = qmv.rmsnorm_quantize(x, w, EPS, residual=res, sum_out=s, y_out=y)
+    assert torch.equal(s, r0[0]) and torch.equal(y, y0[0]) and r.data_ptr() == s.data_ptr()
+    assert all(torch.equal(a, b) for a, b in zip(qmv.act_fields(q, 1, k), qmv.act_fields(q0, 1, k)))
+    c = x.clone()
+    qmv.rmsnorm_quantize(c, w, EPS, residual=res, sum_out=c)
+    assert torch.equal(c, r0[0])

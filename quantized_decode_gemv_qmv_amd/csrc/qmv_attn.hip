@@ -737,7 +737,7 @@ __global__ __launch_bounds__(64 * NW, attn_waves(DT)) void k_kv_attn(AttnArgs a)
   // with few outputs, several threads share one along the splits
   const int sub = items >= T ? 1 : T / items;
   const int share = (active + sub - 1) / sub;
-  float* meet = lds + n_rows * active;
+  float* meet = lds + ((n_rows * active + 3) & ~3);  // 16-byte accesses
   for (int f0 = 0; f0 < items; f0 += T) {
     const int f = sub == 1 ? f0 + (int)threadIdx.x : (int)threadIdx.x % items;
     const int part = sub == 1 ? 0 : (int)threadIdx.x / items;

@@ -572,3 +572,18 @@ def test_append_behind_a_scale_of_zero(new):
             assert kv_ref.split(before, 80)[part][c.table[s, 0], h, :old].any()
             kv_ref.split(c.codes, 80)[part][c.table[s, 0], h, :old] = 0
     same_cache(c, codes, scales, new)
+
+
+@pytest.mark.parametrize("lens,counts,group", [
+    ([1300], [1], 6),  # 21 blocks: 3 parts of 8 for eight waves, 6 of 4 for four
+    ([2500], [1], 1),  # 40 blocks: 5 or 10 parts
+    ([700], [1], 3),   # 11 blocks: 2 or 3 parts
+    ([2000, 190], [1, 1], 3), ([1800, 130, 1349], [3, 1, 2], 5)])
+def test_joins_of_odd_rows_and_parts(lens, counts, group):
+    """Rows times parts of no multiple of four: what is summed lies behind
+    that many factors."""
+    qmv = need_gpu()
+    for dim in (16, 48, 128, 256):
+        say(f"attn join {lens} {dim}")
+        c = Case(63, lens, counts, 1, dim)
+        check_attn(qmv, c, group, (lens, dim))

@@ -587,3 +587,46 @@ def test_joins_of_odd_rows_and_parts(lens, counts, group):
         say(f"attn join {lens} {dim}")
         c = Case(63, lens, counts, 1, dim)
         check_attn(qmv, c, group, (lens, dim))
+
+
+def test_a_run_whose_integer_sums_would_wrap():
+    """Equal weights over 18000 blocks, 2250 a wave without a workspace.  A
+    weight is then kTop / kUnit = 64 * 2^16 - 128 * 2^8 + 0, so a block of codes
+    127 adds 64 * 128 * 127 to the sum of the middle digit: 2064 blocks are
+    more than 2^31 if nothing adds the sums up before."""
+    qmv = need_gpu()
+    say("attn wrap")
+    blocks = 18000
+    assert (blocks // 8) * 64 * 128 * 127 > 2**31
+    c = Case(64, [64 * 5], [1], 1, 16)
+    ids = c.table[0].copy()
+    _, vv = kv_ref.split(c.codes, 16)
+    vv[..., ::3], vv[..., 1::3] = 127, -127
+    c.scales[:, 1] = c.scales[ids[0], 1]
+    c.table = np.tile(ids, blocks // 5).reshape(1, blocks)
+    c.lens[:], c.width = 64 * blocks, blocks
+    q = np.zeros((1, 2, 16), np.float32)
+    q[0, 1] = c.rng.standard_normal(16) * 1e-3
+    for ws in (False, True):
+        check_attn(qmv, c, 2, "wrap", ws=ws, q=q)
+
+
+@pytest.mark.parametrize("lens,counts", [([700, 64], [1, 1]), ([4000], [5])])
+def test_q8_output_alone(lens, counts):
+    """The C call without an fp32 output writes the same Q8 blocks."""
+    import ctypes
+    qmv = need_gpu()
+    say(f"attn q8 alone {lens}")
+    c = Case(65, lens, counts, 2, 64)
+    codes, scales, table, seq, start = c.dev()
+    heads, k = 8, 8 * 64
+    q = to_dev(c.rows(heads))
+    need = qmv.kv_attn_workspace_bytes(len(lens), c.n_tok, c.max_q, heads, 2, 64, c.width)
+    ws = torch.zeros(max(need, 1), dtype=torch.uint8, device="cuda")
+    want, got = (torch.full((qmv.act_bytes(c.n_tok, k),), 9, dtype=torch.uint8, device="cuda") for _ in range(2))
+    qmv.kv_attn(q, codes, scales, table, seq, tok_start=start, max_q=c.max_q, xq=want, ws=ws)
+    kv = qmv._kv(codes, scales, table, seq, start, c.n_tok, c.max_q, 64)
+    st = qmv.lib().qmv_kv_attn(ctypes.byref(kv), q.data_ptr(), k, heads, 64 ** -0.5, 0, None, 0, got.data_ptr(),
+                               ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert torch.equal(got, want)

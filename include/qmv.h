@@ -380,8 +380,8 @@ qmv_status qmv_moe_matvec_noalloc(qmv_type type, const void* w, int64_t n_expert
  *   r = x + residual                          (fp32; r = x without one),
  *   inv = fp32(1 / sqrt(sum r^2 / k + eps))   (the sum and root in fp64),
  *   y = (r * inv) * weight                    (each product rounded to fp32),
- * then the Q8 blocks of y exactly as qmv_quantize_act makes them.  The codes
- * do not depend on how the row is split over threads.
+ * then the Q8 blocks of y exactly as qmv_quantize_act makes them.  A row's
+ * result depends on its own values and k alone, not on the other rows.
  * x        : fp32 [n_tok][ldx] (device), finite values.
  * residual : NULL, or fp32 [n_tok][ldr] (device).
  * weight   : fp32 [k] (device).
@@ -495,9 +495,12 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  * defined result; other rows keep theirs.  Sums are fp32 or exact in integers, maxima and totals
  * fp32; the cached codes enter the products as they are, q rounded to 2^-24 of
  * its row's largest value (a row whose largest is below 1e-30 counts as
- * zero), the softmax weights to 2^-19 of the largest that
- * the row has in the same block (mostly to 2^-22; up to 128 dims a value scale
- * below 1e-30 counts in units of 1e-30).
+ * zero), the softmax weights to 16 / (127 * 2^16), just above 2^-19, of the
+ * largest that the row has in the same block (mostly to 2^-22; up to 128 dims a
+ * value scale below 1e-30 counts in units of 1e-30).  So where a few values of a
+ * row of q are A times the others, and the keys are small just there, the
+ * scores are A times less exact than fp32 ones (128 dims, 512 tokens, A 30:
+ * outputs 2e-6 off, of the row's largest; A 300: 2e-5).
  * q    : fp32 [n_tok][ldq] (device), 16-byte aligned, head h of a row at
  *        columns h * head_dim ..; ldq a multiple of 4, at least
  *        n_heads * head_dim.
@@ -512,7 +515,8 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  *        qmv_kv_attn_workspace_bytes(...) bytes, zero-filled once when
  *        allocated and left so in its counters by every completed call; it
  *        lets workgroups share a sequence's blocks, which calls with few
- *        sequences and heads need for speed.  NULL runs without.  One
+ *        sequences and heads need for speed.  NULL runs without, a long
+ *        sequence then on one workgroup for each kv head.  One
  *        workspace may serve calls of different shapes that do not overlap
  *        in time.  Calls of more than 16 rows (new tokens x query heads of a
  *        kv head) that use it take two launches.
@@ -522,7 +526,11 @@ qmv_status qmv_kv_append(const qmv_kv* kv, const float* k, int64_t ldk, const fl
  * n_heads a positive multiple of n_kv_heads of at most QMV_MAX_HEADS, window
  * >= 0, scale finite.  A call is one launch over all that max_q allows: below
  * 2^23 tiles, n_seqs * n_kv_heads * ceil(max_q * n_heads / n_kv_heads / 16),
- * it always fits, from there on it may be QMV_ERR_UNSUPPORTED.  Asynchronous on `stream`; allocates nothing.
+ * it always fits, from there on it may be QMV_ERR_UNSUPPORTED.  It is also
+ * planned for max_q rows of every sequence: prompts and single tokens are
+ * better two calls than one (31 sequences of up to 8000 tokens with one new
+ * token and a prompt's 512, 8 kv heads with 4 query heads, 128 dims: 642 us
+ * as one call, 57 and 56 us as two).  Asynchronous on `stream`; allocates nothing.
  * qmv_kv_attn_workspace_bytes is host only; 0: the arguments are invalid, or
  * no workspace is used.
  */

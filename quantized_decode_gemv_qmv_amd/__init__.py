@@ -563,7 +563,11 @@ def kv_attn(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_ta
     that is not 0; scale None: 1 / sqrt(head_dim).  Returns out fp32
     [T][n_heads][head_dim] (allocated when None); xq, if given, receives the
     Q8 blocks of its rows.  ``ws`` (uint8, zero-filled once, of
-    kv_attn_workspace_bytes bytes) lets workgroups share a sequence."""
+    kv_attn_workspace_bytes bytes) lets workgroups share a sequence; without
+    it each kv head of a sequence has one workgroup for every tile of rows,
+    which is slow for few sequences (131072 tokens: 8 of 256 compute units).
+    Prompts and single tokens are better two calls than one (the call is
+    planned for max_q new tokens of every sequence)."""
     shape = q.shape
     if len(shape) != 3:
         raise ValueError("q must be [T][n_heads][head_dim]")

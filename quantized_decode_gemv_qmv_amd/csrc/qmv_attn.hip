@@ -312,8 +312,8 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Group& g, int ro
 // block, as long as every row's largest weight in the block lies within
 // 2^-kBelow .. 2^kAbove of what the units were chosen by; else they are added
 // to the fp32 sums in LDS (280 instructions at 96 dims, against 250 of a block)
-// and the units chosen anew.  A weight is so rounded to half a unit, 2^-19 of the
-// largest of its block or less, mostly 2^-22, and a block costs the vector ALU
+// and the units chosen anew.  A weight is so rounded to half a unit, at most
+// 16 / kTop (just above 2^-19) of the largest of its block, mostly 2^-22, and a block costs the vector ALU
 // nothing for O (KEEP; above 128 dims the integer sums do not fit the
 // registers, and fp32 sums take a block's products: 160 of 380 instructions at
 // 128 dims).

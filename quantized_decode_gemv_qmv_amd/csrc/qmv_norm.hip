@@ -35,11 +35,15 @@ __device__ __forceinline__ double row_sum(double v) {
 // Q8 blocks of y as k_quantize makes them.  TPR threads hold one row in
 // registers, NV 16-byte vectors each, so that x, res and w are read once and r
 // and the blocks written once: 13.25 bytes a value, which bounds the kernel
-// (8192 x 14336: 275 us, 5.66 TB/s; one row of 4096: 3.2 us, all latency).
+// (8192 x 14336: 275 us, 5.66 TB/s; one row of 4096: 3.2 us, all latency).  Rows
+// that stay in the caches are bound by the vector ALU: 1000 x 4128 takes 10.2 us,
+// 7.1 of them vector instructions (some 200 a vector of four values: q8_block8
+// divides and rounds each).
 // Eight neighbouring lanes hold a block of 32 (q8_block8).  The squares are
-// summed in fp64 (they are exact there, and the card's fp64 rate leaves the
-// sum hidden behind the loads): inv then does not depend on the order of the
-// sum, so a code does not either, however the row is split over threads.
+// summed in fp64, where each is exact (the card's fp64 rate leaves the sum
+// hidden behind the loads).  The sum's order could change it by some 2^-53 of
+// itself a step, and so inv next to a border between two fp32 numbers; it
+// depends on k alone, so a row gives the same bits wherever it stands.
 // inv and both products are rounded to fp32.
 template <int TPR, int NV, bool RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm(NormArgs a) {
@@ -141,8 +145,8 @@ hipError_t launch(const NormArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Threads of a row by its length: the fewest that hold it in two 16-byte
-// vectors each, up to a whole workgroup.  Us at 1 / 64 / 2048 rows with a
+// Threads of a row by its length: one wave up to two 16-byte vectors each, 256
+// and 512 threads up to two each, beyond that 1024.  Us at 1 / 64 / 2048 rows with a
 // residual (256, 512, 1024 threads): 1024 values 2.1 / 2.4 / 7.8, 2.1 / 2.4 /
 // 7.6, 2.2 / 2.4 / 9.0; 4096 values 4.0 / 4.4 / 25.9, 3.2 / 3.5 / 22.4, 3.3 /
 // 3.7 / 23.5; 8192 values 11.8 / 12.7 / 89.7, 5.0 / 5.5 / 44.4, 4.6 / 5.1 /

@@ -33,9 +33,9 @@ def check(qmv, x, w, res=None, eps=EPS, what="", **kw):
     return y_h
 
 
-# rows and widths of every way a row is split over threads: one wave a row
-# from 1024 rows on up to 4096 values, 256 threads, 1024 threads; widths with a
-# ragged last vector and the largest
+# widths of every way a row is split over threads (one wave, 256, 512 and 1024
+# threads, by width alone), with a ragged last vector and the largest; row
+# counts from one to more than the device holds at once
 @pytest.mark.parametrize("t,k", [(1, 32), (3, 96), (1, 4096), (5, 4128), (16, 5120), (2, 14336), (3, 16416), (2, 65536),
                                  (1, 49184), (1025, 32), (1030, 992), (1024, 4096), (513, 4128), (515, 16384),
                                  (2050, 2080)])

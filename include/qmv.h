@@ -540,6 +540,63 @@ qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, int64_t n_
                        float* out, int64_t ldo, void* xq, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * The steps around a layer's matvecs: adapters beside a projection, norm and
+ * rotation of its heads, the experts' gate, and what a verify step reads off
+ * the output head.
+ *
+ * qmv_head_norm_rope -- root-mean-square norm of each query and key head and
+ * its rotation by the token's positions, one launch, in place or not: the step
+ * between the q/k/v projections and qmv_kv_append.  (Castagna Veloce page,
+ * "Fused operations": position-embedding fusions.)  For row t and head h of q
+ * (and of k, with its own weight):
+ *   r = (x * inv) * weight, inv = 1 / sqrt(sum x^2 / head_dim + eps) (the sum
+ *       in fp64; r = x where the weight is NULL),
+ *   pair i of rot_dim / 2, its dims (a, b) = (i, i + rot_dim / 2), or
+ *       (2i, 2i + 1) if interleaved, turns by
+ *       w = pos[pair_axis[i]][t] * inv_freq[i]   (the product and its place in
+ *                                     the circle in 64 bits and more):
+ *       y_a = scale * (r_a cos w - r_b sin w),
+ *       y_b = scale * (r_b cos w + r_a sin w),
+ *   the other dims, and pairs whose axis is outside [0, n_axes), keep r.
+ * rope     : HOST struct, read during the call only; its pointers are device
+ *            pointers.
+ *   pos       int32 [n_axes][n_tok]; a row whose position on the first axis is
+ *             negative belongs to no sequence: it is neither read nor written.
+ *             NULL only if rot_dim is 0.
+ *   inv_freq  fp32 [rot_dim / 2], finite.  NULL only if rot_dim is 0.
+ *   pair_axis NULL (the first axis), or int32 [rot_dim / 2].
+ *   n_axes    1 .. QMV_MAX_ROPE_AXES (text: one; images and video: time,
+ *             height, width).
+ *   rot_dim   even, 0 (norm alone) .. head_dim.
+ *   interleaved 0 or 1;  scale finite.
+ * q, k     : fp32 [n_tok][ldq], [n_tok][ldk] (device), head h of a row at
+ *            columns h * head_dim ..; k NULL with n_kv_heads 0: q alone.
+ * q_weight, k_weight : NULL, or fp32 [head_dim] (device).
+ * q_out, k_out : fp32 [n_tok][ldqo], [n_tok][ldko]; q and k themselves (same
+ *            pointer and stride), or memory that overlaps no other argument.
+ * Every fp32 pointer except inv_freq 16-byte aligned and every stride a
+ * multiple of 4 (else QMV_ERR_MISALIGNED), strides at least heads * head_dim;
+ * head_dim a positive multiple of 4, eps positive and finite (else
+ * QMV_ERR_INVALID_ARG); n_tok <= QMV_MAX_ACT_ROWS, n_heads <= QMV_MAX_HEADS,
+ * n_kv_heads <= QMV_MAX_KV_HEADS, head_dim <= QMV_MAX_HEAD_DIM (else
+ * QMV_ERR_UNSUPPORTED).  Asynchronous on `stream`; allocates nothing.
+ */
+#define QMV_MAX_ROPE_AXES 4
+typedef struct {
+  const int32_t* pos;
+  const float* inv_freq;
+  const int32_t* pair_axis;
+  int64_t n_axes;
+  int64_t rot_dim;
+  int64_t interleaved;
+  float scale;
+} qmv_rope;
+qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq, int64_t n_heads,
+                              const float* q_weight, const float* k, int64_t ldk, int64_t n_kv_heads,
+                              const float* k_weight, int64_t n_tok, int64_t head_dim, float eps, float* q_out,
+                              int64_t ldqo, float* k_out, int64_t ldko, void* stream);
+
+/*
  * qmv_block_dots -- test hook: the exact integer partial of every 32-weight
  * block, computed by the same device decode and dot routines as qmv_matvec.
  * out : int32 [n_tok][n_rows][k/32][c] (device), c = 2 for q4_K and q5_K

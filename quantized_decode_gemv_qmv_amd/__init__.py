@@ -27,6 +27,7 @@ __all__ = [
     "block_dots",
     "block_dots_mx", "moe_block_dots", "stream_read",
     "rmsnorm_quantize", "kv_append", "kv_attn", "kv_attn_workspace_bytes", "KV_BLOCK",
+    "head_norm_rope",
     "set_tuning", "swiglu_quantize", "router_topk", "variant_name", "variants", "pick_variant", "matvec_plan", "MAX_TOKENS", "MAX_MOE_TOKENS",
 ]
 
@@ -47,6 +48,13 @@ class _Item(ctypes.Structure):
     """qmv_matvec_item of include/qmv.h."""
     _fields_ = [("w", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("y", ctypes.c_void_p),
                 ("ldy", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    """qmv_rope of include/qmv.h."""
+    _fields_ = [("pos", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("n_axes", ctypes.c_int64), ("rot_dim", ctypes.c_int64), ("interleaved", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
 
 
 class _Kv(ctypes.Structure):
@@ -110,6 +118,8 @@ def lib():
         "qmv_kv_append": ([ctypes.POINTER(_Kv), P, I64, P, I64, P], I),
         "qmv_kv_attn_workspace_bytes": ([I64, I64, I64, I64, I64, I64, I64], SZ),
         "qmv_kv_attn": ([ctypes.POINTER(_Kv), P, I64, I64, ctypes.c_float, I64, P, I64, P, P, SZ, P], I),
+        "qmv_head_norm_rope": ([ctypes.POINTER(_Rope), P, I64, I64, P, P, I64, I64, P, I64, I64, ctypes.c_float, P,
+                                I64, P, I64, P], I),
         "qmv_block_dots": ([I, P, I64, I64, P, I64, P, P], I),
         "qmv_block_dots_mx": ([I, P, I64, I64, P, I64, I64, I, P, P], I),
         "qmv_moe_block_dots": ([I, P, I64, I64, I64, P, I, P, I64, I64, I64, P, P, SZ, P], I),
@@ -589,6 +599,62 @@ def kv_attn(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_ta
     _check(lib().qmv_kv_attn(ctypes.byref(kv), q.data_ptr(), ldq, n_heads, dim ** -0.5 if scale is None else scale,
                              window, out.data_ptr(), ldo, qp, wp, ws_bytes, _stream(stream)), "qmv_kv_attn")
     return out
+
+
+# ------------------------------------- steps around a layer's matvecs
+def head_norm_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor | None, inv_freq: torch.Tensor | None,
+                   q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                   pair_axis: torch.Tensor | None = None, interleaved: bool = False, scale: float = 1.0,
+                   q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norm (where a weight fp32 [head_dim] is given) and rotation of the heads
+    of q fp32 [T][n_heads][head_dim] and k fp32 [T][n_kv_heads][head_dim] or
+    None (rows may be strided).  pos int32 [T] or [axes][T]: pair i of the first
+    2 * len(inv_freq) dims turns by pos[pair_axis[i]] * inv_freq[i] (pair_axis
+    int32, None: the first axis), its dims i and i + len(inv_freq), or 2i and
+    2i + 1 if interleaved; rows with a negative first position are left as they
+    are.  inv_freq fp32, None: no rotation (pos may be None then).  Returns
+    (q_out, k_out): q and k themselves, changed in place, where None."""
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [T][n_heads][head_dim]")
+    _here(q, k, pos, inv_freq, q_weight, k_weight, pair_axis, q_out, k_out)
+    n_tok, heads, dim = shape
+    ldq = _rows(q, shape, "q")
+    if q_out is None:
+        q_out = q
+    kp = kop = None
+    kv = ldk = ldko = 0
+    if k is not None:
+        ks = k.shape
+        if len(ks) != 3 or ks[0] != n_tok or ks[2] != dim:
+            raise ValueError("k must be [T][n_kv_heads][head_dim] with the T and head_dim of q")
+        if k_out is None:
+            k_out = k
+        kv, ldk, ldko, kp, kop = ks[1], _rows(k, ks, "k"), _rows(k_out, ks, "k_out"), k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    rope = _Rope(None, None, None, 1, 0, bool(interleaved), scale)
+    if pos is not None:
+        ps = pos.shape
+        if ps[-1] != n_tok or len(ps) > 2:
+            raise ValueError("pos must be [T] or [axes][T]")
+        rope.pos, rope.n_axes = _whole(pos, torch.int32, "pos"), 1 if len(ps) == 1 else ps[0]
+    if inv_freq is not None:
+        n = inv_freq.numel()
+        rope.inv_freq, rope.rot_dim = _whole(inv_freq, torch.float32, "inv_freq"), 2 * n
+        if pair_axis is not None:
+            rope.pair_axis = _whole(pair_axis, torch.int32, "pair_axis")
+            if pair_axis.numel() != n:
+                raise ValueError("pair_axis must hold one axis a pair")
+    weights = []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w.numel() != dim:
+            raise ValueError(f"{name} must hold one value a dim")
+        weights.append(None if w is None else _whole(w, torch.float32, name))
+    _check(lib().qmv_head_norm_rope(ctypes.byref(rope), q.data_ptr(), ldq, heads, weights[0], kp, ldk, kv, weights[1],
+                                    n_tok, dim, eps, q_out.data_ptr(), _rows(q_out, shape, "q_out"), kop, ldko,
+                                    _stream(stream)), "qmv_head_norm_rope")
+    return q_out, k_out
 
 
 def block_dots(fmt: int, w: torch.Tensor, n_rows: int, k: int, xq: torch.Tensor, n_tok: int,

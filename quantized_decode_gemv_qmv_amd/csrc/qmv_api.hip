@@ -9,6 +9,7 @@
 #include "qmv_attn.h"
 #include "qmv_internal.h"
 #include "qmv_mfma.h"
+#include "qmv_steps.h"
 #include "qmv.h"
 
 #define QMV_API extern "C" __attribute__((visibility("default")))
@@ -1051,6 +1052,56 @@ QMV_API qmv_status qmv_matvec_batch(qmv_type type, const qmv_matvec_item* items,
   a.lds_per_cu = dv.lds_per_cu;
   hipError_t e = launch_matvec(a, static_cast<hipStream_t>(stream));
   return hip_status(e);
+}
+
+// ------------------------------------- steps around a layer's matvecs
+QMV_API qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq, int64_t n_heads,
+                                      const float* q_weight, const float* k, int64_t ldk, int64_t n_kv_heads,
+                                      const float* k_weight, int64_t n_tok, int64_t head_dim, float eps, float* q_out,
+                                      int64_t ldqo, float* k_out, int64_t ldko, void* stream) {
+  if (rope == nullptr || q == nullptr || q_out == nullptr || n_tok < 1 || n_heads < 1 || n_kv_heads < 0 ||
+      head_dim < 1 || head_dim % 4 || (k == nullptr) != (n_kv_heads == 0) || (k_out == nullptr) != (k == nullptr) ||
+      (k == nullptr && k_weight != nullptr) || !(eps > 0.f) || !(eps < __builtin_inff()))
+    return QMV_ERR_INVALID_ARG;
+  const int64_t rot = rope->rot_dim;
+  if (rot < 0 || rot % 2 || rot > head_dim || rope->n_axes < 1 || (rope->interleaved != 0 && rope->interleaved != 1) ||
+      !(rope->scale - rope->scale == 0.f) || (rot > 0 && (rope->pos == nullptr || rope->inv_freq == nullptr)))
+    return QMV_ERR_INVALID_ARG;
+  if (n_tok > QMV_MAX_ACT_ROWS || n_heads > QMV_MAX_HEADS || n_kv_heads > QMV_MAX_KV_HEADS ||
+      head_dim > QMV_MAX_HEAD_DIM || rope->n_axes > QMV_MAX_ROPE_AXES)
+    return QMV_ERR_UNSUPPORTED;
+  const int64_t nq = n_heads * head_dim, nk = n_kv_heads * head_dim;
+  if (ldq < nq || ldqo < nq || (k != nullptr && (ldk < nk || ldko < nk))) return QMV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || ldq % 4 || !aligned(q_out, 16) || ldqo % 4 ||
+      (k != nullptr && (!aligned(k, 16) || ldk % 4 || !aligned(k_out, 16) || ldko % 4)) ||
+      (q_weight != nullptr && !aligned(q_weight, 16)) || (k_weight != nullptr && !aligned(k_weight, 16)) ||
+      !aligned(rope->pos, 4) || !aligned(rope->inv_freq, 4) || !aligned(rope->pair_axis, 4))
+    return QMV_ERR_MISALIGNED;
+  HeadsArgs a{};
+  a.x[0] = q;
+  a.x[1] = k;
+  a.ldx[0] = ldq;
+  a.ldx[1] = ldk;
+  a.y[0] = q_out;
+  a.y[1] = k_out;
+  a.ldy[0] = ldqo;
+  a.ldy[1] = ldko;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.heads[0] = static_cast<int>(n_heads);
+  a.heads[1] = static_cast<int>(n_kv_heads);
+  a.pos = rope->pos;
+  a.freq = rope->inv_freq;
+  a.axis = rope->pair_axis;
+  a.n_tok = static_cast<int>(n_tok);
+  a.dim = static_cast<int>(head_dim);
+  a.rot = static_cast<int>(rot);
+  a.n_axes = static_cast<int>(rope->n_axes);
+  a.adjacent = static_cast<int>(rope->interleaved);
+  a.scale = rope->scale;
+  a.eps = eps;
+  a.inv_dim = 1.0 / static_cast<double>(head_dim);
+  return hip_status(launch_head_norm_rope(a, device_cus(), static_cast<hipStream_t>(stream)));
 }
 
 QMV_API qmv_status qmv_block_dots(qmv_type type, const void* w, int64_t n_rows, int64_t k,

@@ -1,0 +1,212 @@
+// qmv_rope.hip -- root-mean-square norm of each query and key head and its
+// rotation by the token's positions, one pass, for gfx950.
+#include "qmv_device.h"
+#include "qmv_steps.h"
+
+namespace qmv {
+
+namespace {
+
+constexpr int kHeadWaves = 4;  // of a workgroup
+constexpr int kHeadBatch = 4;  // passes whose loads are in flight together
+
+// cos and sin of pos * freq.  The product of a 31-bit and a 24-bit number and
+// its turns (times 1 / 2 pi, which two doubles hold to 107 bits) keep their low
+// parts, so the place in the circle is right to 2^-50 turns at every position;
+// the angle's rest within +-pi/4 is rounded to fp32 once and the Taylor sums
+// end below 2^-28 there.
+__device__ __forceinline__ void cos_sin(int pos, float freq, float& c, float& s) {
+  constexpr double kTurn = 0x1.45f306dc9c883p-3;      // 1 / (2 pi)
+  constexpr double kTurnLow = -0x1.6b01ec5417056p-57;  // what kTurn leaves of it
+  const double p = (double)pos, f = (double)freq;
+  const double a = p * f;
+  const double r = a * kTurn;
+  const double low = fma(a, kTurn, -r) + fma(a, kTurnLow, fma(p, f, -a) * kTurn);
+  const double part = (r - rint(r)) + low;  // turns, within +-1/2
+  const double quarter = rint(4.0 * part);
+  const float z = (float)(fma(-0.25, quarter, part) * 6.283185307179586477);
+  const float z2 = z * z;
+  // Taylor sums, up to z^9 / 9! and z^10 / 10!
+  float sn = fmaf(z2, 2.75573192e-6f, -1.98412698e-4f);
+  sn = fmaf(z2, sn, 8.33333333e-3f);
+  sn = fmaf(z2, sn, -0.166666667f);
+  sn = fmaf(z * z2, sn, z);
+  float cs = fmaf(z2, -2.75573192e-7f, 2.48015873e-5f);
+  cs = fmaf(z2, cs, -1.38888889e-3f);
+  cs = fmaf(z2, cs, 4.16666667e-2f);
+  cs = fmaf(z2, cs, -0.5f);
+  cs = fmaf(z2, cs, 1.0f);
+  const int q = (int)quarter & 3;  // -2 .. 2
+  const float u = (q & 1) ? sn : cs, v = (q & 1) ? cs : sn;
+  c = (q == 1 || q == 2) ? -u : u;
+  s = (q & 2) ? -v : v;
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  const uint32_t lo = (uint32_t)dpp_i<CTRL>((int)(uint32_t)b), hi = (uint32_t)dpp_i<CTRL>((int)(uint32_t)(b >> 32));
+  return __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+}
+
+// Sum over each aligned group of L lanes (4 .. 64), in every lane of it.
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v) {
+  v += dpp_d<DPP_XOR1>(v);
+  v += dpp_d<DPP_XOR2>(v);
+  if constexpr (L >= 8) v += dpp_d<DPP_HALF_MIRROR>(v);
+  if constexpr (L >= 16) v += dpp_d<DPP_MIRROR>(v);
+  if constexpr (L >= 32) v += __shfl_xor(v, 16, 64);
+  if constexpr (L >= 64) v += __shfl_xor(v, 32, 64);
+  return v;
+}
+
+}  // namespace
+
+// y = turn(x * inv * w): a wave takes 64 / L heads of one token a pass, L lanes
+// a head with four dims each, and a lane has the same dims in every pass, so
+// that cos and sin are made once a wave.  Squares are summed in fp64 (each is
+// exact, no length of x overflows it).  A pair's other half lies in the lane
+// (neighbouring pairs) or comes through LDS.  One read and one write of every
+// value bound it.
+// V4: the halves' distance is a multiple of four dims, so the partner values
+// of a lane are one 16-byte vector.
+template <int L, bool ADJACENT, bool V4>
+__global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a) {
+  constexpr int HPP = 64 / L;  // heads of a pass
+  __shared__ __align__(16) float s_x[kHeadWaves][256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t g = (int64_t)blockIdx.x * kHeadWaves + wave;
+  const int t = (int)(g / a.waves_a_token), part = (int)(g % a.waves_a_token);
+  if (t >= a.n_tok) return;  // no barrier below
+  if (a.pos != nullptr && a.pos[t] < 0) return;
+  const int d0 = 4 * (lane % L);
+  const bool on = d0 < a.dim;
+  const int half = a.rot / 2;
+  float c[4], s[4];
+  int other[4];
+  bool turn[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int d = d0 + j;
+    c[j] = 1.f;
+    s[j] = 0.f;
+    turn[j] = false;
+    other[j] = d0 + j;
+    if (d < a.rot) {
+      const int i = ADJACENT ? d >> 1 : (d < half ? d : d - half);
+      const bool first = ADJACENT ? (d & 1) == 0 : d < half;
+      if (!ADJACENT) other[j] = first ? d + half : d - half;
+      const int axis = a.axis != nullptr ? a.axis[i] : 0;
+      if (axis >= 0 && axis < a.n_axes) {
+        turn[j] = true;
+        if (ADJACENT && (j & 1)) {  // the pair's angle once
+          c[j] = c[j - 1];
+          s[j] = -s[j - 1];
+        } else {
+          cos_sin(a.pos[(int64_t)axis * a.n_tok + t], a.freq[i], c[j], s[j]);
+          c[j] *= a.scale;
+          s[j] *= first ? -a.scale : a.scale;
+        }
+      }
+    }
+  }
+  f32x4 w[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    w[m] = f32x4{1.f, 1.f, 1.f, 1.f};
+    if (a.w[m] != nullptr && on) w[m] = *reinterpret_cast<const f32x4*>(a.w[m] + d0);
+  }
+  const int total = a.heads[0] + a.heads[1];
+  const int base = 4 * (lane & ~(L - 1));  // of the head's values in s_x
+  for (int p0 = part; p0 < a.passes; p0 += a.waves_a_token * kHeadBatch) {
+    f32x4 x[kHeadBatch];
+#pragma unroll
+    for (int b = 0; b < kHeadBatch; ++b) {
+      const int h = (p0 + b * a.waves_a_token) * HPP + lane / L;
+      x[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (h < total && on) {
+        const int m = h >= a.heads[0];
+        x[b] = *reinterpret_cast<const f32x4*>(a.x[m] + t * a.ldx[m] + (int64_t)(h - m * a.heads[0]) * a.dim + d0);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kHeadBatch; ++b) {
+      const int p = p0 + b * a.waves_a_token;
+      if (p >= a.passes) break;  // uniform
+      const int h = p * HPP + lane / L;
+      const int m = h >= a.heads[0];
+      const f32x4 wm = m ? w[1] : w[0];
+      f32x4 v = x[b];
+      double ss = 0.0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss += (double)v[j] * (double)v[j];
+      ss = lanes_sum<L>(ss);
+      if (m ? a.w[1] != nullptr : a.w[0] != nullptr) {
+        // 1 / sqrt: the hardware's, right to 2^-24, and a Newton step
+        const double ms = fma(ss, a.inv_dim, a.eps);
+        double inv = __builtin_amdgcn_rsq(ms);
+        inv *= fma(-0.5 * ms * inv, inv, 1.5);
+        const float r = (float)inv;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = (v[j] * r) * wm[j];
+      }
+      f32x4 q;
+      if constexpr (ADJACENT) {
+        q = f32x4{v[1], v[0], v[3], v[2]};
+      } else {
+        float* sx = s_x[wave];
+        *reinterpret_cast<f32x4*>(sx + 4 * lane) = v;
+        __builtin_amdgcn_wave_barrier();
+        if constexpr (V4) {
+          q = *reinterpret_cast<const f32x4*>(sx + base + other[0]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) q[j] = sx[base + other[j]];
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = turn[j] ? fmaf(v[j], c[j], q[j] * s[j]) : v[j];
+      if (h < total && on)
+        *reinterpret_cast<f32x4*>(a.y[m] + t * a.ldy[m] + (int64_t)(h - m * a.heads[0]) * a.dim + d0) = v;
+    }
+  }
+}
+
+namespace {
+
+template <int L>
+hipError_t launch(HeadsArgs a, int cus, hipStream_t st) {
+  const int total = a.heads[0] + a.heads[1], hpp = 64 / L;
+  a.passes = (total + hpp - 1) / hpp;
+  // a wave a pass until the device is full, then several, which share the angles
+  int64_t per = (int64_t)a.n_tok * a.passes / ((int64_t)cus * 16);
+  per = per < 1 ? 1 : (per > kHeadBatch ? kHeadBatch : per);
+  // below 2^25 waves, which is 2^31 threads (65536 tokens have 65536 at least)
+  const int64_t least = ((int64_t)a.n_tok * a.passes >> 24) + 1;
+  if (per < least) per = least;
+  a.waves_a_token = (int)((a.passes + per - 1) / per);
+  const int64_t waves = (int64_t)a.n_tok * a.waves_a_token;
+  const int64_t grid = (waves + kHeadWaves - 1) / kHeadWaves;
+  const dim3 b(64 * kHeadWaves);
+  if (a.adjacent)
+    hipLaunchKernelGGL((k_head_norm_rope<L, true, true>), dim3((unsigned)grid), b, 0, st, a);
+  else if (a.rot % 8 == 0)
+    hipLaunchKernelGGL((k_head_norm_rope<L, false, true>), dim3((unsigned)grid), b, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_head_norm_rope<L, false, false>), dim3((unsigned)grid), b, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_head_norm_rope(const HeadsArgs& a, int cus, hipStream_t st) {
+  if (a.dim <= 16) return launch<4>(a, cus, st);
+  if (a.dim <= 32) return launch<8>(a, cus, st);
+  if (a.dim <= 64) return launch<16>(a, cus, st);
+  if (a.dim <= 128) return launch<32>(a, cus, st);
+  return launch<64>(a, cus, st);
+}
+
+}  // namespace qmv

@@ -1,0 +1,31 @@
+// qmv_steps.h -- host-side interface of the steps around a decode layer's
+// matvecs (adapters, head norms with rotation, expert gates, log
+// probabilities) between the C ABI layer and their kernels.  Not installed;
+// not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qmv {
+
+// Norm and rotation of query and key heads.  Index 0: q, 1: k.
+struct HeadsArgs {
+  const float* x[2];  // [n_tok][ldx], head h at columns h * dim ..
+  int64_t ldx[2];
+  float* y[2];
+  int64_t ldy[2];
+  const float* w[2];  // NULL (no norm), or [dim]
+  int heads[2];
+  const int32_t* pos;   // NULL, or [n_axes][n_tok]
+  const float* freq;    // [rot / 2]
+  const int32_t* axis;  // NULL, or [rot / 2]
+  int n_tok, dim, rot, n_axes;
+  int adjacent;  // 1: pairs (2i, 2i + 1), 0: (i, i + rot / 2)
+  float scale;   // of cos and sin
+  double eps, inv_dim;
+  int passes, waves_a_token;  // set at launch
+};
+hipError_t launch_head_norm_rope(const HeadsArgs& a, int cus, hipStream_t st);
+
+}  // namespace qmv

@@ -597,6 +597,59 @@ qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq,
                               int64_t ldqo, float* k_out, int64_t ldko, void* stream);
 
 /*
+ * qmv_lora -- low-rank adapters of many requests beside projections that share
+ * their input (siblings, as in qmv_matvec_batch).  For every item i and row t
+ * with the adapter e = ids[t], of rank r = ranks[e]:
+ *   y_i[t][n] = base_i[t][n] + scales[e] * sum_{j < r} B_i[e][n][j] h[j],
+ *   h[j] = sum_c A_i[e][j][c] x[t][c]           (products and sums in fp32),
+ * and y_i[t] = base_i[t] where ids[t] is outside [0, n_adapters) or r is 0.
+ * type     : of A and B: QMV_F16, QMV_BF16 or QMV_F32.
+ * items    : HOST array of n_items descriptors, read during the call only:
+ *   a        [n_adapters][max_rank][k], b [n_adapters][n_rows][max_rank] of
+ *            `type` (device, 16-byte aligned); rows of A and columns of B from
+ *            an adapter's rank on may hold anything;
+ *   n_rows   1 .. QMV_MAX_LORA_ROWS;
+ *   base     NULL (zeros), or fp32 [n_tok][ldb], the projection's output; it
+ *            may be the item's y with ldb == ldy, else it must not overlap any
+ *            item's y;
+ *   y        fp32 [n_tok][ldy]; columns 0 .. n_rows - 1 of every row are
+ *            written.  y of different items must not overlap.
+ * x        : fp32 [n_tok][ldx] (device), 16-byte aligned, ldx >= k, ldx % 4 == 0.
+ * ids      : int32 [n_tok] (device), in any order; rows are dealt to
+ *            workgroups by eight of one adapter among each aligned 64, so an
+ *            adapter's rows are best neighbours.
+ * ranks    : NULL (max_rank), or int32 [n_adapters] (device), taken as within
+ *            0 .. max_rank;  scales: NULL (1), or fp32 [n_adapters] (device).
+ * ws       : workspace (device, 256-byte aligned) of
+ *            qmv_lora_workspace_bytes(...) bytes; its content does not matter
+ *            before or after a call.  Calls that share it must not overlap in
+ *            time.
+ * k and max_rank positive multiples of 8 (else QMV_ERR_INVALID_ARG); n_items
+ * <= QMV_MAX_BATCH, max_rank <= QMV_MAX_LORA_RANK, n_tok <=
+ * QMV_MAX_LORA_TOKENS, k <= QMV_MAX_LORA_K (else QMV_ERR_UNSUPPORTED).
+ * Asynchronous on `stream`; allocates nothing.  The result is the same on
+ * every call with the same arguments.
+ */
+#define QMV_MAX_LORA_RANK 256
+#define QMV_MAX_LORA_TOKENS 4096
+#define QMV_MAX_LORA_K 65536
+#define QMV_MAX_LORA_ROWS 262144
+typedef enum { QMV_F16 = 0, QMV_BF16 = 1, QMV_F32 = 2 } qmv_float_type;
+typedef struct {
+  const void* a;
+  const void* b;
+  int64_t n_rows;
+  const float* base;
+  int64_t ldb;
+  float* y;
+  int64_t ldy;
+} qmv_lora_item;
+size_t qmv_lora_workspace_bytes(int64_t n_items, int64_t max_rank, int64_t n_tok);
+qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_items, const float* x, int64_t ldx,
+                    int64_t n_tok, int64_t k, const int32_t* ids, int64_t n_adapters, int64_t max_rank,
+                    const int32_t* ranks, const float* scales, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qmv_block_dots -- test hook: the exact integer partial of every 32-weight
  * block, computed by the same device decode and dot routines as qmv_matvec.
  * out : int32 [n_tok][n_rows][k/32][c] (device), c = 2 for q4_K and q5_K

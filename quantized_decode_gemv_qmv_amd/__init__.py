@@ -27,7 +27,7 @@ __all__ = [
     "block_dots",
     "block_dots_mx", "moe_block_dots", "stream_read",
     "rmsnorm_quantize", "kv_append", "kv_attn", "kv_attn_workspace_bytes", "KV_BLOCK",
-    "head_norm_rope",
+    "head_norm_rope", "lora", "lora_workspace_bytes",
     "set_tuning", "swiglu_quantize", "router_topk", "variant_name", "variants", "pick_variant", "matvec_plan", "MAX_TOKENS", "MAX_MOE_TOKENS",
 ]
 
@@ -55,6 +55,12 @@ class _Rope(ctypes.Structure):
     _fields_ = [("pos", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
                 ("n_axes", ctypes.c_int64), ("rot_dim", ctypes.c_int64), ("interleaved", ctypes.c_int64),
                 ("scale", ctypes.c_float)]
+
+
+class _LoraItem(ctypes.Structure):
+    """qmv_lora_item of include/qmv.h."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("base", ctypes.c_void_p),
+                ("ldb", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
 
 
 class _Kv(ctypes.Structure):
@@ -120,6 +126,8 @@ def lib():
         "qmv_kv_attn": ([ctypes.POINTER(_Kv), P, I64, I64, ctypes.c_float, I64, P, I64, P, P, SZ, P], I),
         "qmv_head_norm_rope": ([ctypes.POINTER(_Rope), P, I64, I64, P, P, I64, I64, P, I64, I64, ctypes.c_float, P,
                                 I64, P, I64, P], I),
+        "qmv_lora_workspace_bytes": ([I64, I64, I64], SZ),
+        "qmv_lora": ([I, ctypes.POINTER(_LoraItem), I64, P, I64, I64, I64, P, I64, I64, P, P, P, SZ, P], I),
         "qmv_block_dots": ([I, P, I64, I64, P, I64, P, P], I),
         "qmv_block_dots_mx": ([I, P, I64, I64, P, I64, I64, I, P, P], I),
         "qmv_moe_block_dots": ([I, P, I64, I64, I64, P, I, P, I64, I64, I64, P, P, SZ, P], I),
@@ -655,6 +663,58 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor | 
                                     n_tok, dim, eps, q_out.data_ptr(), _rows(q_out, shape, "q_out"), kop, ldko,
                                     _stream(stream)), "qmv_head_norm_rope")
     return q_out, k_out
+
+
+def lora_workspace_bytes(n_items: int, max_rank: int, n_tok: int) -> int:
+    return int(lib().qmv_lora_workspace_bytes(n_items, max_rank, n_tok))
+
+
+_FLOATS = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def lora(x: torch.Tensor, ids: torch.Tensor, items, ranks: torch.Tensor | None = None,
+         scales: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> list:
+    """Low-rank adapters beside projections that share x fp32 [T][K] (rows may
+    be strided): for each (a, b, base, y) of ``items``, a [E][R][K] and b
+    [E][N][R] of float16, bfloat16 or float32, row t of y becomes base[t] +
+    scales[e] * b[e] (a[e] x[t]) with the adapter e = ids[t] (int32 [T]; outside
+    0 .. E - 1: base alone), over the first ranks[e] (int32 [E], None: R) rows of
+    a and columns of b.  base fp32 [T][N] (None: zeros) may be y itself; y None
+    is allocated.  scales fp32 [E], None: 1.  ``ws`` (uint8, of
+    lora_workspace_bytes bytes) is allocated when None.  Returns the list of y."""
+    if x.dim() != 2 or not items:
+        raise ValueError("x must be [T][K], and there must be an item")
+    n_tok, k = x.shape
+    first = items[0][0]
+    if first.dim() != 3 or first.dtype not in _FLOATS:
+        raise ValueError("a must be [E][R][K] of float16, bfloat16 or float32")
+    kind, (e, rank, _) = first.dtype, first.shape
+    arr = (_LoraItem * len(items))()
+    outs = []
+    for i, (a, b, base, y) in enumerate(items):
+        if a.shape != (e, rank, k) or b.dim() != 3 or b.shape[0] != e or b.shape[2] != rank:
+            raise ValueError("a must be [E][R][K] and b [E][N][R], with the same E and R in every item")
+        n = b.shape[1]
+        if y is None:
+            y = _new(x, (n_tok, n), torch.float32, stream)
+        _here(a, b, base, y)
+        shape = (n_tok, n)
+        arr[i] = _LoraItem(_whole(a, kind, "a"), _whole(b, kind, "b"), n, None if base is None else base.data_ptr(),
+                           0 if base is None else _rows(base, shape, "base"), y.data_ptr(), _rows(y, shape, "y"))
+        outs.append(y)
+    if ws is None:
+        ws = _new(x, (max(lora_workspace_bytes(len(items), rank, n_tok), 1),), torch.uint8, stream)
+    _here(x, ids, ranks, scales, ws)
+    for name, v, dtype, n in (("ids", ids, torch.int32, n_tok), ("ranks", ranks, torch.int32, e),
+                              ("scales", scales, torch.float32, e)):
+        if v is not None and v.numel() != n:
+            raise ValueError(f"{name} must hold {n} values")
+    _check(lib().qmv_lora(_FLOATS[kind], arr, len(items), x.data_ptr(), _rows(x, (n_tok, k), "x"), n_tok, k,
+                          _whole(ids, torch.int32, "ids"), e, rank,
+                          None if ranks is None else _whole(ranks, torch.int32, "ranks"),
+                          None if scales is None else _whole(scales, torch.float32, "scales"),
+                          _whole(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "qmv_lora")
+    return outs
 
 
 def block_dots(fmt: int, w: torch.Tensor, n_rows: int, k: int, xq: torch.Tensor, n_tok: int,

@@ -1104,6 +1104,56 @@ QMV_API qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int6
   return hip_status(launch_head_norm_rope(a, device_cus(), static_cast<hipStream_t>(stream)));
 }
 
+// The sizes of an adapter call, whatever its pointers.
+static qmv_status check_lora_sizes(int64_t n_items, int64_t max_rank, int64_t n_tok) {
+  if (n_items < 1 || max_rank < 1 || max_rank % 8 || n_tok < 1) return QMV_ERR_INVALID_ARG;
+  if (n_items > QMV_MAX_BATCH || max_rank > QMV_MAX_LORA_RANK || n_tok > QMV_MAX_LORA_TOKENS)
+    return QMV_ERR_UNSUPPORTED;
+  return QMV_OK;
+}
+
+QMV_API size_t qmv_lora_workspace_bytes(int64_t n_items, int64_t max_rank, int64_t n_tok) {
+  if (check_lora_sizes(n_items, max_rank, n_tok) != QMV_OK) return 0;
+  return static_cast<size_t>(align256(4 * n_items * max_rank * n_tok * lora_slices(n_items, max_rank, n_tok)));
+}
+
+QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_items, const float* x,
+                            int64_t ldx, int64_t n_tok, int64_t k, const int32_t* ids, int64_t n_adapters,
+                            int64_t max_rank, const int32_t* ranks, const float* scales, void* ws, size_t ws_bytes,
+                            void* stream) {
+  if ((type != QMV_F16 && type != QMV_BF16 && type != QMV_F32) || items == nullptr || x == nullptr || ids == nullptr ||
+      ws == nullptr || n_adapters < 1 || k < 1 || k % 8 || ldx < k)
+    return QMV_ERR_INVALID_ARG;
+  const qmv_status st = check_lora_sizes(n_items, max_rank, n_tok);
+  if (st != QMV_OK) return st;
+  if (n_adapters > INT32_MAX || k > QMV_MAX_LORA_K) return QMV_ERR_UNSUPPORTED;
+  LoraArgs a{};
+  for (int64_t i = 0; i < n_items; ++i) {
+    const qmv_lora_item& m = items[i];
+    if (m.a == nullptr || m.b == nullptr || m.y == nullptr || m.n_rows < 1 || m.ldy < m.n_rows ||
+        (m.base != nullptr && m.ldb < m.n_rows))
+      return QMV_ERR_INVALID_ARG;
+    if (m.n_rows > QMV_MAX_LORA_ROWS) return QMV_ERR_UNSUPPORTED;
+    if (!aligned(m.a, 16) || !aligned(m.b, 16) || !aligned(m.y, 4) || !aligned(m.base, 4)) return QMV_ERR_MISALIGNED;
+    a.item[i] = LoraItem{m.a, m.b, m.base, m.y, m.ldb, m.ldy, static_cast<int>(m.n_rows), 0};
+  }
+  if (!aligned(x, 16) || ldx % 4 || !aligned(ids, 4) || !aligned(ranks, 4) || !aligned(scales, 4) || !aligned(ws, 256))
+    return QMV_ERR_MISALIGNED;
+  if (ws_bytes < qmv_lora_workspace_bytes(n_items, max_rank, n_tok)) return QMV_ERR_WORKSPACE;
+  a.n_items = static_cast<int>(n_items);
+  a.x = x;
+  a.ldx = ldx;
+  a.n_tok = static_cast<int>(n_tok);
+  a.k = static_cast<int>(k);
+  a.ids = ids;
+  a.adapters = static_cast<int>(n_adapters);
+  a.max_rank = static_cast<int>(max_rank);
+  a.ranks = ranks;
+  a.scales = scales;
+  a.h = static_cast<float*>(ws);
+  return hip_status(launch_lora(type, a, static_cast<hipStream_t>(stream)));
+}
+
 QMV_API qmv_status qmv_block_dots(qmv_type type, const void* w, int64_t n_rows, int64_t k,
                                   const void* xq, int64_t n_tok, int32_t* out, void* stream) {
   qmv_status st = check_weights(type, w, n_rows, k);

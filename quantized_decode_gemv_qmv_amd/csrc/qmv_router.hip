@@ -27,35 +27,6 @@ constexpr int kRouterMaxExperts = 1024;
 constexpr int kRouterMaxTopK = 16;
 constexpr int kRouterWaves = 8;
 
-// One butterfly step over the first 2H values of v: lanes whose bit H is set
-// keep the upper half, the others the lower half, each adding its partner's
-// copy of the half it keeps.  After the steps H = P/2 .. 1, lane l holds the
-// sum of value l % P over its aligned group of P lanes.
-template <int H>
-__device__ __forceinline__ void fold(float* v, int lane) {
-  const bool hi = (lane & H) != 0;
-#pragma unroll
-  for (int j = 0; j < H; ++j) {
-    const float send = hi ? v[j] : v[j + H];
-    const float keep = hi ? v[j + H] : v[j];
-    v[j] = keep + __shfl_xor(send, H, 64);
-  }
-}
-
-template <int P>
-__device__ __forceinline__ float fold_all(float* v, int lane) {
-  if constexpr (P >= 64) fold<32>(v, lane);
-  if constexpr (P >= 32) fold<16>(v, lane);
-  if constexpr (P >= 16) fold<8>(v, lane);
-  if constexpr (P >= 8) fold<4>(v, lane);
-  if constexpr (P >= 4) fold<2>(v, lane);
-  if constexpr (P >= 2) fold<1>(v, lane);
-  float r = v[0];
-#pragma unroll
-  for (int o = P; o < 64; o <<= 1) r += __shfl_xor(r, o, 64);  // the other lane groups
-  return r;
-}
-
 // EG experts x one chunk of 256 columns (one 16-byte load per lane and row),
 // TG tokens; rows and tokens past the ends are clamped (their products are
 // discarded at the store).

@@ -28,4 +28,34 @@ struct HeadsArgs {
 };
 hipError_t launch_head_norm_rope(const HeadsArgs& a, int cus, hipStream_t st);
 
+// Low-rank adapters beside projections that share their input.
+enum : int { kF16 = 0, kBF16 = 1, kF32 = 2 };  // qmv_float_type
+constexpr int kLoraItems = 8;
+struct LoraItem {
+  const void* a;  // [adapters][max_rank][k]
+  const void* b;  // [adapters][n][max_rank]
+  const float* base;
+  float* y;
+  int64_t ldb, ldy;
+  int n;
+  int first;  // of its workgroups along the outputs
+};
+struct LoraArgs {
+  LoraItem item[kLoraItems];
+  int n_items;
+  const float* x;
+  int64_t ldx;
+  int n_tok, k;
+  const int32_t* ids;  // [n_tok]
+  int adapters, max_rank;
+  const int32_t* ranks;  // NULL, or [adapters]
+  const float* scales;   // NULL, or [adapters]
+  float* h;              // [slices][n_tok][n_items][max_rank]
+  int slices, slice;     // of k, and their length; set at launch
+};
+// The most partial sums of h that a call makes (k alone can make them fewer).
+constexpr int kLoraMaxSlices = 16;
+int lora_slices(int64_t n_items, int64_t max_rank, int64_t n_tok);
+hipError_t launch_lora(int type, LoraArgs a, hipStream_t st);
+
 }  // namespace qmv

@@ -650,6 +650,111 @@ qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_i
                     const int32_t* ranks, const float* scales, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * qmv_router_gate -- MoE router with scores, a balance bias and expert groups:
+ * the routing ids and weights that qmv_moe_matvec takes, for models whose
+ * choice is more than qmv_router_topk's softmax over the chosen logits.
+ * (Castagna Veloce page, "Fused operations": router matvec, gating, top-k and
+ * weight normalization.)  For token t, in fp64 from the fp32 inputs on, so that
+ * the choice does not hang on the order of a sum:
+ *   l[e] = sum_i wr[e][i] x[t][i],
+ *   s[e] = 1 / (1 + exp(-l[e])), or exp(l[e]) / sum over all experts,
+ *   c[e] = s[e] + bias[e],
+ *   the groups of n_experts / n_groups neighbouring experts are ordered by the
+ *   sum of their group_best largest c; the top_groups first stay (n_groups 1:
+ *   all experts do),
+ *   ids[t][0..top_k-1] = the experts of those by c, the largest first,
+ *   weights[t][j] = scale * s[ids[t][j]], with renorm over the sum of the
+ *                   chosen s (scale / top_k each where that sum is 0).
+ * Equal values are ordered by the lower index.  A c (or a group's sum) that is
+ * not a number counts as -inf: ids are within [0, n_experts) and all different
+ * whatever the inputs hold.
+ * gate     : HOST struct, read during the call only:
+ *   scoring   QMV_GATE_SOFTMAX or QMV_GATE_SIGMOID;
+ *   bias      NULL (zeros), or fp32 [n_experts] (device);
+ *   n_groups, top_groups, group_best: n_groups a divisor of n_experts,
+ *             top_groups 1 .. n_groups with at least top_k experts in them;
+ *             group_best 1 or 2, at most the group's experts (read only if
+ *             n_groups > 1);
+ *   renorm    0 or 1;  scale finite.
+ * x        : fp32 [n_tok][ldx] (device), 16-byte aligned, ldx >= k, ldx % 4 == 0.
+ * wr       : fp32 router weights [n_experts][k] (device), 16-byte aligned.
+ * ids      : int32 [n_tok][top_k] (device); weights: fp32 [n_tok][top_k].
+ * logits   : NULL, or fp32 [n_tok][n_experts] (device) that receives l, rounded.
+ * xq       : NULL, or an activation buffer that receives Q8(x), as for
+ *            qmv_router_topk (k % 32 == 0).
+ * ws       : workspace (device, 256-byte aligned) of
+ *            qmv_router_gate_workspace_bytes(...) bytes, zero-filled once when
+ *            allocated and left so in its counters by every completed call.
+ *            One workspace may serve calls of different shapes that do not
+ *            overlap in time.
+ * 1 <= n_tok <= QMV_MAX_MOE_TOKENS, k % 4 == 0, k <= 2^24,
+ * 1 <= top_k <= min(n_experts, QMV_MAX_TOP_K), n_experts <= QMV_MAX_EXPERTS,
+ * n_groups <= QMV_MAX_GATE_GROUPS.  Errors as for qmv_router_topk, and
+ * QMV_ERR_WORKSPACE.  Asynchronous on `stream`; allocates nothing.
+ */
+#define QMV_MAX_GATE_GROUPS 64
+typedef enum { QMV_GATE_SOFTMAX = 0, QMV_GATE_SIGMOID = 1 } qmv_gate_scoring;
+typedef struct {
+  int64_t scoring;
+  const float* bias;
+  int64_t n_groups;
+  int64_t top_groups;
+  int64_t group_best;
+  int64_t renorm;
+  float scale;
+} qmv_gate;
+size_t qmv_router_gate_workspace_bytes(int64_t n_tok, int64_t n_experts);
+qmv_status qmv_router_gate(const float* x, int64_t ldx, int64_t n_tok, int64_t k, const float* wr, int64_t n_experts,
+                           int64_t top_k, const qmv_gate* gate, int32_t* ids, float* weights, float* logits, void* xq,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * qmv_token_logprobs -- log probabilities of given tokens, entropy and the
+ * likeliest alternatives of rows of logits (the output head's matvec), what a
+ * speculative verify step or a scoring request reads off them.  (zhuai.tech
+ * GLM-5.3 page, "MTP saves full-model execution rounds": drafts verified in
+ * batches.)  For row t, with z = scale * logits[t] over n_vocab tokens:
+ *   lse = ln sum_v exp(z[v]),
+ *   logprobs[t][g] = z[given[t][g]] - lse, -inf for a token outside
+ *                    [0, n_vocab),
+ *   entropy[t] = lse - sum_v p[v] z[v], p = exp(z - lse)  (0 where p is 0),
+ *   top_ids[t] = the top_n tokens by their logits, a larger one first and on
+ *                equal logits the lower index first (-0 equals 0), and
+ *   top_logprobs[t] = their z - lse.
+ * Terms and sums are fp32, relative to the row's largest z.  A logit of -inf
+ * is a forbidden token; a row of nothing else has log probabilities of -inf
+ * and entropy 0.  A row that holds NaN or +inf has log probabilities and an
+ * entropy of NaN, and its alternatives are ordered with NaN as -inf.
+ * logits   : fp32 [n_tok][ldl] (device, 4-byte aligned), ldl >= n_vocab.
+ * scale    : positive and finite (1 / temperature).
+ * given    : int32 [n_tok][n_given] (device), n_given 0 .. QMV_MAX_GIVEN;
+ *            logprobs fp32 of the same shape; both may be NULL if n_given is 0.
+ * entropy  : NULL, or fp32 [n_tok] (device).
+ * top_ids, top_logprobs : int32 and fp32 [n_tok][top_n] (device), top_n
+ *            0 .. QMV_MAX_TOP_TOKENS and at most n_vocab; NULL if top_n is 0.
+ *            Something of logprobs, entropy and alternatives is asked for.
+ * ws       : optional workspace (device, 256-byte aligned) of
+ *            qmv_token_logprobs_workspace_bytes(...) bytes, zero-filled once
+ *            when allocated and left so in its counters by every completed
+ *            call; it lets workgroups share a row, which calls of few rows need
+ *            for speed.  NULL: one workgroup a row.  One workspace may serve
+ *            calls of different shapes that do not overlap in time.  Results
+ *            are the same on every call with the same arguments, and with and
+ *            without a workspace differ in rounding only (ids not at all).
+ * n_tok <= QMV_MAX_ACT_ROWS, n_vocab <= QMV_MAX_VOCAB (else
+ * QMV_ERR_UNSUPPORTED).  Asynchronous on `stream`; allocates nothing.
+ * qmv_token_logprobs_workspace_bytes is host only; 0: the arguments are
+ * invalid, or no workspace is used.
+ */
+#define QMV_MAX_VOCAB (1 << 24)
+#define QMV_MAX_TOP_TOKENS 32
+#define QMV_MAX_GIVEN 65536
+size_t qmv_token_logprobs_workspace_bytes(int64_t n_tok, int64_t n_vocab, int64_t top_n);
+qmv_status qmv_token_logprobs(const float* logits, int64_t ldl, int64_t n_tok, int64_t n_vocab, float scale,
+                              const int32_t* given, int64_t n_given, float* logprobs, float* entropy, int64_t top_n,
+                              int32_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qmv_block_dots -- test hook: the exact integer partial of every 32-weight
  * block, computed by the same device decode and dot routines as qmv_matvec.
  * out : int32 [n_tok][n_rows][k/32][c] (device), c = 2 for q4_K and q5_K

@@ -27,7 +27,8 @@ __all__ = [
     "block_dots",
     "block_dots_mx", "moe_block_dots", "stream_read",
     "rmsnorm_quantize", "kv_append", "kv_attn", "kv_attn_workspace_bytes", "KV_BLOCK",
-    "head_norm_rope", "lora", "lora_workspace_bytes",
+    "head_norm_rope", "lora", "lora_workspace_bytes", "router_gate", "router_gate_workspace_bytes",
+    "token_logprobs", "token_logprobs_workspace_bytes",
     "set_tuning", "swiglu_quantize", "router_topk", "variant_name", "variants", "pick_variant", "matvec_plan", "MAX_TOKENS", "MAX_MOE_TOKENS",
 ]
 
@@ -61,6 +62,13 @@ class _LoraItem(ctypes.Structure):
     """qmv_lora_item of include/qmv.h."""
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("n_rows", ctypes.c_int64), ("base", ctypes.c_void_p),
                 ("ldb", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64)]
+
+
+class _Gate(ctypes.Structure):
+    """qmv_gate of include/qmv.h."""
+    _fields_ = [("scoring", ctypes.c_int64), ("bias", ctypes.c_void_p), ("n_groups", ctypes.c_int64),
+                ("top_groups", ctypes.c_int64), ("group_best", ctypes.c_int64), ("renorm", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
 
 
 class _Kv(ctypes.Structure):
@@ -128,6 +136,10 @@ def lib():
                                 I64, P, I64, P], I),
         "qmv_lora_workspace_bytes": ([I64, I64, I64], SZ),
         "qmv_lora": ([I, ctypes.POINTER(_LoraItem), I64, P, I64, I64, I64, P, I64, I64, P, P, P, SZ, P], I),
+        "qmv_router_gate_workspace_bytes": ([I64, I64], SZ),
+        "qmv_router_gate": ([P, I64, I64, I64, P, I64, I64, ctypes.POINTER(_Gate), P, P, P, P, P, SZ, P], I),
+        "qmv_token_logprobs_workspace_bytes": ([I64, I64, I64], SZ),
+        "qmv_token_logprobs": ([P, I64, I64, I64, ctypes.c_float, P, I64, P, P, I64, P, P, P, SZ, P], I),
         "qmv_block_dots": ([I, P, I64, I64, P, I64, P, P], I),
         "qmv_block_dots_mx": ([I, P, I64, I64, P, I64, I64, I, P, P], I),
         "qmv_moe_block_dots": ([I, P, I64, I64, I64, P, I, P, I64, I64, I64, P, P, SZ, P], I),
@@ -715,6 +727,126 @@ def lora(x: torch.Tensor, ids: torch.Tensor, items, ranks: torch.Tensor | None =
                           None if scales is None else _whole(scales, torch.float32, "scales"),
                           _whole(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "qmv_lora")
     return outs
+
+
+def router_gate_workspace_bytes(n_tok: int, n_experts: int) -> int:
+    return int(lib().qmv_router_gate_workspace_bytes(n_tok, n_experts))
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def router_gate(x: torch.Tensor, wr: torch.Tensor, top_k: int, scoring: str = "softmax",
+                bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int = 1, group_best: int = 2,
+                renorm: bool = True, scale: float = 1.0, ids: torch.Tensor | None = None,
+                weights: torch.Tensor | None = None, logits: torch.Tensor | None = None,
+                xq: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """x fp32 [T][K] (rows may be strided), router weights fp32 [E][K] -> (ids
+    int32 [T][top_k], weights fp32 [T][top_k]): scores "softmax" (over all
+    experts) or "sigmoid" of the router's logits; the choice goes by score +
+    bias (fp32 [E]) within the top_groups of n_groups groups whose group_best
+    largest choices sum highest; the weights are the scores, with renorm over
+    their sum, times scale.  logits (fp32 [T][E]) and xq, if given, receive the
+    logits and the Q8 blocks of x.  ``ws`` (uint8, zero-filled once, of
+    router_gate_workspace_bytes bytes) is allocated when None."""
+    if x.dim() == 1:
+        x = x.view(1, -1)
+    if x.dim() != 2 or wr.dim() != 2 or wr.shape[1] != x.shape[1]:
+        raise ValueError("x must be [T][K] and wr [E][K]")
+    if scoring not in _SCORING:
+        raise ValueError("scoring must be 'softmax' or 'sigmoid'")
+    n_tok, k = x.shape
+    e = wr.shape[0]
+    if ids is None:
+        ids = _new(x, (n_tok, max(top_k, 1)), torch.int32, stream)
+    if weights is None:
+        weights = _new(x, (n_tok, max(top_k, 1)), torch.float32, stream)
+    if ids.shape != (n_tok, top_k) or weights.shape != (n_tok, top_k):
+        raise ValueError("ids and weights must be [T][top_k]")
+    if ws is None:
+        ws = _new(x, (max(router_gate_workspace_bytes(n_tok, e), 1),), torch.uint8, stream)
+        if stream is None:
+            ws.zero_()
+        else:
+            with torch.cuda.stream(stream):
+                ws.zero_()
+    _here(x, wr, bias, ids, weights, logits, xq, ws)
+    if bias is not None and bias.numel() != e:
+        raise ValueError("bias must hold one value an expert")
+    if logits is not None and logits.shape != (n_tok, e):
+        raise ValueError("logits must be [T][E]")
+    if xq is not None and xq.numel() < act_bytes(n_tok, k):
+        raise ValueError("activation buffer too small")
+    gate = _Gate(_SCORING[scoring], None if bias is None else _whole(bias, torch.float32, "bias"), n_groups, top_groups,
+                 group_best, bool(renorm), scale)
+    _check(lib().qmv_router_gate(x.data_ptr(), _rows(x, (n_tok, k), "x"), n_tok, k, _whole(wr, torch.float32, "wr"), e,
+                                 top_k, ctypes.byref(gate), _whole(ids, torch.int32, "ids"),
+                                 _whole(weights, torch.float32, "weights"),
+                                 None if logits is None else _whole(logits, torch.float32, "logits"),
+                                 None if xq is None else _whole(xq, torch.uint8, "xq"), _whole(ws, torch.uint8, "ws"),
+                                 ws.numel(), _stream(stream)), "qmv_router_gate")
+    return ids, weights
+
+
+def token_logprobs_workspace_bytes(n_tok: int, n_vocab: int, top_n: int) -> int:
+    return int(lib().qmv_token_logprobs_workspace_bytes(n_tok, n_vocab, top_n))
+
+
+def token_logprobs(logits: torch.Tensor, given: torch.Tensor | None = None, top_n: int = 0, scale: float = 1.0,
+                   logprobs: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                   top_ids: torch.Tensor | None = None, top_logprobs: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None, stream=None):
+    """logits fp32 [T][V] (rows may be strided) -> (logprobs, entropy, top_ids,
+    top_logprobs) of softmax(scale * logits): the log probabilities of the
+    tokens given (int32 [T] or [T][G]; None without them), the entropies [T],
+    and the top_n likeliest tokens int32 [T][top_n] with theirs (None, None if
+    top_n is 0).  Outputs are allocated when None.  ``ws`` (uint8, zero-filled
+    once, of token_logprobs_workspace_bytes bytes) lets workgroups share a row;
+    without it each row has one, which is slow for few rows."""
+    if logits.dim() == 1:
+        logits = logits.view(1, -1)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T][V]")
+    t, v = logits.shape
+    n_given = 0
+    if given is not None:
+        if given.shape[:1] != (t,) or given.dim() > 2:
+            raise ValueError("given must be [T] or [T][G]")
+        n_given = 1 if given.dim() == 1 else given.shape[1]
+        if logprobs is None:
+            logprobs = _new(logits, given.shape, torch.float32, stream)
+        if logprobs.shape != given.shape:
+            raise ValueError("logprobs must have the shape of given")
+    elif logprobs is not None:
+        raise ValueError("logprobs without given")
+    if entropy is None:
+        entropy = _new(logits, (t,), torch.float32, stream)
+    if entropy.shape != (t,):
+        raise ValueError("entropy must be [T]")
+    if top_n > 0:
+        if top_ids is None:
+            top_ids = _new(logits, (t, top_n), torch.int32, stream)
+        if top_logprobs is None:
+            top_logprobs = _new(logits, (t, top_n), torch.float32, stream)
+        if top_ids.shape != (t, top_n) or top_logprobs.shape != (t, top_n):
+            raise ValueError("top_ids and top_logprobs must be [T][top_n]")
+    elif top_ids is not None or top_logprobs is not None:
+        raise ValueError("top_ids or top_logprobs without top_n")
+    if ws is not None and ws.numel() == 0:
+        ws = None
+    _here(logits, given, logprobs, entropy, top_ids, top_logprobs, ws)
+
+    def whole(x, dtype, name):
+        return None if x is None else _whole(x, dtype, name)
+
+    _check(lib().qmv_token_logprobs(logits.data_ptr(), _rows(logits, (t, v), "logits"), t, v, scale,
+                                    whole(given, torch.int32, "given"), n_given,
+                                    whole(logprobs, torch.float32, "logprobs"),
+                                    _whole(entropy, torch.float32, "entropy"), top_n,
+                                    whole(top_ids, torch.int32, "top_ids"),
+                                    whole(top_logprobs, torch.float32, "top_logprobs"), whole(ws, torch.uint8, "ws"),
+                                    0 if ws is None else ws.numel(), _stream(stream)), "qmv_token_logprobs")
+    return logprobs, entropy, top_ids, top_logprobs
 
 
 def block_dots(fmt: int, w: torch.Tensor, n_rows: int, k: int, xq: torch.Tensor, n_tok: int,

@@ -23,7 +23,8 @@ FORMATS = {0: "q8_0", 1: "q4_k", 2: "iq4_xs", 3: "q5_k", 4: "q6_k", 5: "q8g128"}
 MX_FORMATS = (0, 1, 2, 5)
 SOURCES = ([(s, os.path.splitext(s)[0], []) for s in
             ("qmv_api.hip", "qmv_variants.hip", "qmv_quant.hip", "qmv_moe.hip", "qmv_router.hip",
-             "qmv_measure.hip", "qmv_norm.hip", "qmv_kv.hip", "qmv_attn.hip", "qmv_rope.hip", "qmv_lora.hip")]
+             "qmv_measure.hip", "qmv_norm.hip", "qmv_kv.hip", "qmv_attn.hip", "qmv_rope.hip", "qmv_lora.hip",
+             "qmv_gate.hip", "qmv_logprobs.hip")]
            + [("qmv_matvec.hip", f"qmv_matvec_{n}", [f"-DQMV_MATVEC_FMT={f}"]) for f, n in FORMATS.items()]
            + [("qmv_mfma.hip", f"qmv_mfma_{FORMATS[f]}", [f"-DQMV_MX_FMT={f}"]) for f in MX_FORMATS]
            + [("qmv_mxf.hip", f"qmv_mxf_{FORMATS[f]}", [f"-DQMV_MX_FMT={f}"]) for f in MX_FORMATS])

@@ -1154,6 +1154,118 @@ QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int
   return hip_status(launch_lora(type, a, static_cast<hipStream_t>(stream)));
 }
 
+// Workspace of qmv_router_gate: arrival counters of the token groups, then
+// the logits, at a fixed offset so that calls of different shapes can share it.
+constexpr int64_t kGateCounterBytes = 256;
+
+QMV_API size_t qmv_router_gate_workspace_bytes(int64_t n_tok, int64_t n_experts) {
+  if (n_tok < 1 || n_tok > QMV_MAX_MOE_TOKENS || n_experts < 1 || n_experts > QMV_MAX_EXPERTS) return 0;
+  return static_cast<size_t>(kGateCounterBytes + align256(8 * n_tok * n_experts));
+}
+
+QMV_API qmv_status qmv_router_gate(const float* x, int64_t ldx, int64_t n_tok, int64_t k, const float* wr,
+                                   int64_t n_experts, int64_t top_k, const qmv_gate* gate, int32_t* ids,
+                                   float* weights, float* logits, void* xq, void* ws, size_t ws_bytes, void* stream) {
+  if (x == nullptr || wr == nullptr || gate == nullptr || ids == nullptr || weights == nullptr || ws == nullptr ||
+      n_tok < 1 || k < 1 || k % 4 || ldx < k || ldx % 4 || n_experts < 1 || top_k < 1 || top_k > n_experts ||
+      (xq != nullptr && k % 32))
+    return QMV_ERR_INVALID_ARG;
+  if ((gate->scoring != QMV_GATE_SOFTMAX && gate->scoring != QMV_GATE_SIGMOID) ||
+      (gate->renorm != 0 && gate->renorm != 1) || !(gate->scale - gate->scale == 0.f) || gate->n_groups < 1 ||
+      n_experts % gate->n_groups || gate->top_groups < 1 || gate->top_groups > gate->n_groups ||
+      top_k > gate->top_groups * (n_experts / gate->n_groups) ||
+      (gate->n_groups > 1 && ((gate->group_best != 1 && gate->group_best != 2) ||
+                              gate->group_best > n_experts / gate->n_groups)))
+    return QMV_ERR_INVALID_ARG;
+  if (n_tok > QMV_MAX_MOE_TOKENS || k > (int64_t(1) << 24) || n_experts > QMV_MAX_EXPERTS ||
+      top_k > QMV_MAX_TOP_K || gate->n_groups > QMV_MAX_GATE_GROUPS)
+    return QMV_ERR_UNSUPPORTED;
+  if (!aligned(x, 16) || !aligned(wr, 16) || !aligned(gate->bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(logits, 4) || !aligned(xq, 256) || !aligned(ws, 256))
+    return QMV_ERR_MISALIGNED;
+  if (ws_bytes < qmv_router_gate_workspace_bytes(n_tok, n_experts)) return QMV_ERR_WORKSPACE;
+  GateArgs a{};
+  a.x = x;
+  a.ldx = ldx;
+  a.wr = wr;
+  a.n_tok = static_cast<int>(n_tok);
+  a.k = static_cast<int>(k);
+  a.n_experts = static_cast<int>(n_experts);
+  a.top_k = static_cast<int>(top_k);
+  a.sigmoid = gate->scoring == QMV_GATE_SIGMOID;
+  a.bias = gate->bias;
+  a.groups = static_cast<int>(gate->n_groups);
+  a.top_groups = static_cast<int>(gate->top_groups);
+  a.group_best = static_cast<int>(gate->group_best);
+  a.renorm = static_cast<int>(gate->renorm);
+  a.scale = gate->scale;
+  a.ids = ids;
+  a.weights = weights;
+  a.logits_out = logits;
+  if (xq != nullptr) {
+    const ActView v = act_view(xq, n_tok, k);
+    a.qs = const_cast<int8_t*>(v.qs);
+    a.qd = const_cast<float*>(v.d);
+    a.qsum = const_cast<int32_t*>(v.s);
+  }
+  a.logits = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kGateCounterBytes);
+  return hip_status(launch_router_gate(a, static_cast<hipStream_t>(stream)));
+}
+
+static qmv_status check_logprob_sizes(int64_t n_tok, int64_t n_vocab, int64_t top_n) {
+  if (n_tok < 1 || n_vocab < 1 || top_n < 0 || top_n > n_vocab) return QMV_ERR_INVALID_ARG;
+  if (n_tok > QMV_MAX_ACT_ROWS || n_vocab > QMV_MAX_VOCAB || top_n > QMV_MAX_TOP_TOKENS) return QMV_ERR_UNSUPPORTED;
+  return QMV_OK;
+}
+
+// Workspace of qmv_token_logprobs: arrival counters of the rows, then the
+// parts' keys and sums.
+constexpr int64_t kLogprobCounterBytes = 4096;
+
+QMV_API size_t qmv_token_logprobs_workspace_bytes(int64_t n_tok, int64_t n_vocab, int64_t top_n) {
+  if (check_logprob_sizes(n_tok, n_vocab, top_n) != QMV_OK) return 0;
+  const int64_t slots = n_tok * logprob_parts(n_tok, n_vocab);
+  return slots == 0 ? 0 : static_cast<size_t>(kLogprobCounterBytes + align256(slots * (8 * kPartGroupsOfRow + 16)));
+}
+
+QMV_API qmv_status qmv_token_logprobs(const float* logits, int64_t ldl, int64_t n_tok, int64_t n_vocab, float scale,
+                                      const int32_t* given, int64_t n_given, float* logprobs, float* entropy,
+                                      int64_t top_n, int32_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  if (logits == nullptr || n_given < 0 || (n_given > 0 && (given == nullptr || logprobs == nullptr)) ||
+      (top_n > 0 && (top_ids == nullptr || top_logprobs == nullptr)) ||
+      (n_given == 0 && top_n == 0 && entropy == nullptr) || !(scale > 0.f) || !(scale < __builtin_inff()) ||
+      ldl < n_vocab)
+    return QMV_ERR_INVALID_ARG;
+  const qmv_status st = check_logprob_sizes(n_tok, n_vocab, top_n);
+  if (st != QMV_OK) return st;
+  if (n_given > QMV_MAX_GIVEN) return QMV_ERR_UNSUPPORTED;
+  if (!aligned(logits, 4) || !aligned(given, 4) || !aligned(logprobs, 4) || !aligned(entropy, 4) ||
+      !aligned(top_ids, 4) || !aligned(top_logprobs, 4) || !aligned(ws, 256))
+    return QMV_ERR_MISALIGNED;
+  LogprobArgs a{};
+  a.x = logits;
+  a.ldx = ldl;
+  a.n_tok = static_cast<int>(n_tok);
+  a.n_vocab = static_cast<int>(n_vocab);
+  a.scale = scale;
+  a.given = given;
+  a.n_given = static_cast<int>(n_given);
+  a.top_n = static_cast<int>(top_n);
+  a.logprobs = logprobs;
+  a.entropy = entropy;
+  a.ids = top_ids;
+  a.top = top_logprobs;
+  if (ws != nullptr) {
+    if (ws_bytes < qmv_token_logprobs_workspace_bytes(n_tok, n_vocab, top_n)) return QMV_ERR_WORKSPACE;
+    a.parts = logprob_parts(n_tok, n_vocab);
+    uint8_t* b = static_cast<uint8_t*>(ws) + kLogprobCounterBytes;
+    a.keys = reinterpret_cast<uint64_t*>(b);
+    a.sums = reinterpret_cast<float*>(b + n_tok * a.parts * 8 * kPartGroupsOfRow);
+  }
+  return hip_status(launch_token_logprobs(a, static_cast<hipStream_t>(stream)));
+}
+
 QMV_API qmv_status qmv_block_dots(qmv_type type, const void* w, int64_t n_rows, int64_t k,
                                   const void* xq, int64_t n_tok, int32_t* out, void* stream) {
   qmv_status st = check_weights(type, w, n_rows, k);

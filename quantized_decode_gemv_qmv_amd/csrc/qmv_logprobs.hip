@@ -1,0 +1,413 @@
+// qmv_logprobs.hip -- log probabilities of given tokens, entropy and the
+// likeliest alternatives of the output head's logits in one pass, for gfx950.
+//
+// A row's softmax needs its largest value m, s = sum e^d and u = sum e^d d with
+// d = scale x - scale m: log p = d - ln s, the entropy is ln s - u / s, whose
+// terms all have one sign.  Partial sums over parts of a row join by their
+// maxima.  The n largest come from the same pass: each group of elements gives
+// its largest, the n-th largest of 64 groups of groups is a bound that n
+// elements reach, and only groups whose largest reaches it are read again
+// (some tens, from the caches).
+#include "qmv_device.h"
+#include "qmv_steps.h"
+
+namespace qmv {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504f;
+constexpr int kRowThreads = 1024;  // of a workgroup that has a whole row, or joins one
+constexpr int kPartThreads = 256;
+constexpr int kPartVecs = 4;       // 16-byte vectors of a thread
+constexpr int kPartVec = kPartThreads * kPartVecs;  // vectors of a part
+constexpr int kPartGroups = kPartThreads / 16;      // groups of 16 lanes
+static_assert(kPartGroups == kPartGroupsOfRow, "the workspace holds a part's keys");
+constexpr int kList = 1024;        // candidates, and groups, that LDS lists
+
+// Order of logits as unsigned numbers: the larger value first, then the lower
+// index; NaN counts as -inf, -0 as +0.  0 is below every key.
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t index) {
+  if (!(v == v)) v = -__builtin_inff();
+  uint32_t b = __float_as_uint(v + 0.f);
+  b = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return ((uint64_t)b << 32) | (uint32_t)~index;
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t b = (uint32_t)(key >> 32);
+  return __uint_as_float((b & 0x80000000u) ? (b & 0x7FFFFFFFu) : ~b);
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
+  return ((uint64_t)(uint32_t)dpp_i<CTRL>((int)(uint32_t)(v >> 32)) << 32) | (uint32_t)dpp_i<CTRL>((int)(uint32_t)v);
+}
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
+// The largest of each 16 lanes, in all of them.
+__device__ __forceinline__ uint64_t row_max(uint64_t v) {
+  v = max_u64(v, dpp_u64<DPP_XOR1>(v));
+  v = max_u64(v, dpp_u64<DPP_XOR2>(v));
+  v = max_u64(v, dpp_u64<DPP_HALF_MIRROR>(v));
+  return max_u64(v, dpp_u64<DPP_MIRROR>(v));
+}
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
+  return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32) |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+  v = row_max(v);
+  return max_u64(max_u64(lane_u64(v, 0), lane_u64(v, 16)), max_u64(lane_u64(v, 32), lane_u64(v, 48)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = max8(v);
+  v = fmaxf(v, dpp_f<DPP_MIRROR>(v));
+  const int b = __float_as_int(v);
+  return fmaxf(fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 0)), __int_as_float(__builtin_amdgcn_readlane(b, 16))),
+               fmaxf(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __int_as_float(__builtin_amdgcn_readlane(b, 48))));
+}
+
+// m: largest logit times scale; s and u: sums relative to it.
+struct Sums {
+  float m, s, u;
+};
+
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+// The sums taken relative to m (which is not below their own).  A part with
+// nothing allowed has m -inf and sums of 0, which stay; NaN stays too.
+__device__ __forceinline__ void shift(Sums& a, float m) {
+  const float d = fmaxf(a.m - m, -1e4f);
+  const float f = exp_of(d);
+  a.u = f * fmaf(d, a.s, a.u);
+  a.s *= f;
+  a.m = m;
+}
+
+// Adds one vector's elements to sums relative to ref (finite).
+__device__ __forceinline__ void add(float& s, float& u, const f32x4& v, float scale, float ref) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float d = fmaf(v[i], scale, -ref);
+    const float e = exp_of(d);
+    s += e;
+    u = fmaf(e, fmaxf(d, -1e4f), u);  // 0 for -inf
+  }
+}
+
+__device__ __forceinline__ float max4(const f32x4& v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
+
+// Vector i of a row: elements past its end are -inf.
+__device__ __forceinline__ f32x4 load_vec(const float* row, int64_t i, int n) {
+  if (4 * i + 4 <= n) return *reinterpret_cast<const f32x4*>(row + 4 * i);
+  f32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = 4 * i + j < n ? row[4 * i + j] : -__builtin_inff();
+  return v;
+}
+
+// Joins the sums of a wave's lanes, then of a workgroup's waves, in all threads.
+template <int THREADS>
+__device__ __forceinline__ Sums block_join(Sums a, Sums* tmp) {
+  const float m = wave_max(a.m);
+  shift(a, m);
+  a.s = wave_sum(a.s);
+  a.u = wave_sum(a.u);
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = a;
+  __syncthreads();
+  Sums r = tmp[0];
+  float top = r.m;
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) top = fmaxf(top, tmp[w].m);
+  shift(r, top);
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) {
+    Sums o = tmp[w];
+    shift(o, top);
+    r.s += o.s;
+    r.u += o.u;
+  }
+  return r;
+}
+
+__device__ __forceinline__ float log_prob(float x, float scale, const Sums& a, double log_s) {
+  if (a.m == -__builtin_inff() && a.s == 0.f) return -__builtin_inff();  // nothing is allowed
+  return (float)(((double)x * (double)scale - (double)a.m) - log_s);
+}
+
+// Entropy and the given tokens' log probabilities of row t.
+__device__ __forceinline__ void put_given(const LogprobArgs& a, int t, const float* row, const Sums& r, double log_s) {
+  if (threadIdx.x == 0 && a.entropy != nullptr) {
+    const bool none = r.m == -__builtin_inff() && r.s == 0.f;
+    a.entropy[t] = none ? 0.f : (float)(log_s - (double)r.u / (double)r.s);
+  }
+  for (int g = threadIdx.x; g < a.n_given; g += kRowThreads) {
+    const int64_t at = (int64_t)t * a.n_given + g;
+    const int id = a.given[at];
+    a.logprobs[at] = id < 0 || id >= a.n_vocab ? (r.s == r.s ? -__builtin_inff() : r.s)
+                                               : log_prob(row[id], a.scale, r, log_s);
+  }
+}
+
+struct TopShared {
+  uint64_t coarse[64];
+  uint64_t key[kList];
+  uint32_t group[kList];
+  uint64_t wave[kRowThreads / 64];
+  int groups, keys;
+};
+
+// The n-th largest of 64 keys, one a lane (0 where fewer are above 0), in every
+// lane alike.
+__device__ __forceinline__ uint64_t nth_of_wave(uint64_t key, int n) {
+  int larger = 0;  // keys above 0 are all different
+#pragma unroll 8
+  for (int j = 0; j < 64; ++j) larger += lane_u64(key, j) > key ? 1 : 0;
+  const uint64_t b = __ballot(larger == n - 1 && key != 0);
+  return b == 0 ? 0 : lane_u64(key, __ffsll((unsigned long long)b) - 1);
+}
+
+// The n largest of a row by the 1024 threads that hold its groups' largest keys
+// (mine: the largest of this thread's groups).  each(f) calls f(key, group) for
+// the thread's groups; vec(group, i), i < items, are a group's vectors.  A
+// group's key is its largest value's, with the last index of the vector where
+// that value first stands.
+template <class Each, class Vec>
+__device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sums& r, double log_s, uint64_t mine,
+                        int items, TopShared& sh, Each each, Vec vec) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.top_n;
+  auto bound = [&](uint64_t k) {  // of 64 groups of threads
+    k = row_max(k);
+    if ((tid & 15) == 0) sh.coarse[tid >> 4] = k;
+    if (tid == 0) sh.groups = sh.keys = 0;
+    __syncthreads();
+    return nth_of_wave(sh.coarse[lane], n);
+  };
+  uint64_t least = bound(mine);
+  each([&](uint64_t k, uint32_t g) {
+    if (k != 0 && k >= least) {
+      const int at = atomicAdd(&sh.groups, 1);
+      if (at < kList) sh.group[at] = g;
+    }
+  });
+  __syncthreads();
+  const bool listed = sh.groups <= kList;
+  // all vectors that may hold one: of the listed groups, or of the row
+  const int64_t count = listed ? (int64_t)sh.groups * items : (a.n_vocab + 3) / 4;
+  const int n_groups = sh.groups;
+  auto scan = [&](auto f) {
+    for (int64_t q = tid; q < count; q += kRowThreads) {
+      int64_t i = q;
+      if (listed) i = vec(sh.group[q % n_groups], (int)(q / n_groups));
+      if (4 * i >= a.n_vocab) continue;
+      const f32x4 v = load_vec(row, i, a.n_vocab);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (4 * i + j < a.n_vocab) f(key_of(v[j], (uint32_t)(4 * i + j)));
+    }
+  };
+  uint64_t top = 0;
+  scan([&](uint64_t k) {
+    if (k >= least) {
+      top = max_u64(top, k);
+      const int at = atomicAdd(&sh.keys, 1);
+      if (at < kList) sh.key[at] = k;
+    }
+  });
+  __syncthreads();
+  if (sh.keys > kList) {  // once more with the bound that these themselves give
+    __syncthreads();
+    least = max_u64(least, bound(top));
+    scan([&](uint64_t k) {
+      if (k >= least) {
+        const int at = atomicAdd(&sh.keys, 1);
+        if (at < kList) sh.key[at] = k;
+      }
+    });
+    __syncthreads();
+  }
+  const int c = sh.keys;
+  auto put = [&](int j, uint64_t k) {
+    a.ids[(int64_t)t * n + j] = (int)~(uint32_t)k;
+    a.top[(int64_t)t * n + j] = log_prob(value_of(k), a.scale, r, log_s);
+  };
+  if (c <= 128) {  // each one's place is the number of larger ones
+    if (tid < c) {
+      const uint64_t k = sh.key[tid];
+      int larger = 0;
+      for (int j = 0; j < c; ++j) larger += sh.key[j] > k ? 1 : 0;
+      if (larger < n) put(larger, k);
+    }
+  } else if (c <= kList) {  // one after the other, by one wave
+    if (wave == 0) {
+      uint64_t k[kList / 64];
+#pragma unroll
+      for (int i = 0; i < kList / 64; ++i) k[i] = lane + 64 * i < c ? sh.key[lane + 64 * i] : 0;
+      uint64_t last = ~0ull;
+      for (int j = 0; j < n; ++j) {
+        uint64_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kList / 64; ++i) best = k[i] < last ? max_u64(best, k[i]) : best;
+        last = wave_max(best);
+        if (lane == 0) put(j, last);
+      }
+    }
+  } else {  // too many that the bounds cannot tell apart: a scan for each
+    uint64_t last = ~0ull;
+    for (int j = 0; j < n; ++j) {
+      uint64_t best = 0;
+      scan([&](uint64_t k) { best = k < last ? max_u64(best, k) : best; });
+      best = wave_max(best);
+      __syncthreads();
+      if (lane == 0) sh.wave[wave] = best;
+      __syncthreads();
+      best = sh.wave[lane & 15];
+      last = row_max(best);
+      if (tid == 0) put(j, last);
+    }
+  }
+}
+
+}  // namespace
+
+// A whole row by one workgroup: each thread keeps sums relative to its own
+// largest, four vectors a step.
+__global__ __launch_bounds__(kRowThreads) void k_logprob_row(LogprobArgs a) {
+  __shared__ Sums tmp[kRowThreads / 64];
+  __shared__ TopShared sh;
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const float* row = a.x + t * a.ldx;
+  const int vecs = (a.n_vocab + 3) / 4;
+  float top = -__builtin_inff();
+  int at = tid;
+  Sums r{-__builtin_inff(), 0.f, 0.f};
+  constexpr int B = 4;
+  for (int i0 = tid; i0 < vecs; i0 += B * kRowThreads) {
+    f32x4 v[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = i0 + b * kRowThreads;
+      v[b] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+      if (i < vecs) v[b] = load_vec(row, i, a.n_vocab);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const float m = max4(v[b]);
+      if (m > top) {
+        top = m;
+        at = i0 + b * kRowThreads;
+      }
+    }
+    const float m = top * a.scale;
+    shift(r, m);
+    const float ref = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+    for (int b = 0; b < B; ++b) add(r.s, r.u, v[b], a.scale, ref);
+  }
+  r = block_join<kRowThreads>(r, tmp);
+  const double log_s = log((double)r.s);
+  put_given(a, t, row, r, log_s);
+  if (a.top_n > 0) {
+    const uint64_t key = tid < vecs ? key_of(top, (uint32_t)(4 * at + 3)) : 0;
+    put_top(a, t, row, r, log_s, key, (vecs + kRowThreads - 1) / kRowThreads, sh,
+            [&](auto f) { f(key, (uint32_t)tid); },
+            [](uint32_t g, int i) { return (int64_t)g + (int64_t)i * kRowThreads; });
+  }
+}
+
+// One part of a row, held in registers: its sums and the largest of each 16
+// lanes' 64 vectors.
+__global__ __launch_bounds__(kPartThreads) void k_logprob_part(LogprobArgs a) {
+  __shared__ Sums tmp[kPartThreads / 64];
+  const int t = blockIdx.y, p = blockIdx.x, tid = threadIdx.x;
+  const float* row = a.x + t * a.ldx;
+  const int vecs = (a.n_vocab + 3) / 4, i0 = p * kPartVec + tid;
+  f32x4 v[kPartVecs];
+#pragma unroll
+  for (int b = 0; b < kPartVecs; ++b) {
+    const int i = i0 + b * kPartThreads;
+    v[b] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+    if (i < vecs) v[b] = load_vec(row, i, a.n_vocab);
+  }
+  float top = -__builtin_inff();
+  int at = i0;
+#pragma unroll
+  for (int b = 0; b < kPartVecs; ++b) {
+    const float m = max4(v[b]);
+    if (m > top) {
+      top = m;
+      at = i0 + b * kPartThreads;
+    }
+  }
+  const float m = wave_max(top) * a.scale;
+  const float ref = m == -__builtin_inff() ? 0.f : m;
+  Sums r{m, 0.f, 0.f};
+#pragma unroll
+  for (int b = 0; b < kPartVecs; ++b) add(r.s, r.u, v[b], a.scale, ref);
+  const int64_t slot = (int64_t)t * a.parts + p;
+  if (a.top_n > 0) {
+    const uint64_t key = row_max(i0 < vecs ? key_of(top, (uint32_t)(4 * at + 3)) : 0);
+    if ((tid & 15) == 0) a.keys[slot * kPartGroups + (tid >> 4)] = key;
+  }
+  r = block_join<kPartThreads>(r, tmp);
+  if (tid == 0) {
+    float* o = a.sums + 4 * slot;
+    o[0] = r.m;
+    o[1] = r.s;
+    o[2] = r.u;
+  }
+}
+
+// Joins a row's parts.
+__global__ __launch_bounds__(kRowThreads) void k_logprob_join(LogprobArgs a) {
+  __shared__ Sums tmp[kRowThreads / 64];
+  __shared__ TopShared sh;
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const float* row = a.x + t * a.ldx;
+  Sums r{-__builtin_inff(), 0.f, 0.f};
+  for (int p = tid; p < a.parts; p += kRowThreads) {
+    const float* o = a.sums + 4 * ((int64_t)t * a.parts + p);
+    Sums q{o[0], o[1], o[2]};
+    const float m = fmaxf(q.m, r.m);
+    shift(q, m);
+    shift(r, m);
+    r.s += q.s;
+    r.u += q.u;
+  }
+  r = block_join<kRowThreads>(r, tmp);
+  const double log_s = log((double)r.s);
+  put_given(a, t, row, r, log_s);
+  if (a.top_n > 0) {
+    const uint64_t* keys = a.keys + (int64_t)t * a.parts * kPartGroups;
+    const int groups = a.parts * kPartGroups;
+    uint64_t mine = 0;
+    for (int g = tid; g < groups; g += kRowThreads) mine = max_u64(mine, keys[g]);
+    put_top(a, t, row, r, log_s, mine, kPartVecs * 16, sh,
+            [&](auto f) {
+              for (int g = tid; g < groups; g += kRowThreads) f(keys[g], (uint32_t)g);
+            },
+            [](uint32_t g, int i) {
+              return (int64_t)(g / kPartGroups) * kPartVec + (i >> 4) * kPartThreads + (g % kPartGroups) * 16 +
+                     (i & 15);
+            });
+  }
+}
+
+// Rows are shared by workgroups where whole rows would leave compute units idle.
+int logprob_parts(int64_t n_tok, int64_t n_vocab) {
+  const int64_t parts = (n_vocab + 4 * kPartVec - 1) / (4 * kPartVec);
+  return n_tok <= 256 && parts >= 3 ? (int)parts : 0;
+}
+
+hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st) {
+  if (a.parts == 0) {
+    hipLaunchKernelGGL(k_logprob_row, dim3((unsigned)a.n_tok), dim3(kRowThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_logprob_part, dim3((unsigned)a.parts, (unsigned)a.n_tok), dim3(kPartThreads), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_logprob_join, dim3((unsigned)a.n_tok), dim3(kRowThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace qmv

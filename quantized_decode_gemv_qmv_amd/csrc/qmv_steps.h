@@ -58,4 +58,46 @@ constexpr int kLoraMaxSlices = 16;
 int lora_slices(int64_t n_items, int64_t max_rank, int64_t n_tok);
 hipError_t launch_lora(int type, LoraArgs a, hipStream_t st);
 
+// Routing to experts.
+struct GateArgs {
+  const float* x;  // [n_tok][ldx]
+  int64_t ldx;
+  const float* wr;  // [n_experts][k]
+  int n_tok, k, n_experts, top_k;
+  int sigmoid;         // 1: sigmoid scores, 0: softmax
+  const float* bias;   // NULL, or [n_experts]
+  int groups, top_groups, group_best;
+  int renorm;
+  float scale;
+  int32_t* ids;       // [n_tok][top_k]
+  float* weights;     // [n_tok][top_k]
+  float* logits_out;  // NULL, or [n_tok][n_experts]
+  int8_t* qs;         // NULL, or the Q8 blocks of x
+  float* qd;
+  int32_t* qsum;
+  double* logits;  // [n_tok][n_experts]
+};
+hipError_t launch_router_gate(const GateArgs& a, hipStream_t st);
+
+// Log probabilities of a row of logits.
+constexpr int kPartGroupsOfRow = 16;  // keys of a part
+struct LogprobArgs {
+  const float* x;  // [n_tok][ldx]
+  int64_t ldx;
+  int n_tok, n_vocab;
+  float scale;
+  const int32_t* given;  // [n_tok][n_given]
+  int n_given, top_n;
+  float* logprobs;  // [n_tok][n_given]
+  float* entropy;   // NULL, or [n_tok]
+  int32_t* ids;     // [n_tok][top_n]
+  float* top;       // [n_tok][top_n]
+  int parts;        // of a row, 0: whole rows
+  float* sums;      // [n_tok][parts][4]
+  uint64_t* keys;   // [n_tok][parts][kPartGroupsOfRow]
+};
+// Parts of a row that a call with a workspace makes; 0: none.
+int logprob_parts(int64_t n_tok, int64_t n_vocab);
+hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st);
+
 }  // namespace qmv

@@ -1,0 +1,209 @@
+"""Log probabilities, entropy and alternatives against the formula in 64 bits.
+
+Ids are equal.  Tolerances in half steps u = 2^-24: e^d has d (rounded once, |d| u)
+times log2 e (rounded twice) and the hardware's exponential (2 u): (3 |d| + 3) u
+of itself, which is (3 mean|d| + 3) u of the sum, mean|d| under the
+probabilities being at most ln V < 17.  All terms of the sums have one sign; a
+lane adds at most V / 1024 + 16 terms in turn, rescales (3 roundings) at most
+every 16 of them, and joins 16 times: the sums are off by
+N = V / 1024 * 1.2 + 140 half steps of themselves.  A log probability is off by N u and
+its own rounding, the entropy by 2 N u (1 + entropy)."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import gpu, need_gpu, say
+
+pytestmark = gpu
+
+U = 2.0 ** -24
+
+
+def reference(x, given, n, scale):
+    z = x.astype(np.float64) * float(np.float32(scale))
+    m = z.max(1, keepdims=True)
+    m[m == -np.inf] = 0.0
+    p = np.exp(z - m)
+    s = p.sum(1, keepdims=True)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        lp = z - m - np.log(s)
+        lp[z == -np.inf] = -np.inf
+        p = p / s
+        ent = -np.where(p > 0, p * lp, 0.0).sum(1)
+    ent[s[:, 0] == 0] = 0.0
+    out = None
+    if given is not None:
+        ok = (given >= 0) & (given < x.shape[1])
+        out = np.where(ok, np.take_along_axis(lp, np.where(ok, given, 0), 1), -np.inf)
+    order = np.argsort(-(x.astype(np.float64)), axis=1, kind="stable")[:, :n]
+    return out, ent, order.astype(np.int32), np.take_along_axis(lp, order, 1)
+
+
+def close(got, want, tol):
+    got = got.cpu().numpy().astype(np.float64)
+    fin = np.isfinite(want)
+    assert np.array_equal(got[~fin], want[~fin])
+    err = np.abs(got - np.where(fin, want, 0))[fin]
+    lim = (tol + U * np.abs(want))[fin] if np.ndim(tol) == 0 else tol[fin]
+    assert np.all(err <= lim), (float(err.max()), float(lim.min()))
+
+
+def check(qmv, x, given=None, n=0, scale=1.0, pad=0, ws="both"):
+    t, v = x.shape
+    say(f"logprobs T {t} V {v} given {None if given is None else given.shape} top {n} scale {scale} pad {pad}")
+    dx = torch.full((t, v + pad), float("nan"), device="cuda")[:, :v]
+    dx.copy_(torch.from_numpy(x))
+    dg = None if given is None else torch.from_numpy(given.astype(np.int32)).cuda()
+    want = reference(x, given, n, scale)
+    size = 1.2 * v / 1024 + 140
+    for with_ws in (False, True):
+        need = qmv.token_logprobs_workspace_bytes(t, v, n)
+        buf = torch.zeros(need, dtype=torch.uint8, device="cuda") if with_ws else None
+        if with_ws and need == 0:
+            continue
+        lp, ent, ids, top = qmv.token_logprobs(dx, dg, top_n=n, scale=scale, ws=buf)
+        torch.cuda.synchronize()
+        if given is not None:
+            close(lp, want[0], size * U)
+        close(ent, want[1], 2 * size * U * (1 + want[1]))
+        if n:
+            assert np.array_equal(ids.cpu().numpy(), want[2])
+            close(top, want[3], size * U)
+        else:
+            assert ids is None and top is None
+        if with_ws:
+            assert not buf[:4096].any()
+
+
+def make(t, v, seed=0, spread=3.0):
+    rng = np.random.default_rng(seed + 31 * t + v)
+    return (rng.standard_normal((t, v)) * spread).astype(np.float32), rng
+
+
+@pytest.mark.parametrize("v", [1, 2, 3, 4, 5, 63, 100, 255, 1000, 1024, 1100, 4095, 4097, 8191, 8193, 12289, 20000, 32003, 50257,
+                               152064])
+def test_vocabularies(v):
+    qmv = need_gpu()
+    x, rng = make(3, v)
+    check(qmv, x, rng.integers(0, v, (3, 2)), min(20, v))
+    check(qmv, x, rng.integers(-2, v + 2, (3, 1)), min(1, v), scale=0.7, pad=3)
+    check(qmv, x, None, min(32, v), pad=1)
+    check(qmv, x, rng.integers(0, v, (3, 1)), 0)
+
+
+@pytest.mark.parametrize("t", [1, 2, 16, 64, 256, 257, 700])
+def test_rows(t):
+    qmv = need_gpu()
+    x, rng = make(t, 20011)
+    check(qmv, x, rng.integers(0, 20011, (t, 3)), 7, scale=1.25)
+
+
+@pytest.mark.parametrize("v", [300, 5000, 60000])
+def test_ties(v):
+    """Few different values: the lower index first, also where all are equal or zeros differ in sign."""
+    qmv = need_gpu()
+    rng = np.random.default_rng(v)
+    x = rng.integers(-2, 3, (4, v)).astype(np.float32)
+    x[1] = 1.5
+    x[2] = np.where(rng.random(v) < 0.5, 0.0, -0.0)
+    x[3, :] = np.floor(np.arange(v) / 50)
+    check(qmv, x, rng.integers(0, v, (4, 1)), 32)
+
+
+@pytest.mark.parametrize("v", [5000, 70001, 152064])
+def test_sorted_rows(v):
+    """The largest lie side by side, at the end, at the start, in one stride."""
+    qmv = need_gpu()
+    x = np.stack([np.linspace(-9, 9, v), np.linspace(9, -9, v), np.linspace(-1, 1, v) ** 2 * 20,
+                  np.where(np.arange(v) % 1024 == 7, 5 + np.arange(v) / v, np.arange(v) / v)]).astype(np.float32)
+    check(qmv, x, np.zeros((4, 1), np.int64), 32)
+
+
+@pytest.mark.parametrize("v", [400, 9000, 100003])
+def test_forbidden_tokens(v):
+    qmv = need_gpu()
+    x, rng = make(6, v)
+    x[rng.random(x.shape) < 0.5] = -np.inf
+    x[1] = -np.inf
+    x[1, v // 2] = -3.0
+    x[2] = -np.inf  # nothing is left
+    x[3, : v - 5] = -np.inf
+    x[4, 5:] = -np.inf
+    given = rng.integers(0, v, (6, 4))
+    given[1, 0] = v // 2
+    given[:, 3] = -1
+    check(qmv, x, given, 20)
+
+
+def test_wide_ranges():
+    """Logits so far apart that one token has it all, and large ones of both signs."""
+    qmv = need_gpu()
+    x, rng = make(4, 30000)
+    x[0] *= 1e30
+    x[1] += 1e6
+    x[2] -= 1e6
+    x[3, 77] = 3e38
+    check(qmv, x, rng.integers(0, 30000, (4, 2)), 5)
+
+
+def test_no_numbers():
+    qmv = need_gpu()
+    for v in (900, 40000):
+        x, _ = make(5, v)
+        x[0, 17], x[1, 30], x[2, :] = np.nan, np.inf, np.nan
+        x[3, 40:60] = np.nan
+        dx = torch.from_numpy(x).cuda()
+        given = torch.full((5,), 3, dtype=torch.int32, device="cuda")
+        for need in (0, qmv.token_logprobs_workspace_bytes(5, v, 4)):
+            ws = torch.zeros(need, dtype=torch.uint8, device="cuda") if need else None
+            lp, ent, ids, top = qmv.token_logprobs(dx, given, top_n=4, ws=ws)
+            assert torch.isnan(lp[:4]).all() and torch.isnan(ent[:4]).all() and torch.isnan(top[:4]).all()
+            assert torch.isfinite(lp[4]) and torch.isfinite(ent[4]) and torch.isfinite(top[4]).all()
+            order = np.argsort(-np.where(np.isnan(x), -np.inf, x.astype(np.float64)), axis=1, kind="stable")[:, :4]
+            assert np.array_equal(ids.cpu().numpy(), order)
+
+
+def test_rows_beyond_32_bits():
+    """Rows whose offsets pass 2^31 elements."""
+    qmv = need_gpu()
+    t, ld = 3, (1 << 30) + 4
+    base = torch.empty((t - 1) * ld + 5000, device="cuda")
+    x = base.as_strided((t, 5000), (ld, 1))
+    x.normal_()
+    lp, ent, ids, top = qmv.token_logprobs(x, torch.zeros(t, 1, dtype=torch.int32, device="cuda"), top_n=3)
+    want = reference(x.cpu().numpy(), np.zeros((t, 1), np.int64), 3, 1.0)
+    assert np.array_equal(ids.cpu().numpy(), want[2])
+    close(lp, want[0], 200 * U)
+
+
+def test_graphs_streams_and_one_workspace():
+    qmv = need_gpu()
+    t, v = 6, 50257
+    x = torch.randn(t, v, device="cuda") * 3
+    given = torch.randint(0, v, (t, 1), dtype=torch.int32, device="cuda")
+    ws = torch.zeros(qmv.token_logprobs_workspace_bytes(t, v, 20), dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for n_tok, n in ((t, 20), (2, 3)):
+        o = (torch.empty(n_tok, 1, device="cuda"), torch.empty(n_tok, device="cuda"),
+             torch.empty(n_tok, n, dtype=torch.int32, device="cuda"), torch.empty(n_tok, n, device="cuda"))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qmv.token_logprobs(x[:n_tok], given[:n_tok], top_n=n, logprobs=o[0], entropy=o[1], top_ids=o[2],
+                               top_logprobs=o[3], ws=ws)
+        outs.append(o)
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    for rep in range(8):
+        x.normal_()
+        given.random_(0, v)
+        i = rep % 2
+        n_tok, n = outs[i][2].shape
+        other = torch.zeros_like(ws)
+        want = qmv.token_logprobs(x[:n_tok], given[:n_tok], top_n=n, ws=other)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want)), rep
+        again = qmv.token_logprobs(x[:n_tok], given[:n_tok], top_n=n, ws=other, stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(again, want)), rep
+    assert not ws[:4096].any()

@@ -90,3 +90,80 @@ def test_lora_workspace_and_binding():
                   [(a.long(), b, None, None)]):
         with pytest.raises(ValueError):
             q.lora(x, ids, items)
+
+
+def gate(**kw):
+    a = dict(scoring=0, bias=None, groups=4, top_groups=2, best=2, renorm=1, scale=1.0, x=FAKE, ldx=64, t=3, k=64,
+             w=FAKE, e=32, top_k=8, gate=1, ids=FAKE, weights=FAKE, logits=None, xq=None, ws=FAKE, wsb=1 << 30)
+    a.update(kw)
+    g = q._Gate(a["scoring"], a["bias"], a["groups"], a["top_groups"], a["best"], a["renorm"], a["scale"])
+    return q.lib().qmv_router_gate(a["x"], a["ldx"], a["t"], a["k"], a["w"], a["e"], a["top_k"],
+                                   ctypes.byref(g) if a["gate"] else None, a["ids"], a["weights"], a["logits"],
+                                   a["xq"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(gate=None), INVALID), (dict(ids=None), INVALID),
+    (dict(weights=None), INVALID), (dict(ws=None), INVALID), (dict(t=0), INVALID), (dict(k=0), INVALID),
+    (dict(k=62), INVALID), (dict(ldx=60), INVALID), (dict(ldx=66), INVALID), (dict(e=0), INVALID),
+    (dict(top_k=0), INVALID), (dict(top_k=17), INVALID), (dict(top_k=33, groups=1, top_groups=1), INVALID),
+    (dict(xq=FAKE, k=36, ldx=36), INVALID), (dict(scoring=2), INVALID), (dict(scoring=-1), INVALID),
+    (dict(renorm=2), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(groups=0), INVALID),
+    (dict(groups=5), INVALID), (dict(groups=-4), INVALID), (dict(top_groups=0), INVALID), (dict(top_groups=5), INVALID),
+    (dict(best=0), INVALID), (dict(best=3), INVALID), (dict(groups=32, top_groups=32), INVALID),
+    (dict(t=65), UNSUPPORTED), (dict(k=(1 << 24) + 4, ldx=1 << 25), UNSUPPORTED),
+    (dict(e=1028), UNSUPPORTED), (dict(top_k=17, groups=1, top_groups=1), UNSUPPORTED),
+    (dict(e=130, groups=65, top_groups=65), UNSUPPORTED),
+    (dict(x=FAKE + 4), MISALIGNED), (dict(w=FAKE + 8), MISALIGNED), (dict(bias=FAKE + 2), MISALIGNED),
+    (dict(ids=FAKE + 1), MISALIGNED), (dict(weights=FAKE + 2), MISALIGNED), (dict(logits=FAKE + 2), MISALIGNED),
+    (dict(xq=FAKE + 64), MISALIGNED), (dict(ws=FAKE + 128), MISALIGNED), (dict(wsb=1023), WORKSPACE),
+    (dict(wsb=0), WORKSPACE)])
+def test_gate_refusals(change, status):
+    assert gate(**change) == status
+
+
+def test_gate_workspace_and_binding():
+    f = q.router_gate_workspace_bytes
+    assert f(3, 32) == 1024 and f(64, 1024) >= 64 * 1024 * 8
+    for bad in ((0, 32), (65, 32), (1, 0), (1, 1025)):
+        assert f(*bad) == 0, bad
+    x, w = torch.zeros(2, 64), torch.zeros(8, 64)
+    for call in (lambda: q.router_gate(x, w, 2), lambda: q.router_gate(x, w[:, :32], 2),
+                 lambda: q.router_gate(x, w, 2, scoring="max")):
+        with pytest.raises(ValueError):
+            call()
+
+
+def logprobs(**kw):
+    a = dict(x=FAKE, ld=1000, t=3, v=1000, scale=1.0, given=FAKE, n=1, lp=FAKE, ent=FAKE, top=5, ids=FAKE, tl=FAKE,
+             ws=None, wsb=0)
+    a.update(kw)
+    return q.lib().qmv_token_logprobs(a["x"], a["ld"], a["t"], a["v"], a["scale"], a["given"], a["n"], a["lp"],
+                                      a["ent"], a["top"], a["ids"], a["tl"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), INVALID), (dict(given=None), INVALID), (dict(lp=None), INVALID), (dict(ids=None), INVALID),
+    (dict(tl=None), INVALID), (dict(n=-1), INVALID), (dict(n=0, top=0, ent=None), INVALID), (dict(scale=0.0), INVALID),
+    (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(ld=999), INVALID),
+    (dict(t=0), INVALID), (dict(v=0), INVALID), (dict(top=-1), INVALID), (dict(top=11, v=10), INVALID),
+    (dict(t=65537), UNSUPPORTED), (dict(v=(1 << 24) + 1, ld=1 << 25), UNSUPPORTED), (dict(top=33), UNSUPPORTED),
+    (dict(n=65537), UNSUPPORTED),
+    (dict(x=FAKE + 2), MISALIGNED), (dict(given=FAKE + 1), MISALIGNED), (dict(lp=FAKE + 2), MISALIGNED),
+    (dict(ent=FAKE + 3), MISALIGNED), (dict(ids=FAKE + 2), MISALIGNED), (dict(tl=FAKE + 1), MISALIGNED),
+    (dict(ws=FAKE + 64, wsb=1 << 30), MISALIGNED), (dict(ws=FAKE, wsb=100, v=100000, ld=100000), WORKSPACE)])
+def test_logprob_refusals(change, status):
+    assert logprobs(**change) == status
+
+
+def test_logprob_workspace_and_binding():
+    f = q.token_logprobs_workspace_bytes
+    assert f(1, 152064, 20) > 4096 and f(5000, 152064, 20) == 0 and f(1, 100, 20) == 0
+    for bad in ((0, 152064, 0), (1, 0, 0), (1, 152064, -1), (1, 152064, 33), (65537, 152064, 0), (1, (1 << 24) + 1, 0)):
+        assert f(*bad) == 0, bad
+    x = torch.zeros(2, 64)
+    g = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: q.token_logprobs(x), lambda: q.token_logprobs(x, g[:1]),
+                 lambda: q.token_logprobs(x, logprobs=torch.zeros(2)), lambda: q.token_logprobs(x, top_ids=g)):
+        with pytest.raises(ValueError):
+            call()

@@ -15,68 +15,75 @@ namespace qmv {
 
 namespace {
 
-constexpr int kTile = 8;      // tokens of a tile
-constexpr int kDownWaves = 4;
-constexpr int kDownRows = 4;  // of A in a workgroup
-constexpr int kChunk = 512;   // columns of a wave's step: 8 a lane
-constexpr int kUpThreads = 256;
+constexpr int kTile = 4;       // tokens of a tile
+constexpr int kWaves = 4;      // of a workgroup
+constexpr int kDownRows = 4;   // of A in a wave
+constexpr int kChunk = 512;    // columns of a wave's step: 8 a lane
+constexpr int kUpThreads = 64 * kWaves;
+constexpr int64_t kDownTarget = 512, kUpTarget = 1024;
+constexpr int kUpAhead = 4;    // steps of rows whose loads are in flight
 
-// Eight neighbouring weights as fp32.
+// Eight neighbouring weights as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load8(const void* base, int64_t at, float (&o)[8]) {
-  if constexpr (DT == kF32) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at);
-    const f32x4 u = p[0], v = p[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = u[i];
-      o[4 + i] = v[i];
-    }
-  } else {
-    const u32x4 u = ld16(static_cast<const uint16_t*>(base) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == kF16) {
-        o[2 * i] = half_bits_to_float(u[i]);
-        o[2 * i + 1] = half_bits_to_float(u[i] >> 16);
-      } else {
-        o[2 * i] = __uint_as_float(u[i] << 16);
-        o[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      }
+struct Raw8 {
+  u32x4 v[DT == kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    if constexpr (DT == kF32) {
+      v[0] = ld16(static_cast<const float*>(base) + at);
+      v[1] = ld16(static_cast<const float*>(base) + at + 4);
+    } else {
+      v[0] = ld16(static_cast<const uint16_t*>(base) + at);
     }
   }
-}
-
-struct Tile {
-  int n;         // tokens, 0: another workgroup has them
-  int adapter;   // -1: none
-  uint64_t left; // of the 64 tokens, this tile's
-  int base;      // the first of the 64
+  __device__ __forceinline__ void clear() {
+    v[0] = u32x4{0, 0, 0, 0};
+    if constexpr (DT == kF32) v[1] = u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (DT == kF32) return __uint_as_float(v[i / 4][i % 4]);
+    if constexpr (DT == kF16) return half_bits_to_float(v[0][i / 2] >> (16 * (i & 1)));
+    return __uint_as_float(i & 1 ? v[0][i / 2] & 0xFFFF0000u : v[0][i / 2] << 16);
+  }
 };
 
-// The tile of token t, in every wave alike.
-__device__ __forceinline__ Tile tile_of(const LoraArgs& a, int t) {
-  const int lane = threadIdx.x & 63, base = t & ~63;
-  int id = -2;
-  if (base + lane < a.n_tok) {
-    id = a.ids[base + lane];
-    if (id < 0 || id >= a.adapters) id = -1;
-  }
-  const int mine = __builtin_amdgcn_readlane(id, t & 63);
-  uint64_t m = __ballot(id == mine);
-  const int before = __popcll(m & ((1ull << (t & 63)) - 1));
-  Tile r{0, mine, 0, base};
-  if (before % kTile != 0) return r;
-  m &= ~0ull << (t & 63);
-  r.n = min(__popcll(m), kTile);
-  r.left = m;
+struct Tile {
+  int n;        // tokens, 0: another workgroup has them
+  int adapter;  // -1: none
+  int tokens;   // lane j: the j-th one
+  __device__ __forceinline__ int token(int j) const { return __builtin_amdgcn_readlane(tokens, min(j, n - 1)); }
+};
+
+// The tile that starts at token t, in every wave alike; id: the adapter of
+// token `lane` of t's 64.
+__device__ __forceinline__ Tile tile_of(int id, int t) {
+  const int lane = threadIdx.x & 63, at = t & 63;
+  Tile r;
+  r.adapter = __builtin_amdgcn_readlane(id, at);
+  uint64_t m = __ballot(id == r.adapter);
+  const int before = __popcll(m & ((1ull << at) - 1));
+  m &= ~0ull << at;
+  r.n = before % kTile == 0 ? min((int)__popcll(m), kTile) : 0;
+  // each of them writes its number to the lane of its place; the others go to
+  // the last lane, which is a place only if there are no others
+  const int place = (m >> lane) & 1 ? (int)__popcll(m & ((1ull << lane) - 1)) : 63;
+  r.tokens = __builtin_amdgcn_ds_permute(4 * place, (t & ~63) + lane);
   return r;
 }
 
-__device__ __forceinline__ int next_token(Tile& t) {
-  const int i = __ffsll((unsigned long long)t.left) - 1;
-  t.left &= t.left - 1;
-  return t.base + i;
+// The tokens that a slot looks at, one of each 16 of its 64: tiles of tokens
+// side by side begin 8 apart, those of tokens in turn at neighbours, and both
+// kinds fall on different slots.
+constexpr int kSlots = 16;
+__device__ __forceinline__ int slot_token(int slot, int q) {
+  return (slot / kSlots) * 64 + q * kSlots + ((slot - 3 * q) & (kSlots - 1));
+}
+
+// The adapters of t's 64 tokens, one a lane (-1: none, -2: past the end).
+__device__ __forceinline__ int ids_of(const LoraArgs& a, int t) {
+  const int i = (t & ~63) + (threadIdx.x & 63);
+  if (i >= a.n_tok) return -2;
+  const int id = a.ids[i];
+  return id < 0 || id >= a.adapters ? -1 : id;
 }
 
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
@@ -85,223 +92,312 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
   return max(0, min(a.ranks[adapter], a.max_rank));
 }
 
-// TG tokens (the first n count) by kDownRows rows of A over this wave's part
-// of a slice: the sums in lane row * TG + token.
+// TG tokens by kDownRows rows of A over the columns lo .. hi - 1: the sums in
+// lane row * TG + token.  All loads of a step are in flight together.
 template <int DT, int TG>
 __device__ __forceinline__ float down(const LoraArgs& a, const void* w, const int64_t (&row)[kDownRows],
-                                      const int (&tok)[kTile], int lo, int hi) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                                      const Tile& tile, int lo, int hi) {
+  constexpr int U = TG == 1 ? 2 : 1;  // steps whose loads are in flight
+  const int lane = threadIdx.x & 63;
   float acc[kDownRows * TG];
 #pragma unroll
   for (int i = 0; i < kDownRows * TG; ++i) acc[i] = 0.f;
-  for (int c = lo + kChunk * wave + 8 * lane; c < hi; c += kChunk * kDownWaves) {
-    float wv[kDownRows][8];
+  int64_t col[TG];
 #pragma unroll
-    for (int r = 0; r < kDownRows; ++r) load8<DT>(w, row[r] + c, wv[r]);
+  for (int j = 0; j < TG; ++j) col[j] = tile.token(j) * a.ldx;
+  for (int c0 = lo + 8 * lane; c0 < hi; c0 += U * kChunk) {
+    Raw8<DT> wv[U][kDownRows];
+    Raw8<kF32> xv[U][TG];
 #pragma unroll
-    for (int j = 0; j < TG; ++j) {
-      float xv[8];
-      load8<kF32>(a.x, tok[j] * a.ldx + c, xv);
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * kChunk;
+#pragma unroll
+      for (int r = 0; r < kDownRows; ++r) wv[u][r].clear();
+#pragma unroll
+      for (int j = 0; j < TG; ++j) xv[u][j].clear();
+      if (u == 0 || c < hi) {
+#pragma unroll
+        for (int r = 0; r < kDownRows; ++r) wv[u][r].load(w, row[r] + c);
+#pragma unroll
+        for (int j = 0; j < TG; ++j) xv[u][j].load(a.x, col[j] + c);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int r = 0; r < kDownRows; ++r)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[r * TG + j] = fmaf(wv[r][i], xv[i], acc[r * TG + j]);
-    }
+        for (int i = 0; i < 8; ++i) {
+          const float wf = wv[u][r].get(i);
+#pragma unroll
+          for (int j = 0; j < TG; ++j) acc[r * TG + j] = fmaf(wf, xv[u][j].get(i), acc[r * TG + j]);
+        }
   }
   return fold_all<kDownRows * TG>(acc, lane);
 }
 
 }  // namespace
 
-// h[slice][t][item][r] = sum over the slice's columns of A[r][c] x[t][c]:
-// workgroups along (item, rows), tokens and slices; four waves share a slice.
+// h[slice][t][item][r] = sum over the slice's columns of A[r][c] x[t][c]: a
+// wave for four rows, the workgroup's waves side by side over the same columns,
+// so that x comes from memory once for 16 rows.
 template <int DT>
-__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraArgs a) {
-  __shared__ float part[kDownWaves][kDownRows * kTile];
-  Tile tile = tile_of(a, blockIdx.y);
-  const int groups = (a.max_rank + kDownRows - 1) / kDownRows;
-  const int item = blockIdx.x / groups, r0 = (blockIdx.x % groups) * kDownRows;
-  const int rank = rank_of(a, tile.adapter);
-  if (tile.n == 0 || r0 >= rank) return;
-  int64_t row[kDownRows];
-#pragma unroll
-  for (int r = 0; r < kDownRows; ++r)  // rows past the rank repeat the last one
-    row[r] = ((int64_t)tile.adapter * a.max_rank + min(r0 + r, rank - 1)) * a.k;
-  int tok[kTile];
-#pragma unroll
-  for (int j = 0; j < kTile; ++j) tok[j] = j < tile.n ? next_token(tile) : tok[0];
-  const int lo = blockIdx.z * a.slice, hi = min(lo + a.slice, a.k);
-  const void* w = a.item[item].a;
+__global__ __launch_bounds__(64 * kWaves) void k_lora_down(LoraArgs a) {
+  const int groups = (a.max_rank + kDownRows * kWaves - 1) / (kDownRows * kWaves);
+  const int item = blockIdx.x / groups;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float s;
-  int tg;
-  if (tile.n == 1) {
-    tg = 1;
-    s = down<DT, 1>(a, w, row, tok, lo, hi);
-  } else if (tile.n == 2) {
-    tg = 2;
-    s = down<DT, 2>(a, w, row, tok, lo, hi);
-  } else if (tile.n <= 4) {
-    tg = 4;
-    s = down<DT, 4>(a, w, row, tok, lo, hi);
-  } else {
-    tg = 8;
-    s = down<DT, 8>(a, w, row, tok, lo, hi);
-  }
-  if (lane < kDownRows * tg) part[wave][lane] = s;
-  __syncthreads();
-  if (threadIdx.x < kDownRows * tg) {
-    float v = part[0][threadIdx.x];
+  const int r0 = (blockIdx.x % groups) * kDownRows * kWaves + __builtin_amdgcn_readfirstlane(wave) * kDownRows;
+  const int lo = blockIdx.z * a.slice, hi = min(lo + a.slice, a.k);
+  const int id = ids_of(a, slot_token(blockIdx.y, 0));
+  const void* w = a.item[item].a;
+  for (int q = 0; q < 64 / kSlots; ++q) {
+    const int t = slot_token(blockIdx.y, q);
+    if (t >= a.n_tok) continue;
+    const Tile tile = tile_of(id, t);
+    const int n = tile.n;
+    if (n == 0) continue;
+    const int rank = rank_of(a, tile.adapter);
+    if (r0 >= rank) continue;
+    int64_t row[kDownRows];
 #pragma unroll
-    for (int i = 1; i < kDownWaves; ++i) v += part[i][threadIdx.x];
-    const int r = r0 + threadIdx.x / tg, j = threadIdx.x % tg;
-    int t = tok[0];
-#pragma unroll
-    for (int i = 1; i < kTile; ++i) t = i == j ? tok[i] : t;
-    if (r < rank && j < tile.n)
-      a.h[(((int64_t)blockIdx.z * a.n_tok + t) * a.n_items + item) * a.max_rank + r] = v;
+    for (int r = 0; r < kDownRows; ++r)  // rows past the rank repeat the last one
+      row[r] = ((int64_t)tile.adapter * a.max_rank + min(r0 + r, rank - 1)) * a.k;
+    float s;
+    int tg;
+    if (n == 1) {
+      tg = 1;
+      s = down<DT, 1>(a, w, row, tile, lo, hi);
+    } else if (n == 2) {
+      tg = 2;
+      s = down<DT, 2>(a, w, row, tile, lo, hi);
+    } else {
+      tg = 4;
+      s = down<DT, 4>(a, w, row, tile, lo, hi);
+    }
+    const int r = r0 + lane / tg, j = lane % tg;
+    const int at = __shfl(tile.tokens, j);
+    if (lane < kDownRows * tg && r < rank && j < n)
+      a.h[(((int64_t)blockIdx.z * a.n_tok + at) * a.n_items + item) * a.max_rank + r] = s;
   }
 }
 
 namespace {
 
-template <int LPR>
-__device__ __forceinline__ float lanes_sum(float v) {
-  if constexpr (LPR >= 2) v += dpp_f<DPP_XOR1>(v);
-  if constexpr (LPR >= 4) v += dpp_f<DPP_XOR2>(v);
-  if constexpr (LPR >= 8) v += dpp_f<DPP_HALF_MIRROR>(v);
-  if constexpr (LPR >= 16) v += dpp_f<DPP_MIRROR>(v);
-  if constexpr (LPR >= 32) v += __shfl_xor(v, 16, 64);
-  return v;
+// The partner whose bit H differs: a mirror where no exchange of that distance
+// exists (every lane below that bit holds the same kind of value).
+template <int H>
+__device__ __forceinline__ float partner(float v) {
+  if constexpr (H == 1) return dpp_f<DPP_XOR1>(v);
+  if constexpr (H == 2) return dpp_f<DPP_XOR2>(v);
+  if constexpr (H == 4) return dpp_f<DPP_HALF_MIRROR>(v);
+  if constexpr (H == 8) return dpp_f<DPP_MIRROR>(v);
+  return __shfl_xor(v, H, 64);
 }
 
-// RPT rows a lane group, LPR lanes a row, TG tokens (the first n count).
-template <int DT, int LPR, int RPT, int TG>
-__device__ __forceinline__ void up(const LoraArgs& a, const LoraItem& it, const float* hs, int adapter, int rank,
-                                   int n, const int (&tok)[kTile], int n0) {
-  const int l = threadIdx.x % LPR, c = 8 * l;
-  const float scale = a.scales != nullptr ? a.scales[adapter] : 1.f;
+// Sums of N values over a lane group of 2 H lanes.  While a lane has several
+// values, it keeps one half of them and gives the other away; `at` counts up
+// the place of the first one that it keeps, `own` whether it is to store them.
+template <int H, int N>
+__device__ __forceinline__ void fold_group(float* v, int lane, int& at, bool& own) {
+  if constexpr (H >= 1) {
+    const bool hi = (lane & H) != 0;
+    if constexpr (N > 1) {
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const float send = hi ? v[j] : v[j + N / 2];
+        const float keep = hi ? v[j + N / 2] : v[j];
+        v[j] = keep + partner<H>(send);
+      }
+      at += hi ? N / 2 : 0;
+      fold_group<H / 2, N / 2>(v, lane, at, own);
+    } else {
+      v[0] += partner<H>(v[0]);
+      own = own && !hi;
+      fold_group<H / 2, 1>(v, lane, at, own);
+    }
+  }
+}
+
+// The outputs of a tile of at most TG tokens: steps of kUpThreads / LPR rows, LPR
+// lanes a row, TG tokens at once.  The weights and base of kUpAhead steps are
+// on their way while one is worked on.
+template <int DT, int LPR, int TG>
+__device__ __forceinline__ void up(const LoraArgs& a, const LoraItem& it, int m, const Tile& tile, int rank, float* hs,
+                                   int n0, int steps) {
+  constexpr int OWN = TG > LPR ? TG / LPR : 1;  // values that a lane stores
+  constexpr int kStep = kUpThreads / LPR;
+  const int l = threadIdx.x % LPR, row = n0 + (int)threadIdx.x / LPR;
+  int at = 0;
+  bool own = true;
+  {
+    float none[TG] = {};
+    fold_group<LPR / 2, TG>(none, l, at, own);
+  }
+  const char* wp = static_cast<const char*>(it.b) + (int64_t)tile.adapter * it.n * a.max_rank * (DT == kF32 ? 4 : 2);
+  const float* bp[OWN];
+  float* yp[OWN];
+  bool ok[OWN];
+#pragma unroll
+  for (int j = 0; j < OWN; ++j) {
+    const int t = __shfl(tile.tokens, min(at + j, tile.n - 1));
+    bp[j] = it.base + t * it.ldb;
+    yp[j] = it.y + t * it.ldy;
+    ok[j] = own && at + j < tile.n;
+  }
+  Raw8<DT> b[kUpAhead];
+  float base[kUpAhead][OWN];
+  auto fetch = [&](int s, Raw8<DT>& w, float (&v)[OWN]) {
+    const int r = row + s * kStep;
+    w.clear();
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) v[j] = 0.f;
+    if (s < steps && r < it.n) {
+      if (8 * l < rank) w.load(wp, (int64_t)r * a.max_rank + 8 * l);
+      if (it.base != nullptr) {
+#pragma unroll
+        for (int j = 0; j < OWN; ++j)
+          if (ok[j]) v[j] = bp[j][r];
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kUpAhead; ++i) fetch(i, b[i], base[i]);
+  const float scale = a.scales != nullptr ? a.scales[tile.adapter] : 1.f;
+  __syncthreads();  // the tile before is done with hs
+  // h: the slices' sums, eight loads in flight
+  const int64_t step = (int64_t)a.n_tok * a.n_items * a.max_rank;
+  for (int e = threadIdx.x; e < TG * 8 * LPR; e += kUpThreads) {
+    const int j = e / (8 * LPR), r = e % (8 * LPR);
+    float v = 0.f;
+    const int t = __shfl(tile.tokens, min(j, tile.n - 1));
+    if (r < rank && j < tile.n) {
+      const float* p = a.h + ((int64_t)t * a.n_items + m) * a.max_rank + r;
+      for (int z0 = 0; z0 < a.slices; z0 += 8) {
+        float u[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) u[z] = p[min(z0 + z, a.slices - 1) * step];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) v += z0 + z < a.slices ? u[z] : 0.f;
+      }
+    }
+    hs[e] = v;
+  }
+  __syncthreads();
   float h[TG][8];
 #pragma unroll
-  for (int j = 0; j < TG; ++j)
+  for (int j = 0; j < TG; ++j) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(hs + j * 8 * LPR + 8 * l);
+    const f32x4 u = p[0], v = p[1];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[j][i] = hs[j * 8 * LPR + c + i];
-  float b[RPT][8];
-#pragma unroll
-  for (int q = 0; q < RPT; ++q) {
-    const int r = min(n0 + q * (kUpThreads / LPR) + (int)threadIdx.x / LPR, it.n - 1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[q][i] = 0.f;
-    if (c < rank) load8<DT>(it.b, ((int64_t)adapter * it.n + r) * a.max_rank + c, b[q]);
-    // columns past the rank may hold anything
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[q][i] = c + i < rank ? b[q][i] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      h[j][i] = u[i];
+      h[j][4 + i] = v[i];
+    }
   }
+  for (int s0 = 0; s0 < steps; s0 += kUpAhead) {
 #pragma unroll
-  for (int q = 0; q < RPT; ++q) {
-    const int r = n0 + q * (kUpThreads / LPR) + (int)threadIdx.x / LPR;
-    const bool ok = r < it.n;
-    float base[TG], s[TG];
+    for (int i = 0; i < kUpAhead; ++i) {
+      if (s0 + i < steps) {  // uniform
+        const int r = row + (s0 + i) * kStep;
+        float s[TG];
 #pragma unroll
-    for (int j = 0; j < TG; ++j) {
-      base[j] = 0.f;
-      if (ok && j < n && j % LPR == l && it.base != nullptr) base[j] = it.base[tok[j] * it.ldb + r];
+        for (int j = 0; j < TG; ++j) s[j] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = 8 * l + e < rank ? b[i].get(e) : 0.f;  // columns past the rank may hold anything
+#pragma unroll
+          for (int j = 0; j < TG; ++j) s[j] = fmaf(w, h[j][e], s[j]);
+        }
+        int unused = 0;
+        bool skip = true;
+        fold_group<LPR / 2, TG>(s, l, unused, skip);
+        float y[OWN];
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) y[j] = fmaf(scale, s[j], base[i][j]);
+        fetch(s0 + i + kUpAhead, b[i], base[i]);
+#pragma unroll
+        for (int j = 0; j < OWN; ++j)
+          if (ok[j] && r < it.n) yp[j][r] = y[j];
+      }
     }
-#pragma unroll
-    for (int j = 0; j < TG; ++j) {
-      s[j] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[j] = fmaf(b[q][i], h[j][i], s[j]);
-      s[j] = lanes_sum<LPR>(s[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < TG; ++j)
-      if (ok && j < n && j % LPR == l) it.y[tok[j] * it.ldy + r] = fmaf(scale, s[j], base[j]);
   }
 }
 
 }  // namespace
 
-// y[t][r] = base[t][r] + scale * sum over i of B[r][i] h[t][i].
-template <int DT, int LPR, int RPT>
+// y[t][r] = base[t][r] + scale * sum over i of B[r][i] h[t][i]: a workgroup
+// takes `steps` steps of an item's rows for a tile.
+template <int DT, int LPR>
 __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraArgs a) {
-  __shared__ float hs[kTile * 8 * LPR];
-  Tile tile = tile_of(a, blockIdx.y);
-  if (tile.n == 0) return;
+  __shared__ __align__(16) float hs[kTile * 8 * LPR];
   int m = 0;
   for (int i = 1; i < a.n_items; ++i) m += (int)blockIdx.x >= a.item[i].first ? 1 : 0;
   const LoraItem it = a.item[m];
-  const int rank = rank_of(a, tile.adapter), n = tile.n;
-  const int n0 = ((int)blockIdx.x - it.first) * (kUpThreads / LPR) * RPT;
-  int tok[kTile];
-#pragma unroll
-  for (int j = 0; j < kTile; ++j) tok[j] = j < n ? next_token(tile) : tok[0];
-  if (rank == 0) {  // no adapter: y = base
-    if (it.y == it.base) return;
-    for (int j = 0; j < n; ++j) {
-      const int t = tok[0];
-#pragma unroll
-      for (int i = 0; i + 1 < kTile; ++i) tok[i] = tok[i + 1];
-      for (int r = n0 + threadIdx.x; r < min(n0 + kUpThreads / LPR * RPT, it.n); r += kUpThreads)
-        it.y[t * it.ldy + r] = it.base != nullptr ? it.base[t * it.ldb + r] : 0.f;
+  const int n0 = ((int)blockIdx.x - it.first) * (kUpThreads / LPR) * a.steps;
+  const int rows = min(kUpThreads / LPR * a.steps, it.n - n0);
+  const int id = ids_of(a, slot_token(blockIdx.y, 0));
+  for (int q = 0; q < 64 / kSlots; ++q) {
+    const int t = slot_token(blockIdx.y, q);
+    if (t >= a.n_tok) continue;
+    const Tile tile = tile_of(id, t);
+    if (tile.n == 0) continue;
+    const int rank = rank_of(a, tile.adapter);
+    if (rank == 0) {  // no adapter: y = base
+      if (it.y == it.base) continue;
+      for (int j = 0; j < tile.n; ++j) {
+        const int s = tile.token(j);
+        for (int r = n0 + threadIdx.x; r < n0 + rows; r += kUpThreads)
+          it.y[s * it.ldy + r] = it.base != nullptr ? it.base[s * it.ldb + r] : 0.f;
+      }
+      continue;
     }
-    return;
+    const int steps = (rows + kUpThreads / LPR - 1) / (kUpThreads / LPR);
+    if (tile.n == 1) up<DT, LPR, 1>(a, it, m, tile, rank, hs, n0, steps);
+    else if (tile.n == 2) up<DT, LPR, 2>(a, it, m, tile, rank, hs, n0, steps);
+    else up<DT, LPR, 4>(a, it, m, tile, rank, hs, n0, steps);
   }
-  for (int i = threadIdx.x; i < kTile * 8 * LPR; i += kUpThreads) {
-    const int j = i / (8 * LPR), r = i % (8 * LPR);
-    float v = 0.f;
-    if (j < n && r < rank) {
-      int t = tok[0];
-#pragma unroll
-      for (int q = 1; q < kTile; ++q) t = q == j ? tok[q] : t;
-      const int64_t step = (int64_t)a.n_tok * a.n_items * a.max_rank;
-      const float* p = a.h + ((int64_t)t * a.n_items + m) * a.max_rank + r;
-      for (int z = 0; z < a.slices; ++z) v += p[z * step];
-    }
-    hs[i] = v;
-  }
-  __syncthreads();
-  if (n == 1) up<DT, LPR, RPT, 1>(a, it, hs, tile.adapter, rank, n, tok, n0);
-  else if (n == 2) up<DT, LPR, RPT, 2>(a, it, hs, tile.adapter, rank, n, tok, n0);
-  else if (n <= 4) up<DT, LPR, RPT, 4>(a, it, hs, tile.adapter, rank, n, tok, n0);
-  else up<DT, LPR, RPT, 8>(a, it, hs, tile.adapter, rank, n, tok, n0);
+}
+
+// Tiles that a call's tokens are taken to make: one of n_tok / kTile .. n_tok,
+// which the ids decide.
+static int64_t likely_tiles(int64_t n_tok) {
+  const int64_t few = n_tok < 8 ? n_tok : 8, least = (n_tok + kTile - 1) / kTile;
+  return few > least ? few : least;
 }
 
 int lora_slices(int64_t n_items, int64_t max_rank, int64_t n_tok) {
-  // about two workgroups a compute unit at the fewest tiles that the tokens can make
-  const int64_t groups = n_items * ((max_rank + kDownRows - 1) / kDownRows) * ((n_tok + kTile - 1) / kTile);
-  const int64_t want = (512 + groups - 1) / groups;
+  const int64_t rows = kDownRows * kWaves;
+  const int64_t groups = n_items * ((max_rank + rows - 1) / rows) * likely_tiles(n_tok);
+  const int64_t want = (kDownTarget + groups - 1) / groups;
   return (int)(want > kLoraMaxSlices ? kLoraMaxSlices : want);
 }
 
 namespace {
 
-template <int DT, int LPR, int RPT>
-hipError_t launch_up(LoraArgs& a, hipStream_t st) {
-  const int rows = kUpThreads / LPR * RPT;
-  int64_t wgs = 0;
-  for (int i = 0; i < a.n_items; ++i) {
-    a.item[i].first = (int)wgs;
-    wgs += (a.item[i].n + rows - 1) / rows;
-  }
-  hipLaunchKernelGGL((k_lora_up<DT, LPR, RPT>), dim3((unsigned)wgs, (unsigned)a.n_tok), dim3(kUpThreads), 0, st, a);
-  return hipGetLastError();
-}
+unsigned lora_slots(int n_tok) { return n_tok < kSlots ? n_tok : (n_tok + 63) / 64 * kSlots; }
 
 template <int DT, int LPR>
 hipError_t launch_up(LoraArgs& a, hipStream_t st) {
-  int64_t rows = 0;
-  for (int i = 0; i < a.n_items; ++i) rows += a.item[i].n;
-  // four rows a lane group once that leaves four workgroups a compute unit
-  if (rows * LPR / kUpThreads / 4 * ((a.n_tok + kTile - 1) / kTile) >= 1024) return launch_up<DT, LPR, 4>(a, st);
-  return launch_up<DT, LPR, 1>(a, st);
+  constexpr int kStep = kUpThreads / LPR;
+  int64_t steps = 0;
+  for (int i = 0; i < a.n_items; ++i) steps += (a.item[i].n + kStep - 1) / kStep;
+  const int64_t want = (kUpTarget + likely_tiles(a.n_tok) - 1) / likely_tiles(a.n_tok);
+  a.steps = (int)((steps + want - 1) / want);
+  int64_t wgs = 0;
+  for (int i = 0; i < a.n_items; ++i) {
+    a.item[i].first = (int)wgs;
+    wgs += (a.item[i].n + kStep * a.steps - 1) / (kStep * a.steps);
+  }
+  hipLaunchKernelGGL((k_lora_up<DT, LPR>), dim3((unsigned)wgs, lora_slots(a.n_tok)), dim3(kUpThreads), 0, st, a);
+  return hipGetLastError();
 }
 
 template <int DT>
 hipError_t launch(LoraArgs a, hipStream_t st) {
-  const int groups = (a.max_rank + kDownRows - 1) / kDownRows;
-  hipLaunchKernelGGL((k_lora_down<DT>), dim3((unsigned)(a.n_items * groups), (unsigned)a.n_tok, (unsigned)a.slices),
-                     dim3(64 * kDownWaves), 0, st, a);
+  const int rows = kDownRows * kWaves, groups = (a.max_rank + rows - 1) / rows;
+  hipLaunchKernelGGL((k_lora_down<DT>), dim3((unsigned)(a.n_items * groups), lora_slots(a.n_tok), (unsigned)a.slices),
+                     dim3(64 * kWaves), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int v = a.max_rank / 8;
@@ -316,10 +412,10 @@ hipError_t launch(LoraArgs a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_lora(int type, LoraArgs a, hipStream_t st) {
-  // as many slices as have a chunk for every wave
-  const int most = (a.k + kChunk * kDownWaves - 1) / (kChunk * kDownWaves);
+  const int most = (a.k + kChunk - 1) / kChunk;
   a.slices = min(lora_slices(a.n_items, a.max_rank, a.n_tok), most);
-  a.slice = ((a.k + a.slices - 1) / a.slices + kChunk - 1) / kChunk * kChunk;
+  a.slice = (most + a.slices - 1) / a.slices * kChunk;
+  a.slices = (a.k + a.slice - 1) / a.slice;
   if (type == kF16) return launch<kF16>(a, st);
   if (type == kBF16) return launch<kBF16>(a, st);
   return launch<kF32>(a, st);

@@ -52,6 +52,7 @@ struct LoraArgs {
   const float* scales;   // NULL, or [adapters]
   float* h;              // [slices][n_tok][n_items][max_rank]
   int slices, slice;     // of k, and their length; set at launch
+  int steps;             // of rows that a workgroup of the outputs takes; set at launch
 };
 // The most partial sums of h that a call makes (k alone can make them fewer).
 constexpr int kLoraMaxSlices = 16;

@@ -1154,13 +1154,14 @@ QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int
   return hip_status(launch_lora(type, a, static_cast<hipStream_t>(stream)));
 }
 
-// Workspace of qmv_router_gate: arrival counters of the token groups, then
-// the logits, at a fixed offset so that calls of different shapes can share it.
+// Workspace of qmv_router_gate: an arrival counter, then the
+// logits of each slice of k, at a fixed offset so that calls of different
+// shapes can share it.
 constexpr int64_t kGateCounterBytes = 256;
 
 QMV_API size_t qmv_router_gate_workspace_bytes(int64_t n_tok, int64_t n_experts) {
   if (n_tok < 1 || n_tok > QMV_MAX_MOE_TOKENS || n_experts < 1 || n_experts > QMV_MAX_EXPERTS) return 0;
-  return static_cast<size_t>(kGateCounterBytes + align256(8 * n_tok * n_experts));
+  return static_cast<size_t>(kGateCounterBytes + align256(8 * n_tok * n_experts * gate_slices(n_tok, n_experts)));
 }
 
 QMV_API qmv_status qmv_router_gate(const float* x, int64_t ldx, int64_t n_tok, int64_t k, const float* wr,
@@ -1208,6 +1209,7 @@ QMV_API qmv_status qmv_router_gate(const float* x, int64_t ldx, int64_t n_tok, i
     a.qd = const_cast<float*>(v.d);
     a.qsum = const_cast<int32_t*>(v.s);
   }
+  a.cnt = static_cast<int*>(ws);
   a.logits = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kGateCounterBytes);
   return hip_status(launch_router_gate(a, static_cast<hipStream_t>(stream)));
 }

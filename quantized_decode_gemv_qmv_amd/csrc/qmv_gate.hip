@@ -12,8 +12,12 @@ namespace qmv {
 
 namespace {
 
-constexpr int kGateWaves = 8;
-constexpr int kGatePer = 16;  // experts of a lane at most
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kGateWaves = 16;
+constexpr int kGateTile = 16;  // experts and tokens of a matrix product
+constexpr int kGateAhead = 5;  // steps whose loads are in flight
+constexpr int kFewExperts = 4; // of a workgroup, up to four tokens
 
 template <int CTRL>
 __device__ __forceinline__ double dpp_d(double v) {
@@ -79,109 +83,101 @@ __device__ __forceinline__ int wave_first(uint64_t key, int index) {
 }
 
 // One token's choice by one wave.  l: the lane's logits, of experts lane + 64 i;
-// sc: an array of n_experts doubles in LDS of this wave's own.
-__device__ __forceinline__ void gate_select(const GateArgs& a, int t, double (&l)[kGatePer], double* sc) {
+// sc: an array of 64 PER doubles in LDS of this wave's own.
+template <int PER>
+__device__ __forceinline__ void gate_select(const GateArgs& a, int t, double (&l)[PER], double* sc) {
   const int lane = threadIdx.x & 63;
-  const int per = (a.n_experts + 63) / 64;
   // scores
   if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < kGatePer; ++i)
-      if (i < per) l[i] = 1.0 / (1.0 + exp(-l[i]));
+    for (int i = 0; i < PER; ++i) l[i] = 1.0 / (1.0 + exp(-l[i]));
   } else {
     double m = -__builtin_inf(), sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < kGatePer; ++i)
+    for (int i = 0; i < PER; ++i)
       if (lane + 64 * i < a.n_experts) m = fmax(m, l[i]);
     m = wave_max_d(m);
 #pragma unroll
-    for (int i = 0; i < kGatePer; ++i)
-      if (i < per) {
-        l[i] = exp(l[i] - m);
-        if (lane + 64 * i < a.n_experts) sum += l[i];
-      }
-    sum = wave_sum_d(sum);
+    for (int i = 0; i < PER; ++i) {
+      l[i] = exp(l[i] - m);
+      if (lane + 64 * i < a.n_experts) sum += l[i];
+    }
+    const double inv = 1.0 / wave_sum_d(sum);
 #pragma unroll
-    for (int i = 0; i < kGatePer; ++i)
-      if (i < per) l[i] = l[i] / sum;
+    for (int i = 0; i < PER; ++i) l[i] *= inv;
   }
-  // choices: with the bias, in LDS for the groups
-  double c[kGatePer];
-  uint32_t in = 0;  // bit i: expert lane + 64 i may be chosen
+  // choices: with the bias; 0 is below each of them
+  uint64_t key[PER];
 #pragma unroll
-  for (int i = 0; i < kGatePer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
-    c[i] = 0.0;
+    key[i] = 0;
     if (e < a.n_experts) {
-      c[i] = l[i] + (a.bias != nullptr ? (double)a.bias[e] : 0.0);
-      in |= 1u << i;
+      const double c = l[i] + (a.bias != nullptr ? (double)a.bias[e] : 0.0);
+      key[i] = place(c);
+      if (a.groups > 1) sc[e] = c;
     }
   }
   if (a.groups > 1) {
-#pragma unroll
-    for (int i = 0; i < kGatePer; ++i)
-      if (lane + 64 * i < a.n_experts) sc[lane + 64 * i] = c[i];
     __builtin_amdgcn_wave_barrier();
     const int size = a.n_experts / a.groups;
-    uint64_t key = 0;
-    if (lane < a.groups) {  // a group's worth: its largest one or two
-      double u = -__builtin_inf(), v = u;
-      for (int i = 0; i < size; ++i) {
-        double w = sc[lane * size + i];
+    // a group's worth, its largest one or two: S lanes a group
+    int shift = 6;
+    while ((a.groups << shift) > 64) --shift;
+    const int g = lane >> shift, first = lane & ((1 << shift) - 1);
+    double u = -__builtin_inf(), v = u;
+    if (g < a.groups) {
+      for (int i = first; i < size; i += 1 << shift) {
+        double w = sc[g * size + i];
         w = w == w ? w : -__builtin_inf();
         v = fmax(v, fmin(u, w));
         u = fmax(u, w);
       }
-      key = place(a.group_best == 2 ? u + v : u);
     }
+    for (int o = 1; o < 1 << shift; o <<= 1) {
+      const double p = __shfl_xor(u, o), q = __shfl_xor(v, o);
+      v = fmax(fmin(u, p), fmax(v, q));
+      u = fmax(u, p);
+    }
+    uint64_t worth = g < a.groups && first == 0 ? place(a.group_best == 2 ? u + v : u) : 0;
     uint64_t kept = 0;
     for (int j = 0; j < a.top_groups; ++j) {
-      const int g = wave_first(key, lane);
-      kept |= 1ull << g;
-      if (lane == g) key = 0;
+      const int w = wave_first(worth, lane);
+      kept |= 1ull << (w >> shift);
+      if (lane == w) worth = 0;
     }
 #pragma unroll
-    for (int i = 0; i < kGatePer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const int e = lane + 64 * i;
-      if (e < a.n_experts && !((kept >> (e / size)) & 1)) in &= ~(1u << i);
+      if (e < a.n_experts && !((kept >> (e / size)) & 1)) key[i] = 0;
     }
     __builtin_amdgcn_wave_barrier();
   }
   // the largest one after the other
-  uint64_t key = 0;
-  int at = 0;
-  auto best = [&]() {
-    key = 0;
-    at = 0;
-#pragma unroll
-    for (int i = 0; i < kGatePer; ++i)
-      if (i < per && (in >> i) & 1) {
-        const uint64_t p = place(c[i]);
-        if (p > key) {
-          key = p;
-          at = i;
-        }
-      }
-  };
-  best();
   double mine = 0.0, total = 0.0;
   int id = 0;
   for (int j = 0; j < a.top_k; ++j) {
-    const int w = wave_first(key, lane + 64 * at);
+    uint64_t best = key[0];
     double s = l[0];
+    int at = 0;
 #pragma unroll
-    for (int i = 1; i < kGatePer; ++i) s = at == i ? l[i] : s;
+    for (int i = 1; i < PER; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        s = l[i];
+        at = i;
+      }
+    const int w = wave_first(best, lane + 64 * at);
+    const int i = __builtin_amdgcn_readlane(at, w);
     s = lane_d(s, w);
-    const int e = w + 64 * __builtin_amdgcn_readlane(at, w);
     total += s;
     if (lane == j) {
-      id = e;
+      id = w + 64 * i;
       mine = s;
     }
-    if (lane == w) {
-      in &= ~(1u << at);
-      best();
-    }
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (lane == w && q == i) key[q] = 0;
   }
   if (lane < a.top_k) {
     double w = mine;
@@ -191,120 +187,240 @@ __device__ __forceinline__ void gate_select(const GateArgs& a, int t, double (&l
   }
 }
 
-// EG experts x TG tokens x 4 columns of a lane.
-template <int EG, int TG>
-struct GateChunk {
-  f32x4 w[EG];
-  f32x4 x[TG];
-  __device__ __forceinline__ void load(const GateArgs& a, int e0, int t0, int c) {
+// A token's logits from the slices' sums, many loads of a lane in flight, then
+// its choice.  DEVICE: the sums are another workgroup's of this launch.
+template <int PER, bool DEVICE>
+__device__ __forceinline__ void gate_token(const GateArgs& a, int t, double* sc) {
+  constexpr int Z = PER >= 4 ? 16 / PER : 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t step = (int64_t)a.n_tok * a.n_experts;
+  const double* p = a.logits + (int64_t)t * a.n_experts;
+  double l[PER];
 #pragma unroll
-    for (int e = 0; e < EG; ++e)
-      w[e] = *reinterpret_cast<const f32x4*>(a.wr + (int64_t)min(e0 + e, a.n_experts - 1) * a.k + c);
+  for (int i = 0; i < PER; ++i) l[i] = 0.0;
+  for (int z0 = 0; z0 < a.slices; z0 += Z) {
+    double v[Z][PER];
 #pragma unroll
-    for (int t = 0; t < TG; ++t)
-      x[t] = *reinterpret_cast<const f32x4*>(a.x + (int64_t)min(t0 + t, a.n_tok - 1) * a.ldx + c);
+    for (int z = 0; z < Z; ++z)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const double* q = p + min(z0 + z, a.slices - 1) * step + min(lane + 64 * i, a.n_experts - 1);
+        if constexpr (DEVICE)
+          v[z][i] = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else
+          v[z][i] = *q;
+      }
+#pragma unroll
+    for (int z = 0; z < Z; ++z)
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (z0 + z < a.slices) l[i] += v[z][i];
   }
-  __device__ __forceinline__ void fma_into(double (&acc)[EG * TG]) const {
+  if (a.logits_out != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      double wd[EG], xd[TG];
-#pragma unroll
-      for (int e = 0; e < EG; ++e) wd[e] = (double)w[e][i];
-#pragma unroll
-      for (int t = 0; t < TG; ++t) xd[t] = (double)x[t][i];
-#pragma unroll
-      for (int e = 0; e < EG; ++e)
-#pragma unroll
-        for (int t = 0; t < TG; ++t) acc[e * TG + t] = fma(wd[e], xd[t], acc[e * TG + t]);
+    for (int i = 0; i < PER; ++i)
+      if (lane + 64 * i < a.n_experts) a.logits_out[(int64_t)t * a.n_experts + lane + 64 * i] = (float)l[i];
+  }
+  gate_select<PER>(a, t, l, sc);
+}
+
+// Q8 blocks of columns lo .. hi - 1 of one row of x by the workgroup.
+__device__ __forceinline__ void put_q8(const GateArgs& a, int t, int lo, int hi) {
+  for (int c = lo + 4 * (int)threadIdx.x; c < hi; c += 4 * 64 * kGateWaves) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(a.x + t * a.ldx + c);
+    const float vv[4] = {v[0], v[1], v[2], v[3]};
+    float d;
+    int sum;
+    const uint32_t packed = q8_block8(vv, d, sum);
+    *reinterpret_cast<uint32_t*>(a.qs + (int64_t)t * a.k + c) = packed;
+    if ((threadIdx.x & 7) == 0) {
+      a.qd[(int64_t)t * (a.k / 32) + c / 32] = d;
+      a.qsum[(int64_t)t * (a.k / 32) + c / 32] = sum;
     }
   }
-};
+}
+
+// Sums of N values over each 16 lanes: lane l has that of value l % N (while
+// there are several, a lane keeps one half of them and gives the other away).
+template <int H, int N>
+__device__ __forceinline__ void fold16(double* v, int lane) {
+  if constexpr (H >= 1) {
+    constexpr int kCtrl = H == 8 ? DPP_MIRROR : (H == 4 ? DPP_HALF_MIRROR : (H == 2 ? DPP_XOR2 : DPP_XOR1));
+    if constexpr (N > H) {
+      static_assert(N == 2 * H, "N a power of two of at most 16");
+      const bool hi = (lane & H) != 0;
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        const double send = hi ? v[j] : v[j + H];
+        const double keep = hi ? v[j + H] : v[j];
+        v[j] = keep + dpp_d<kCtrl>(send);
+      }
+      fold16<H / 2, N / 2>(v, lane);
+    } else {
+      static_assert(H >= N, "lanes above the values' hold the same ones");
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] += dpp_d<kCtrl>(v[j]);
+      fold16<H / 2, N>(v, lane);
+    }
+  }
+}
 
 }  // namespace
 
-// l[t][e] = sum over c of wr[e][c] x[t][c] in fp64 (products of fp32 numbers
-// are exact there), EG experts by TG tokens a workgroup whose waves share the
-// columns.  Workgroups of the first experts also write the Q8 blocks of x.
-template <int EG, int TG>
-__global__ __launch_bounds__(64 * kGateWaves) void k_gate_logits(GateArgs a) {
-  constexpr int P = EG * TG;
-  __shared__ double red[kGateWaves][P];
+// Few tokens: a workgroup has kFewExperts experts and TG tokens, its waves the
+// columns between them, four a lane; l in fp64, where products of fp32 numbers
+// are exact.  The last workgroup to arrive chooses, a wave for each token.
+template <int PER, int TG>
+__global__ __launch_bounds__(64 * kGateWaves) void k_gate_few(GateArgs a) {
+  constexpr int P = kFewExperts * TG;
+  constexpr int kRed = kGateWaves * 4 * P, kSc = TG * 64 * PER;
+  __shared__ double lds[kRed > kSc ? kRed : kSc];
+  __shared__ int s_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e0 = blockIdx.x * EG, t0 = blockIdx.y * TG;
+  const int e0 = blockIdx.x * kFewExperts;
   double acc[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) acc[i] = 0.0;
-  constexpr int kStep = 4 * 64 * kGateWaves;
-  const bool qx = a.qs != nullptr && blockIdx.x == 0;
-  auto put = [&](const GateChunk<EG, TG>& ch, int col) {
+  for (int c = 4 * (int)threadIdx.x; c < a.k; c += 4 * 64 * kGateWaves) {
+    f32x4 w[kFewExperts], x[TG];
 #pragma unroll
-    for (int t = 0; t < TG; ++t) {
-      if (t0 + t < a.n_tok) {  // uniform
-        const float vv[4] = {ch.x[t].x, ch.x[t].y, ch.x[t].z, ch.x[t].w};
-        float db;
-        int sum;
-        const uint32_t packed = q8_block8(vv, db, sum);
-        *reinterpret_cast<uint32_t*>(a.qs + (int64_t)(t0 + t) * a.k + col) = packed;
-        if ((lane & 7) == 0) {
-          a.qd[(int64_t)(t0 + t) * (a.k / 32) + col / 32] = db;
-          a.qsum[(int64_t)(t0 + t) * (a.k / 32) + col / 32] = sum;
-        }
-      }
-    }
-  };
-  for (int c = 4 * (lane + 64 * wave); c < a.k; c += kStep) {
-    GateChunk<EG, TG> ch;
-    ch.load(a, e0, t0, c);
-    if (qx) put(ch, c);
-    ch.fma_into(acc);
-  }
+    for (int e = 0; e < kFewExperts; ++e)
+      w[e] = *reinterpret_cast<const f32x4*>(a.wr + (int64_t)min(e0 + e, a.n_experts - 1) * a.k + c);
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const double v = wave_sum_d(acc[i]);
-    if (lane == 0) red[wave][i] = v;
+    for (int t = 0; t < TG; ++t) x[t] = *reinterpret_cast<const f32x4*>(a.x + min(t, a.n_tok - 1) * a.ldx + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < kFewExperts; ++e)
+#pragma unroll
+        for (int t = 0; t < TG; ++t) acc[e * TG + t] = fma((double)w[e][i], (double)x[t][i], acc[e * TG + t]);
   }
+  if (a.qs != nullptr && (int)blockIdx.x < a.n_tok) put_q8(a, blockIdx.x, 0, a.k);
+  if (a.qs != nullptr && gridDim.x < a.n_tok && blockIdx.x == 0)  // fewer workgroups than tokens
+    for (int t = gridDim.x; t < a.n_tok; ++t) put_q8(a, t, 0, a.k);
+  fold16<8, P>(acc, lane);
+  if ((lane & 15) < P) lds[(4 * wave + lane / 16) * P + (lane & 15)] = acc[0];
   __syncthreads();
   if (threadIdx.x < P) {
-    double s = red[0][threadIdx.x];
+    double s = 0.0;
 #pragma unroll
-    for (int w = 1; w < kGateWaves; ++w) s += red[w][threadIdx.x];
-    const int e = e0 + threadIdx.x / TG, t = t0 + threadIdx.x % TG;
-    if (e < a.n_experts && t < a.n_tok) a.logits[(int64_t)t * a.n_experts + e] = s;
+    for (int i = 0; i < 4 * kGateWaves; ++i) s += lds[i * P + threadIdx.x];
+    const int e = e0 + threadIdx.x / TG, t = threadIdx.x % TG;
+    if (e < a.n_experts && t < a.n_tok)
+      __hip_atomic_store(&a.logits[(int64_t)t * a.n_experts + e], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  // Logits are device-scope atomic accesses (written through and reloaded by
+  // the L2s), so waiting for this lane's own stores before the barrier and the
+  // counter's update orders them without a device-scope fence.
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(a.cnt, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  if (threadIdx.x == 0) atomicExch(a.cnt, 0);
+  if (wave < a.n_tok) gate_token<PER, true>(a, wave, lds + wave * 64 * PER);  // no barrier in it
+}
+
+// More tokens: l on the fp64 matrix unit.  A workgroup has 16 experts and 16
+// tokens, its waves deal the columns of its slice among themselves, 16 a step.
+// A lane holds four neighbouring columns of one expert and of one token, of
+// which each product takes one.
+__global__ __launch_bounds__(64 * kGateWaves) void k_gate_logits(GateArgs a) {
+  constexpr int kPad = kGateTile + 1;
+  __shared__ double lds[kGateWaves * kGateTile * kPad];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e0 = blockIdx.x * kGateTile, t0 = blockIdx.y * kGateTile;
+  const int lo = blockIdx.z * a.slice, hi = min(lo + a.slice, a.k);
+  const int at = 4 * (lane / 16);
+  const float* w = a.wr + (int64_t)min(e0 + lane % 16, a.n_experts - 1) * a.k + at;
+  const float* x = a.x + min(t0 + lane % 16, a.n_tok - 1) * a.ldx + at;
+  f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+  constexpr int kStep = 16 * kGateWaves;
+  for (int c0 = lo + 16 * wave; c0 < hi; c0 += kGateAhead * kStep) {  // uniform
+    f32x4 wv[kGateAhead], xv[kGateAhead];
+#pragma unroll
+    for (int u = 0; u < kGateAhead; ++u) {
+      const int c = c0 + u * kStep;
+      wv[u] = xv[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (c + at < hi) {
+        wv[u] = *reinterpret_cast<const f32x4*>(w + c);
+        xv[u] = *reinterpret_cast<const f32x4*>(x + c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kGateAhead; ++u)
+      if (c0 + u * kStep < hi) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)wv[u][i], (double)xv[u][i], acc, 0, 0, 0);
+      }
+  }
+  if (a.qs != nullptr)  // the slice's Q8 blocks, the tile's tokens dealt among the workgroups along the experts
+    for (int t = t0 + blockIdx.x; t < min(t0 + kGateTile, a.n_tok); t += gridDim.x) put_q8(a, t, lo, hi);
+  // element r of the product: expert 4 r + lane / 16, token lane % 16
+#pragma unroll
+  for (int r = 0; r < 4; ++r) lds[(wave * kGateTile + lane % 16) * kPad + 4 * r + lane / 16] = acc[r];
+  __syncthreads();
+  if (threadIdx.x < kGateTile * kGateTile) {
+    const int e = threadIdx.x % kGateTile, t = threadIdx.x / kGateTile;
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kGateWaves; ++i) s += lds[(i * kGateTile + t) * kPad + e];
+    if (e0 + e < a.n_experts && t0 + t < a.n_tok)
+      a.logits[((int64_t)blockIdx.z * a.n_tok + t0 + t) * a.n_experts + e0 + e] = s;
   }
 }
 
 // One wave a token.
+template <int PER>
 __global__ __launch_bounds__(64) void k_gate_select(GateArgs a) {
-  __shared__ double sc[64 * kGatePer];
-  const int t = blockIdx.x, lane = threadIdx.x;
-  double l[kGatePer];
-#pragma unroll
-  for (int i = 0; i < kGatePer; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < a.n_experts ? a.logits[(int64_t)t * a.n_experts + e] : 0.0;
-    if (a.logits_out != nullptr && e < a.n_experts) a.logits_out[(int64_t)t * a.n_experts + e] = (float)l[i];
-  }
-  gate_select(a, t, l, sc);
+  __shared__ double sc[64 * PER];
+  gate_token<PER, false>(a, blockIdx.x, sc);
+}
+
+int gate_slices(int64_t n_tok, int64_t n_experts) {
+  // a workgroup for each compute unit
+  const int64_t tiles = ((n_tok + kGateTile - 1) / kGateTile) * ((n_experts + kGateTile - 1) / kGateTile);
+  const int64_t s = 256 / tiles;
+  return (int)(s < 1 ? 1 : (s > kGateMaxSlices ? kGateMaxSlices : s));
 }
 
 namespace {
 
-template <int EG, int TG>
-void launch_logits(const GateArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.n_experts + EG - 1) / EG), (unsigned)((a.n_tok + TG - 1) / TG));
-  hipLaunchKernelGGL((k_gate_logits<EG, TG>), grid, dim3(64 * kGateWaves), 0, st, a);
+template <int PER>
+hipError_t launch(const GateArgs& a, hipStream_t st) {
+  const dim3 block(64 * kGateWaves);
+  if (a.n_tok <= 4) {
+    const dim3 grid((unsigned)((a.n_experts + kFewExperts - 1) / kFewExperts));
+    if (a.n_tok == 1) hipLaunchKernelGGL((k_gate_few<PER, 1>), grid, block, 0, st, a);
+    else if (a.n_tok == 2) hipLaunchKernelGGL((k_gate_few<PER, 2>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_gate_few<PER, 4>), grid, block, 0, st, a);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)((a.n_experts + kGateTile - 1) / kGateTile), (unsigned)((a.n_tok + kGateTile - 1) / kGateTile),
+                  (unsigned)a.slices);
+  hipLaunchKernelGGL(k_gate_logits, grid, block, 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_gate_select<PER>), dim3((unsigned)a.n_tok), dim3(64), 0, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_router_gate(const GateArgs& a, hipStream_t st) {
-  if (a.n_tok == 1) launch_logits<1, 1>(a, st);
-  else if (a.n_tok == 2) launch_logits<2, 2>(a, st);
-  else launch_logits<4, 4>(a, st);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_gate_select, dim3((unsigned)a.n_tok), dim3(64), 0, st, a);
-  return hipGetLastError();
+hipError_t launch_router_gate(GateArgs a, hipStream_t st) {
+  // slices in whole steps of all waves (which Q8 blocks are too), two for each wave or more
+  constexpr int kStep = 16 * kGateWaves;
+  const int steps = (a.k + kStep - 1) / kStep;
+  a.slices = a.n_tok <= 4 ? 1 : min(gate_slices(a.n_tok, a.n_experts), (steps + 1) / 2);
+  a.slice = (steps + a.slices - 1) / a.slices * kStep;
+  a.slices = (a.k + a.slice - 1) / a.slice;
+  const int per = (a.n_experts + 63) / 64;
+  if (per <= 1) return launch<1>(a, st);
+  if (per <= 2) return launch<2>(a, st);
+  if (per <= 4) return launch<4>(a, st);
+  if (per <= 8) return launch<8>(a, st);
+  return launch<16>(a, st);
 }
 
 }  // namespace qmv

@@ -76,9 +76,14 @@ struct GateArgs {
   int8_t* qs;         // NULL, or the Q8 blocks of x
   float* qd;
   int32_t* qsum;
-  double* logits;  // [n_tok][n_experts]
+  double* logits;  // [slices][n_tok][n_experts]
+  int* cnt;        // the arrival counter
+  int slices, slice;  // of k, and their length; set at launch
 };
-hipError_t launch_router_gate(const GateArgs& a, hipStream_t st);
+// The most slices of k that a call makes (k alone can make them fewer).
+constexpr int kGateMaxSlices = 8;
+int gate_slices(int64_t n_tok, int64_t n_experts);
+hipError_t launch_router_gate(GateArgs a, hipStream_t st);
 
 // Log probabilities of a row of logits.
 constexpr int kPartGroupsOfRow = 16;  // keys of a part

@@ -116,7 +116,7 @@ def gate(**kw):
     (dict(e=130, groups=65, top_groups=65), UNSUPPORTED),
     (dict(x=FAKE + 4), MISALIGNED), (dict(w=FAKE + 8), MISALIGNED), (dict(bias=FAKE + 2), MISALIGNED),
     (dict(ids=FAKE + 1), MISALIGNED), (dict(weights=FAKE + 2), MISALIGNED), (dict(logits=FAKE + 2), MISALIGNED),
-    (dict(xq=FAKE + 64), MISALIGNED), (dict(ws=FAKE + 128), MISALIGNED), (dict(wsb=1023), WORKSPACE),
+    (dict(xq=FAKE + 64), MISALIGNED), (dict(ws=FAKE + 128), MISALIGNED), (dict(wsb=q.router_gate_workspace_bytes(3, 32) - 1), WORKSPACE),
     (dict(wsb=0), WORKSPACE)])
 def test_gate_refusals(change, status):
     assert gate(**change) == status
@@ -124,7 +124,7 @@ def test_gate_refusals(change, status):
 
 def test_gate_workspace_and_binding():
     f = q.router_gate_workspace_bytes
-    assert f(3, 32) == 1024 and f(64, 1024) >= 64 * 1024 * 8
+    assert f(3, 32) >= 256 + 3 * 32 * 8 and f(64, 1024) >= 64 * 1024 * 8
     for bad in ((0, 32), (65, 32), (1, 0), (1, 1025)):
         assert f(*bad) == 0, bad
     x, w = torch.zeros(2, 64), torch.zeros(8, 64)

@@ -16,7 +16,8 @@ namespace qmv {
 namespace {
 
 constexpr float kLog2e = 1.44269504f;
-constexpr int kRowThreads = 1024;  // of a workgroup that has a whole row, or joins one
+constexpr int kRowThreads = 512;   // of a workgroup that has a whole row
+constexpr int kJoinThreads = 512;  // of one that joins a row
 constexpr int kPartThreads = 256;
 constexpr int kPartVecs = 4;       // 16-byte vectors of a thread
 constexpr int kPartVec = kPartThreads * kPartVecs;  // vectors of a part
@@ -97,7 +98,7 @@ __device__ __forceinline__ void add(float& s, float& u, const f32x4& v, float sc
 __device__ __forceinline__ float max4(const f32x4& v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 
 // Vector i of a row: elements past its end are -inf.
-__device__ __forceinline__ f32x4 load_vec(const float* row, int64_t i, int n) {
+__device__ __forceinline__ f32x4 load_vec(const float* row, int i, int n) {
   if (4 * i + 4 <= n) return *reinterpret_cast<const f32x4*>(row + 4 * i);
   f32x4 v;
 #pragma unroll
@@ -134,55 +135,83 @@ __device__ __forceinline__ float log_prob(float x, float scale, const Sums& a, d
   return (float)(((double)x * (double)scale - (double)a.m) - log_s);
 }
 
+// The given token that a thread starts with, and its logit.
+struct Given {
+  int id;
+  float x;
+};
+__device__ __forceinline__ Given first_given(const LogprobArgs& a, int t, const float* row) {
+  Given g{-1, 0.f};
+  if ((int)threadIdx.x < a.n_given) g.id = a.given[(int64_t)t * a.n_given + threadIdx.x];
+  if (g.id >= 0 && g.id < a.n_vocab) g.x = row[g.id];
+  return g;
+}
+
 // Entropy and the given tokens' log probabilities of row t.
-__device__ __forceinline__ void put_given(const LogprobArgs& a, int t, const float* row, const Sums& r, double log_s) {
+template <int THREADS>
+__device__ __forceinline__ void put_given(const LogprobArgs& a, int t, const float* row, const Sums& r, double log_s,
+                                          Given g) {
   if (threadIdx.x == 0 && a.entropy != nullptr) {
     const bool none = r.m == -__builtin_inff() && r.s == 0.f;
     a.entropy[t] = none ? 0.f : (float)(log_s - (double)r.u / (double)r.s);
   }
-  for (int g = threadIdx.x; g < a.n_given; g += kRowThreads) {
-    const int64_t at = (int64_t)t * a.n_given + g;
-    const int id = a.given[at];
-    a.logprobs[at] = id < 0 || id >= a.n_vocab ? (r.s == r.s ? -__builtin_inff() : r.s)
-                                               : log_prob(row[id], a.scale, r, log_s);
+  for (int i = threadIdx.x; i < a.n_given; i += THREADS) {
+    const int64_t at = (int64_t)t * a.n_given + i;
+    if (i != (int)threadIdx.x) {
+      g.id = a.given[at];
+      if (g.id >= 0 && g.id < a.n_vocab) g.x = row[g.id];
+    }
+    a.logprobs[at] = g.id < 0 || g.id >= a.n_vocab ? (r.s == r.s ? -__builtin_inff() : r.s)
+                                                   : log_prob(g.x, a.scale, r, log_s);
   }
 }
 
 struct TopShared {
   uint64_t coarse[64];
   uint64_t key[kList];
+  uint64_t wave[16];
+  uint64_t least;
   uint32_t group[kList];
-  uint64_t wave[kRowThreads / 64];
   int groups, keys;
 };
 
-// The n-th largest of 64 keys, one a lane (0 where fewer are above 0), in every
-// lane alike.
-__device__ __forceinline__ uint64_t nth_of_wave(uint64_t key, int n) {
-  int larger = 0;  // keys above 0 are all different
-#pragma unroll 8
-  for (int j = 0; j < 64; ++j) larger += lane_u64(key, j) > key ? 1 : 0;
-  const uint64_t b = __ballot(larger == n - 1 && key != 0);
-  return b == 0 ? 0 : lane_u64(key, __ffsll((unsigned long long)b) - 1);
+// The n-th largest of the largest keys of 64 groups of neighbouring threads
+// (0 where fewer are above 0; the others are all different), in every thread.
+template <int THREADS>
+__device__ __forceinline__ uint64_t bound(uint64_t k, int n, TopShared& sh) {
+  constexpr int L = THREADS / 64;  // threads of a group: 8 or 16
+  const int tid = threadIdx.x;
+  k = max_u64(k, dpp_u64<DPP_XOR1>(k));
+  k = max_u64(k, dpp_u64<DPP_XOR2>(k));
+  k = max_u64(k, dpp_u64<DPP_HALF_MIRROR>(k));
+  if constexpr (L == 16) k = max_u64(k, dpp_u64<DPP_MIRROR>(k));
+  if (tid % L == 0) sh.coarse[tid / L] = k;
+  if (tid == 0) {
+    sh.least = 0;
+    sh.groups = sh.keys = 0;
+  }
+  __syncthreads();
+  // a group's threads compare its key with 64 / L others each
+  int larger = 0;
+#pragma unroll
+  for (int j = 0; j < 64 / L; ++j) larger += sh.coarse[j * L + tid % L] > k ? 1 : 0;
+  larger = sum8(larger);
+  if constexpr (L == 16) larger += dpp_i<DPP_MIRROR>(larger);
+  if (tid % L == 0 && larger == n - 1 && k != 0) sh.least = k;
+  __syncthreads();
+  return sh.least;
 }
 
-// The n largest of a row by the 1024 threads that hold its groups' largest keys
+// The n largest of a row by the threads that hold its groups' largest keys
 // (mine: the largest of this thread's groups).  each(f) calls f(key, group) for
-// the thread's groups; vec(group, i), i < items, are a group's vectors.  A
-// group's key is its largest value's, with the last index of the vector where
-// that value first stands.
-template <class Each, class Vec>
+// the thread's groups; vec(list, q), q < count(groups), is the q-th vector of the
+// listed groups.  A group's key is its largest value's, with the last index of
+// the vector where that value first stands.
+template <int THREADS, class Each, class Count, class Vec>
 __device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sums& r, double log_s, uint64_t mine,
-                        int items, TopShared& sh, Each each, Vec vec) {
+                        TopShared& sh, Each each, Count count_of, Vec vec) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.top_n;
-  auto bound = [&](uint64_t k) {  // of 64 groups of threads
-    k = row_max(k);
-    if ((tid & 15) == 0) sh.coarse[tid >> 4] = k;
-    if (tid == 0) sh.groups = sh.keys = 0;
-    __syncthreads();
-    return nth_of_wave(sh.coarse[lane], n);
-  };
-  uint64_t least = bound(mine);
+  uint64_t least = bound<THREADS>(mine, n, sh);
   each([&](uint64_t k, uint32_t g) {
     if (k != 0 && k >= least) {
       const int at = atomicAdd(&sh.groups, 1);
@@ -190,14 +219,13 @@ __device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sum
     }
   });
   __syncthreads();
-  const bool listed = sh.groups <= kList;
-  // all vectors that may hold one: of the listed groups, or of the row
-  const int64_t count = listed ? (int64_t)sh.groups * items : (a.n_vocab + 3) / 4;
   const int n_groups = sh.groups;
+  const bool listed = n_groups <= kList;
+  // all vectors that may hold one: of the listed groups, or of the row
+  const int count = listed ? count_of(n_groups) : (a.n_vocab + 3) / 4;
   auto scan = [&](auto f) {
-    for (int64_t q = tid; q < count; q += kRowThreads) {
-      int64_t i = q;
-      if (listed) i = vec(sh.group[q % n_groups], (int)(q / n_groups));
+    for (int q = tid; q < count; q += THREADS) {
+      const int i = listed ? vec(sh.group, q, n_groups) : q;
       if (4 * i >= a.n_vocab) continue;
       const f32x4 v = load_vec(row, i, a.n_vocab);
 #pragma unroll
@@ -216,7 +244,7 @@ __device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sum
   __syncthreads();
   if (sh.keys > kList) {  // once more with the bound that these themselves give
     __syncthreads();
-    least = max_u64(least, bound(top));
+    least = max_u64(least, bound<THREADS>(top, n, sh));
     scan([&](uint64_t k) {
       if (k >= least) {
         const int at = atomicAdd(&sh.keys, 1);
@@ -230,13 +258,12 @@ __device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sum
     a.ids[(int64_t)t * n + j] = (int)~(uint32_t)k;
     a.top[(int64_t)t * n + j] = log_prob(value_of(k), a.scale, r, log_s);
   };
-  if (c <= 128) {  // each one's place is the number of larger ones
-    if (tid < c) {
-      const uint64_t k = sh.key[tid];
-      int larger = 0;
-      for (int j = 0; j < c; ++j) larger += sh.key[j] > k ? 1 : 0;
-      if (larger < n) put(larger, k);
-    }
+  if (c <= THREADS / 8) {  // each one's place is the number of larger ones; eight threads count
+    const uint64_t k = tid / 8 < c ? sh.key[tid / 8] : 0;
+    int larger = 0;
+    for (int j = tid & 7; j < c; j += 8) larger += sh.key[j] > k ? 1 : 0;
+    larger = sum8(larger);
+    if ((tid & 7) == 0 && k != 0 && larger < n) put(larger, k);
   } else if (c <= kList) {  // one after the other, by one wave
     if (wave == 0) {
       uint64_t k[kList / 64];
@@ -260,8 +287,7 @@ __device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sum
       __syncthreads();
       if (lane == 0) sh.wave[wave] = best;
       __syncthreads();
-      best = sh.wave[lane & 15];
-      last = row_max(best);
+      last = row_max(sh.wave[lane & (THREADS / 64 - 1)]);
       if (tid == 0) put(j, last);
     }
   }
@@ -277,6 +303,7 @@ __global__ __launch_bounds__(kRowThreads) void k_logprob_row(LogprobArgs a) {
   const int t = blockIdx.x, tid = threadIdx.x;
   const float* row = a.x + t * a.ldx;
   const int vecs = (a.n_vocab + 3) / 4;
+  const Given given = first_given(a, t, row);
   float top = -__builtin_inff();
   int at = tid;
   Sums r{-__builtin_inff(), 0.f, 0.f};
@@ -305,12 +332,15 @@ __global__ __launch_bounds__(kRowThreads) void k_logprob_row(LogprobArgs a) {
   }
   r = block_join<kRowThreads>(r, tmp);
   const double log_s = log((double)r.s);
-  put_given(a, t, row, r, log_s);
+  put_given<kRowThreads>(a, t, row, r, log_s, given);
   if (a.top_n > 0) {
     const uint64_t key = tid < vecs ? key_of(top, (uint32_t)(4 * at + 3)) : 0;
-    put_top(a, t, row, r, log_s, key, (vecs + kRowThreads - 1) / kRowThreads, sh,
-            [&](auto f) { f(key, (uint32_t)tid); },
-            [](uint32_t g, int i) { return (int64_t)g + (int64_t)i * kRowThreads; });
+    const int items = (vecs + kRowThreads - 1) / kRowThreads;
+    put_top<kRowThreads>(a, t, row, r, log_s, key, sh, [&](auto f) { f(key, (uint32_t)tid); },
+                         [&](int groups) { return groups * items; },
+                         [](const uint32_t* list, int q, int groups) {
+                           return (int)(list[(uint32_t)q % (uint32_t)groups] + (uint32_t)q / (uint32_t)groups * kRowThreads);
+                         });
   }
 }
 
@@ -358,14 +388,19 @@ __global__ __launch_bounds__(kPartThreads) void k_logprob_part(LogprobArgs a) {
 }
 
 // Joins a row's parts.
-__global__ __launch_bounds__(kRowThreads) void k_logprob_join(LogprobArgs a) {
-  __shared__ Sums tmp[kRowThreads / 64];
+__global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobArgs a) {
+  __shared__ Sums tmp[kJoinThreads / 64];
   __shared__ TopShared sh;
   const int t = blockIdx.x, tid = threadIdx.x;
   const float* row = a.x + t * a.ldx;
+  const uint64_t* keys = a.keys + (int64_t)t * a.parts * kPartGroups;
+  const int groups = a.parts * kPartGroups;
+  // the first of what each later step needs, all on their way together
+  const uint64_t first = a.top_n > 0 && tid < groups ? keys[tid] : 0;
+  const Given given = first_given(a, t, row);
   Sums r{-__builtin_inff(), 0.f, 0.f};
-  for (int p = tid; p < a.parts; p += kRowThreads) {
-    const float* o = a.sums + 4 * ((int64_t)t * a.parts + p);
+  for (int p = tid; p < a.parts; p += kJoinThreads) {
+    const f32x4 o = *reinterpret_cast<const f32x4*>(a.sums + 4 * ((int64_t)t * a.parts + p));
     Sums q{o[0], o[1], o[2]};
     const float m = fmaxf(q.m, r.m);
     shift(q, m);
@@ -373,29 +408,34 @@ __global__ __launch_bounds__(kRowThreads) void k_logprob_join(LogprobArgs a) {
     r.s += q.s;
     r.u += q.u;
   }
-  r = block_join<kRowThreads>(r, tmp);
+  r = block_join<kJoinThreads>(r, tmp);
   const double log_s = log((double)r.s);
-  put_given(a, t, row, r, log_s);
+  put_given<kJoinThreads>(a, t, row, r, log_s, given);
   if (a.top_n > 0) {
-    const uint64_t* keys = a.keys + (int64_t)t * a.parts * kPartGroups;
-    const int groups = a.parts * kPartGroups;
-    uint64_t mine = 0;
-    for (int g = tid; g < groups; g += kRowThreads) mine = max_u64(mine, keys[g]);
-    put_top(a, t, row, r, log_s, mine, kPartVecs * 16, sh,
-            [&](auto f) {
-              for (int g = tid; g < groups; g += kRowThreads) f(keys[g], (uint32_t)g);
-            },
-            [](uint32_t g, int i) {
-              return (int64_t)(g / kPartGroups) * kPartVec + (i >> 4) * kPartThreads + (g % kPartGroups) * 16 +
-                     (i & 15);
-            });
+    uint64_t mine = first;
+    for (int g = tid + kJoinThreads; g < groups; g += kJoinThreads) mine = max_u64(mine, keys[g]);
+    put_top<kJoinThreads>(a, t, row, r, log_s, mine, sh,
+                          [&](auto f) {
+                            f(first, (uint32_t)tid);
+                            for (int g = tid + kJoinThreads; g < groups; g += kJoinThreads) f(keys[g], (uint32_t)g);
+                          },
+                          [](int listed) { return listed * kPartVecs * 16; },
+                          [](const uint32_t* list, int q, int) {
+                            const int g = (int)list[q / (kPartVecs * 16)], i = q % (kPartVecs * 16);
+                            return g / kPartGroups * kPartVec + (i >> 4) * kPartThreads + g % kPartGroups * 16 + (i & 15);
+                          });
   }
 }
 
-// Rows are shared by workgroups where whole rows would leave compute units idle.
+// Rows are shared by workgroups where whole rows leave compute units idle for
+// longer than the second launch takes: rows of more than 2^15 tokens, at most
+// one row for each 1024 of them.  Us as whole rows / in parts, five alternatives:
+// 32003 tokens 1 row 7.3 / 7.3, 64 rows 8.2 / 8.6; 50257 tokens 1 row 9.5 / 7.3,
+// 64 rows 10.7 / 9.8, 128 rows 11.6 / 14.0; 152064 tokens 1 row 17.8 / 7.9, 128
+// rows 22.6 / 21.0, 256 rows 32.9 / 33.7.
 int logprob_parts(int64_t n_tok, int64_t n_vocab) {
-  const int64_t parts = (n_vocab + 4 * kPartVec - 1) / (4 * kPartVec);
-  return n_tok <= 256 && parts >= 3 ? (int)parts : 0;
+  if (n_vocab <= 32768 || n_tok * 1024 > n_vocab || n_tok > 1024) return 0;
+  return (int)((n_vocab + 4 * kPartVec - 1) / (4 * kPartVec));
 }
 
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st) {
@@ -406,7 +446,7 @@ hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(k_logprob_part, dim3((unsigned)a.parts, (unsigned)a.n_tok), dim3(kPartThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_logprob_join, dim3((unsigned)a.n_tok), dim3(kRowThreads), 0, st, a);
+  hipLaunchKernelGGL(k_logprob_join, dim3((unsigned)a.n_tok), dim3(kJoinThreads), 0, st, a);
   return hipGetLastError();
 }
 

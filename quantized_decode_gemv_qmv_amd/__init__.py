@@ -698,30 +698,32 @@ def lora(x: torch.Tensor, ids: torch.Tensor, items, ranks: torch.Tensor | None =
         raise ValueError("x must be [T][K], and there must be an item")
     n_tok, k = x.shape
     first = items[0][0]
-    if first.dim() != 3 or first.dtype not in _FLOATS:
+    kind = first.dtype
+    if first.dim() != 3 or kind not in _FLOATS:
         raise ValueError("a must be [E][R][K] of float16, bfloat16 or float32")
-    kind, (e, rank, _) = first.dtype, first.shape
-    arr = (_LoraItem * len(items))()
-    outs = []
-    for i, (a, b, base, y) in enumerate(items):
-        if a.shape != (e, rank, k) or b.dim() != 3 or b.shape[0] != e or b.shape[2] != rank:
+    e, rank, _ = first.shape
+    n_items = len(items)
+    arr = (_LoraItem * n_items)()
+    outs, seen = [], [x, ids, ranks, scales, ws]
+    for m, (a, b, base, y) in zip(arr, items):
+        bs = b.shape
+        if a.shape != (e, rank, k) or len(bs) != 3 or bs[0] != e or bs[2] != rank:
             raise ValueError("a must be [E][R][K] and b [E][N][R], with the same E and R in every item")
-        n = b.shape[1]
+        n = bs[1]
         if y is None:
             y = _new(x, (n_tok, n), torch.float32, stream)
-        _here(a, b, base, y)
-        shape = (n_tok, n)
-        arr[i] = _LoraItem(_whole(a, kind, "a"), _whole(b, kind, "b"), n, None if base is None else base.data_ptr(),
-                           0 if base is None else _rows(base, shape, "base"), y.data_ptr(), _rows(y, shape, "y"))
+        m.a, m.b, m.n_rows, m.y = _whole(a, kind, "a"), _whole(b, kind, "b"), n, y.data_ptr()
+        m.ldy = _rows(y, (n_tok, n), "y")
+        if base is not None:
+            m.base, m.ldb = base.data_ptr(), _rows(base, (n_tok, n), "base")
+        seen += (a, b, base, y)
         outs.append(y)
     if ws is None:
-        ws = _new(x, (max(lora_workspace_bytes(len(items), rank, n_tok), 1),), torch.uint8, stream)
-    _here(x, ids, ranks, scales, ws)
-    for name, v, dtype, n in (("ids", ids, torch.int32, n_tok), ("ranks", ranks, torch.int32, e),
-                              ("scales", scales, torch.float32, e)):
-        if v is not None and v.numel() != n:
-            raise ValueError(f"{name} must hold {n} values")
-    _check(lib().qmv_lora(_FLOATS[kind], arr, len(items), x.data_ptr(), _rows(x, (n_tok, k), "x"), n_tok, k,
+        ws = _new(x, (max(lora_workspace_bytes(n_items, rank, n_tok), 1),), torch.uint8, stream)
+    _here(*seen)
+    if ids.numel() != n_tok or (ranks is not None and ranks.numel() != e) or (scales is not None and scales.numel() != e):
+        raise ValueError("ids must hold one number a row of x, ranks and scales one an adapter")
+    _check(lib().qmv_lora(_FLOATS[kind], arr, n_items, x.data_ptr(), _rows(x, (n_tok, k), "x"), n_tok, k,
                           _whole(ids, torch.int32, "ids"), e, rank,
                           None if ranks is None else _whole(ranks, torch.int32, "ranks"),
                           None if scales is None else _whole(scales, torch.float32, "scales"),

@@ -1135,22 +1135,22 @@ QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int
       return QMV_ERR_INVALID_ARG;
     if (m.n_rows > QMV_MAX_LORA_ROWS) return QMV_ERR_UNSUPPORTED;
     if (!aligned(m.a, 16) || !aligned(m.b, 16) || !aligned(m.y, 4) || !aligned(m.base, 4)) return QMV_ERR_MISALIGNED;
-    a.item[i] = LoraItem{m.a, m.b, m.base, m.y, m.ldb, m.ldy, static_cast<int>(m.n_rows), 0};
+    a.item[i] = LoraItem{m.a, m.b, m.base, m.y, m.ldb, m.ldy, static_cast<int>(m.n_rows)};
   }
   if (!aligned(x, 16) || ldx % 4 || !aligned(ids, 4) || !aligned(ranks, 4) || !aligned(scales, 4) || !aligned(ws, 256))
     return QMV_ERR_MISALIGNED;
   if (ws_bytes < qmv_lora_workspace_bytes(n_items, max_rank, n_tok)) return QMV_ERR_WORKSPACE;
-  a.n_items = static_cast<int>(n_items);
+  a.call.ids = ids;
+  a.call.ranks = ranks;
+  a.call.h = static_cast<float*>(ws);
+  a.call.n_tok = static_cast<int>(n_tok);
+  a.call.n_items = static_cast<int>(n_items);
+  a.call.adapters = static_cast<int>(n_adapters);
+  a.call.max_rank = static_cast<int>(max_rank);
   a.x = x;
   a.ldx = ldx;
-  a.n_tok = static_cast<int>(n_tok);
   a.k = static_cast<int>(k);
-  a.ids = ids;
-  a.adapters = static_cast<int>(n_adapters);
-  a.max_rank = static_cast<int>(max_rank);
-  a.ranks = ranks;
   a.scales = scales;
-  a.h = static_cast<float*>(ws);
   return hip_status(launch_lora(type, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -23,6 +23,31 @@ constexpr int kUpThreads = 64 * kWaves;
 constexpr int64_t kDownTarget = 512, kUpTarget = 1024;
 constexpr int kUpAhead = 4;    // steps of rows whose loads are in flight
 
+// Kernel arguments.  The host writes them out at some 5 ns a byte, so a call's
+// one to four items do not carry the room of eight (three items as one array of
+// eight in both kernels: 10.7 us of host time a call, 6.0 as it is).
+struct DownArgs {
+  LoraCall c;
+  const float* x;
+  int64_t ldx;
+  int k, slice;
+  const void* a[kLoraItems];
+};
+struct UpItem {
+  const void* b;
+  const float* base;
+  float* y;
+  int64_t ldb, ldy;
+  int n, first;  // first: of its workgroups along the outputs
+};
+template <int N>
+struct UpArgs {
+  LoraCall c;
+  const float* scales;
+  int steps;  // of rows that a workgroup takes
+  UpItem item[N];
+};
+
 // Eight neighbouring weights as they lie in memory.
 template <int DT>
 struct Raw8 {
@@ -79,14 +104,14 @@ __device__ __forceinline__ int slot_token(int slot, int q) {
 }
 
 // The adapters of t's 64 tokens, one a lane (-1: none, -2: past the end).
-__device__ __forceinline__ int ids_of(const LoraArgs& a, int t) {
+__device__ __forceinline__ int ids_of(const LoraCall& a, int t) {
   const int i = (t & ~63) + (threadIdx.x & 63);
   if (i >= a.n_tok) return -2;
   const int id = a.ids[i];
   return id < 0 || id >= a.adapters ? -1 : id;
 }
 
-__device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
+__device__ __forceinline__ int rank_of(const LoraCall& a, int adapter) {
   if (adapter < 0) return 0;
   if (a.ranks == nullptr) return a.max_rank;
   return max(0, min(a.ranks[adapter], a.max_rank));
@@ -95,7 +120,7 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
 // TG tokens by kDownRows rows of A over the columns lo .. hi - 1: the sums in
 // lane row * TG + token.  All loads of a step are in flight together.
 template <int DT, int TG>
-__device__ __forceinline__ float down(const LoraArgs& a, const void* w, const int64_t (&row)[kDownRows],
+__device__ __forceinline__ float down(const DownArgs& a, const void* w, const int64_t (&row)[kDownRows],
                                       const Tile& tile, int lo, int hi) {
   constexpr int U = TG == 1 ? 2 : 1;  // steps whose loads are in flight
   const int lane = threadIdx.x & 63;
@@ -143,26 +168,26 @@ __device__ __forceinline__ float down(const LoraArgs& a, const void* w, const in
 // wave for four rows, the workgroup's waves side by side over the same columns,
 // so that x comes from memory once for 16 rows.
 template <int DT>
-__global__ __launch_bounds__(64 * kWaves) void k_lora_down(LoraArgs a) {
-  const int groups = (a.max_rank + kDownRows * kWaves - 1) / (kDownRows * kWaves);
+__global__ __launch_bounds__(64 * kWaves) void k_lora_down(DownArgs a) {
+  const int groups = (a.c.max_rank + kDownRows * kWaves - 1) / (kDownRows * kWaves);
   const int item = blockIdx.x / groups;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r0 = (blockIdx.x % groups) * kDownRows * kWaves + __builtin_amdgcn_readfirstlane(wave) * kDownRows;
   const int lo = blockIdx.z * a.slice, hi = min(lo + a.slice, a.k);
-  const int id = ids_of(a, slot_token(blockIdx.y, 0));
-  const void* w = a.item[item].a;
+  const int id = ids_of(a.c, slot_token(blockIdx.y, 0));
+  const void* w = a.a[item];
   for (int q = 0; q < 64 / kSlots; ++q) {
     const int t = slot_token(blockIdx.y, q);
-    if (t >= a.n_tok) continue;
+    if (t >= a.c.n_tok) continue;
     const Tile tile = tile_of(id, t);
     const int n = tile.n;
     if (n == 0) continue;
-    const int rank = rank_of(a, tile.adapter);
+    const int rank = rank_of(a.c, tile.adapter);
     if (r0 >= rank) continue;
     int64_t row[kDownRows];
 #pragma unroll
     for (int r = 0; r < kDownRows; ++r)  // rows past the rank repeat the last one
-      row[r] = ((int64_t)tile.adapter * a.max_rank + min(r0 + r, rank - 1)) * a.k;
+      row[r] = ((int64_t)tile.adapter * a.c.max_rank + min(r0 + r, rank - 1)) * a.k;
     float s;
     int tg;
     if (n == 1) {
@@ -178,7 +203,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_down(LoraArgs a) {
     const int r = r0 + lane / tg, j = lane % tg;
     const int at = __shfl(tile.tokens, j);
     if (lane < kDownRows * tg && r < rank && j < n)
-      a.h[(((int64_t)blockIdx.z * a.n_tok + at) * a.n_items + item) * a.max_rank + r] = s;
+      a.c.h[(((int64_t)blockIdx.z * a.c.n_tok + at) * a.c.n_items + item) * a.c.max_rank + r] = s;
   }
 }
 
@@ -223,7 +248,7 @@ __device__ __forceinline__ void fold_group(float* v, int lane, int& at, bool& ow
 // lanes a row, TG tokens at once.  The weights and base of kUpAhead steps are
 // on their way while one is worked on.
 template <int DT, int LPR, int TG>
-__device__ __forceinline__ void up(const LoraArgs& a, const LoraItem& it, int m, const Tile& tile, int rank, float* hs,
+__device__ __forceinline__ void up(const LoraCall& a, const float* scales, const UpItem& it, int m, const Tile& tile, int rank, float* hs,
                                    int n0, int steps) {
   constexpr int OWN = TG > LPR ? TG / LPR : 1;  // values that a lane stores
   constexpr int kStep = kUpThreads / LPR;
@@ -263,7 +288,7 @@ __device__ __forceinline__ void up(const LoraArgs& a, const LoraItem& it, int m,
   };
 #pragma unroll
   for (int i = 0; i < kUpAhead; ++i) fetch(i, b[i], base[i]);
-  const float scale = a.scales != nullptr ? a.scales[tile.adapter] : 1.f;
+  const float scale = scales != nullptr ? scales[tile.adapter] : 1.f;
   __syncthreads();  // the tile before is done with hs
   // h: the slices' sums, eight loads in flight
   const int64_t step = (int64_t)a.n_tok * a.n_items * a.max_rank;
@@ -328,21 +353,22 @@ __device__ __forceinline__ void up(const LoraArgs& a, const LoraItem& it, int m,
 
 // y[t][r] = base[t][r] + scale * sum over i of B[r][i] h[t][i]: a workgroup
 // takes `steps` steps of an item's rows for a tile.
-template <int DT, int LPR>
-__global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraArgs a) {
+template <int DT, int LPR, int N>
+__global__ __launch_bounds__(kUpThreads) void k_lora_up(UpArgs<N> a) {
   __shared__ __align__(16) float hs[kTile * 8 * LPR];
   int m = 0;
-  for (int i = 1; i < a.n_items; ++i) m += (int)blockIdx.x >= a.item[i].first ? 1 : 0;
-  const LoraItem it = a.item[m];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m += i < a.c.n_items && (int)blockIdx.x >= a.item[i].first ? 1 : 0;
+  const UpItem it = a.item[m];
   const int n0 = ((int)blockIdx.x - it.first) * (kUpThreads / LPR) * a.steps;
   const int rows = min(kUpThreads / LPR * a.steps, it.n - n0);
-  const int id = ids_of(a, slot_token(blockIdx.y, 0));
+  const int id = ids_of(a.c, slot_token(blockIdx.y, 0));
   for (int q = 0; q < 64 / kSlots; ++q) {
     const int t = slot_token(blockIdx.y, q);
-    if (t >= a.n_tok) continue;
+    if (t >= a.c.n_tok) continue;
     const Tile tile = tile_of(id, t);
     if (tile.n == 0) continue;
-    const int rank = rank_of(a, tile.adapter);
+    const int rank = rank_of(a.c, tile.adapter);
     if (rank == 0) {  // no adapter: y = base
       if (it.y == it.base) continue;
       for (int j = 0; j < tile.n; ++j) {
@@ -353,9 +379,9 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(LoraArgs a) {
       continue;
     }
     const int steps = (rows + kUpThreads / LPR - 1) / (kUpThreads / LPR);
-    if (tile.n == 1) up<DT, LPR, 1>(a, it, m, tile, rank, hs, n0, steps);
-    else if (tile.n == 2) up<DT, LPR, 2>(a, it, m, tile, rank, hs, n0, steps);
-    else up<DT, LPR, 4>(a, it, m, tile, rank, hs, n0, steps);
+    if (tile.n == 1) up<DT, LPR, 1>(a.c, a.scales, it, m, tile, rank, hs, n0, steps);
+    else if (tile.n == 2) up<DT, LPR, 2>(a.c, a.scales, it, m, tile, rank, hs, n0, steps);
+    else up<DT, LPR, 4>(a.c, a.scales, it, m, tile, rank, hs, n0, steps);
   }
 }
 
@@ -377,45 +403,62 @@ namespace {
 
 unsigned lora_slots(int n_tok) { return n_tok < kSlots ? n_tok : (n_tok + 63) / 64 * kSlots; }
 
-template <int DT, int LPR>
-hipError_t launch_up(LoraArgs& a, hipStream_t st) {
+template <int DT, int LPR, int N>
+hipError_t launch_up(const LoraArgs& a, hipStream_t st) {
   constexpr int kStep = kUpThreads / LPR;
+  UpArgs<N> u{};
+  u.c = a.call;
+  u.scales = a.scales;
   int64_t steps = 0;
-  for (int i = 0; i < a.n_items; ++i) steps += (a.item[i].n + kStep - 1) / kStep;
-  const int64_t want = (kUpTarget + likely_tiles(a.n_tok) - 1) / likely_tiles(a.n_tok);
-  a.steps = (int)((steps + want - 1) / want);
+  for (int i = 0; i < a.call.n_items; ++i) steps += (a.item[i].n + kStep - 1) / kStep;
+  const int64_t tiles = likely_tiles(a.call.n_tok), want = (kUpTarget + tiles - 1) / tiles;
+  u.steps = (int)((steps + want - 1) / want);
   int64_t wgs = 0;
-  for (int i = 0; i < a.n_items; ++i) {
-    a.item[i].first = (int)wgs;
-    wgs += (a.item[i].n + kStep * a.steps - 1) / (kStep * a.steps);
+  for (int i = 0; i < a.call.n_items; ++i) {
+    const LoraItem& m = a.item[i];
+    u.item[i] = UpItem{m.b, m.base, m.y, m.ldb, m.ldy, m.n, (int)wgs};
+    wgs += (m.n + kStep * u.steps - 1) / (kStep * u.steps);
   }
-  hipLaunchKernelGGL((k_lora_up<DT, LPR>), dim3((unsigned)wgs, lora_slots(a.n_tok)), dim3(kUpThreads), 0, st, a);
+  hipLaunchKernelGGL((k_lora_up<DT, LPR, N>), dim3((unsigned)wgs, lora_slots(a.call.n_tok)), dim3(kUpThreads), 0, st, u);
   return hipGetLastError();
 }
 
+template <int DT, int N>
+hipError_t launch_up(const LoraArgs& a, hipStream_t st) {
+  const int v = a.call.max_rank / 8;
+  if (v <= 1) return launch_up<DT, 1, N>(a, st);
+  if (v <= 2) return launch_up<DT, 2, N>(a, st);
+  if (v <= 4) return launch_up<DT, 4, N>(a, st);
+  if (v <= 8) return launch_up<DT, 8, N>(a, st);
+  if (v <= 16) return launch_up<DT, 16, N>(a, st);
+  return launch_up<DT, 32, N>(a, st);
+}
+
 template <int DT>
-hipError_t launch(LoraArgs a, hipStream_t st) {
-  const int rows = kDownRows * kWaves, groups = (a.max_rank + rows - 1) / rows;
-  hipLaunchKernelGGL((k_lora_down<DT>), dim3((unsigned)(a.n_items * groups), lora_slots(a.n_tok), (unsigned)a.slices),
-                     dim3(64 * kWaves), 0, st, a);
+hipError_t launch(LoraArgs& a, hipStream_t st) {
+  DownArgs d{};
+  // slices of whole chunks
+  const int most = (a.k + kChunk - 1) / kChunk;
+  const int want = min(lora_slices(a.call.n_items, a.call.max_rank, a.call.n_tok), most);
+  d.slice = (most + want - 1) / want * kChunk;
+  a.call.slices = (a.k + d.slice - 1) / d.slice;
+  d.c = a.call;
+  d.x = a.x;
+  d.ldx = a.ldx;
+  d.k = a.k;
+  for (int i = 0; i < a.call.n_items; ++i) d.a[i] = a.item[i].a;
+  const int rows = kDownRows * kWaves, groups = (a.call.max_rank + rows - 1) / rows;
+  hipLaunchKernelGGL((k_lora_down<DT>),
+                     dim3((unsigned)(a.call.n_items * groups), lora_slots(a.call.n_tok), (unsigned)a.call.slices),
+                     dim3(64 * kWaves), 0, st, d);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int v = a.max_rank / 8;
-  if (v <= 1) return launch_up<DT, 1>(a, st);
-  if (v <= 2) return launch_up<DT, 2>(a, st);
-  if (v <= 4) return launch_up<DT, 4>(a, st);
-  if (v <= 8) return launch_up<DT, 8>(a, st);
-  if (v <= 16) return launch_up<DT, 16>(a, st);
-  return launch_up<DT, 32>(a, st);
+  return a.call.n_items <= 4 ? launch_up<DT, 4>(a, st) : launch_up<DT, kLoraItems>(a, st);
 }
 
 }  // namespace
 
-hipError_t launch_lora(int type, LoraArgs a, hipStream_t st) {
-  const int most = (a.k + kChunk - 1) / kChunk;
-  a.slices = min(lora_slices(a.n_items, a.max_rank, a.n_tok), most);
-  a.slice = (most + a.slices - 1) / a.slices * kChunk;
-  a.slices = (a.k + a.slice - 1) / a.slice;
+hipError_t launch_lora(int type, LoraArgs& a, hipStream_t st) {
   if (type == kF16) return launch<kF16>(a, st);
   if (type == kBF16) return launch<kBF16>(a, st);
   return launch<kF32>(a, st);

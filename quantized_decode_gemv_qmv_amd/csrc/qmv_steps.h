@@ -38,26 +38,27 @@ struct LoraItem {
   float* y;
   int64_t ldb, ldy;
   int n;
-  int first;  // of its workgroups along the outputs
+};
+// What both kernels need.
+struct LoraCall {
+  const int32_t* ids;    // [n_tok]
+  const int32_t* ranks;  // NULL, or [adapters]
+  float* h;              // [slices][n_tok][n_items][max_rank]
+  int n_tok, n_items, adapters, max_rank;
+  int slices;  // of k; set at launch
 };
 struct LoraArgs {
+  LoraCall call;
   LoraItem item[kLoraItems];
-  int n_items;
   const float* x;
   int64_t ldx;
-  int n_tok, k;
-  const int32_t* ids;  // [n_tok]
-  int adapters, max_rank;
-  const int32_t* ranks;  // NULL, or [adapters]
-  const float* scales;   // NULL, or [adapters]
-  float* h;              // [slices][n_tok][n_items][max_rank]
-  int slices, slice;     // of k, and their length; set at launch
-  int steps;             // of rows that a workgroup of the outputs takes; set at launch
+  int k;
+  const float* scales;  // NULL, or [adapters]
 };
 // The most partial sums of h that a call makes (k alone can make them fewer).
 constexpr int kLoraMaxSlices = 16;
 int lora_slices(int64_t n_items, int64_t max_rank, int64_t n_tok);
-hipError_t launch_lora(int type, LoraArgs a, hipStream_t st);
+hipError_t launch_lora(int type, LoraArgs& a, hipStream_t st);
 
 // Routing to experts.
 struct GateArgs {

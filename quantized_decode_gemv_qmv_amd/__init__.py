@@ -807,47 +807,51 @@ def token_logprobs(logits: torch.Tensor, given: torch.Tensor | None = None, top_
     without it each row has one, which is slow for few rows."""
     if logits.dim() == 1:
         logits = logits.view(1, -1)
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be [T][V]")
-    t, v = logits.shape
-    n_given = 0
+    t, v = shape
+    ask = []  # the caller's own outputs
+    n_given, gp, lp, ip, tp = 0, None, None, None, None
     if given is not None:
-        if given.shape[:1] != (t,) or given.dim() > 2:
+        gs = given.shape
+        if gs[:1] != (t,) or len(gs) > 2:
             raise ValueError("given must be [T] or [T][G]")
-        n_given = 1 if given.dim() == 1 else given.shape[1]
+        n_given, gp = 1 if len(gs) == 1 else gs[1], _whole(given, torch.int32, "given")
         if logprobs is None:
-            logprobs = _new(logits, given.shape, torch.float32, stream)
-        if logprobs.shape != given.shape:
-            raise ValueError("logprobs must have the shape of given")
+            logprobs = _new(logits, gs, torch.float32, stream)
+        else:
+            ask.append((logprobs, gs, torch.float32, "logprobs"))
+        lp = logprobs.data_ptr()
     elif logprobs is not None:
         raise ValueError("logprobs without given")
     if entropy is None:
         entropy = _new(logits, (t,), torch.float32, stream)
-    if entropy.shape != (t,):
-        raise ValueError("entropy must be [T]")
+    else:
+        ask.append((entropy, (t,), torch.float32, "entropy"))
     if top_n > 0:
         if top_ids is None:
             top_ids = _new(logits, (t, top_n), torch.int32, stream)
+        else:
+            ask.append((top_ids, (t, top_n), torch.int32, "top_ids"))
         if top_logprobs is None:
             top_logprobs = _new(logits, (t, top_n), torch.float32, stream)
-        if top_ids.shape != (t, top_n) or top_logprobs.shape != (t, top_n):
-            raise ValueError("top_ids and top_logprobs must be [T][top_n]")
+        else:
+            ask.append((top_logprobs, (t, top_n), torch.float32, "top_logprobs"))
+        ip, tp = top_ids.data_ptr(), top_logprobs.data_ptr()
     elif top_ids is not None or top_logprobs is not None:
         raise ValueError("top_ids or top_logprobs without top_n")
-    if ws is not None and ws.numel() == 0:
-        ws = None
-    _here(logits, given, logprobs, entropy, top_ids, top_logprobs, ws)
-
-    def whole(x, dtype, name):
-        return None if x is None else _whole(x, dtype, name)
-
-    _check(lib().qmv_token_logprobs(logits.data_ptr(), _rows(logits, (t, v), "logits"), t, v, scale,
-                                    whole(given, torch.int32, "given"), n_given,
-                                    whole(logprobs, torch.float32, "logprobs"),
-                                    _whole(entropy, torch.float32, "entropy"), top_n,
-                                    whole(top_ids, torch.int32, "top_ids"),
-                                    whole(top_logprobs, torch.float32, "top_logprobs"), whole(ws, torch.uint8, "ws"),
-                                    0 if ws is None else ws.numel(), _stream(stream)), "qmv_token_logprobs")
+    wp, ws_bytes = None, 0
+    if ws is not None and ws.numel() > 0:
+        wp, ws_bytes = _whole(ws, torch.uint8, "ws"), ws.numel()
+    _here(logits, given, ws, *(x[0] for x in ask))
+    for x, want, dtype, name in ask:
+        _whole(x, dtype, name)
+        if x.shape != want:
+            raise ValueError(f"{name} must be {list(want)}")
+    _check(lib().qmv_token_logprobs(logits.data_ptr(), _rows(logits, shape, "logits"), t, v, scale, gp, n_given, lp,
+                                    entropy.data_ptr(), top_n, ip, tp, wp, ws_bytes, _stream(stream)),
+           "qmv_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
 
 

@@ -1222,7 +1222,7 @@ static qmv_status check_logprob_sizes(int64_t n_tok, int64_t n_vocab, int64_t to
 
 // Workspace of qmv_token_logprobs: arrival counters of the rows, then the
 // parts' keys and sums.
-constexpr int64_t kLogprobCounterBytes = 4096;
+constexpr int64_t kLogprobCounterBytes = 4 * kCounterStep * kLogprobCounters;
 
 QMV_API size_t qmv_token_logprobs_workspace_bytes(int64_t n_tok, int64_t n_vocab, int64_t top_n) {
   if (check_logprob_sizes(n_tok, n_vocab, top_n) != QMV_OK) return 0;
@@ -1261,6 +1261,7 @@ QMV_API qmv_status qmv_token_logprobs(const float* logits, int64_t ldl, int64_t 
   if (ws != nullptr) {
     if (ws_bytes < qmv_token_logprobs_workspace_bytes(n_tok, n_vocab, top_n)) return QMV_ERR_WORKSPACE;
     a.parts = logprob_parts(n_tok, n_vocab);
+    a.cnt = static_cast<int*>(ws);
     uint8_t* b = static_cast<uint8_t*>(ws) + kLogprobCounterBytes;
     a.keys = reinterpret_cast<uint64_t*>(b);
     a.sums = reinterpret_cast<float*>(b + n_tok * a.parts * 8 * kPartGroupsOfRow);

@@ -17,9 +17,8 @@ namespace {
 
 constexpr float kLog2e = 1.44269504f;
 constexpr int kRowThreads = 512;   // of a workgroup that has a whole row
-constexpr int kJoinThreads = 512;  // of one that joins a row
-constexpr int kPartThreads = 256;
-constexpr int kPartVecs = 4;       // 16-byte vectors of a thread
+constexpr int kPartThreads = 512;  // of one that has a part, and may join the row
+constexpr int kPartVecs = 2;       // 16-byte vectors of a thread
 constexpr int kPartVec = kPartThreads * kPartVecs;  // vectors of a part
 constexpr int kPartGroups = kPartThreads / 16;      // groups of 16 lanes
 static_assert(kPartGroups == kPartGroupsOfRow, "the workspace holds a part's keys");
@@ -344,10 +343,23 @@ __global__ __launch_bounds__(kRowThreads) void k_logprob_row(LogprobArgs a) {
   }
 }
 
+namespace {
+
+__device__ __forceinline__ void put_device(uint64_t* p, uint64_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t get_device(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+}  // namespace
+
 // One part of a row, held in registers: its sums and the largest of each 16
-// lanes' 64 vectors.
+// lanes' vectors.  The last workgroup of a row to arrive joins its parts.
 __global__ __launch_bounds__(kPartThreads) void k_logprob_part(LogprobArgs a) {
   __shared__ Sums tmp[kPartThreads / 64];
+  __shared__ TopShared sh;
+  __shared__ int s_last;
   const int t = blockIdx.y, p = blockIdx.x, tid = threadIdx.x;
   const float* row = a.x + t * a.ldx;
   const int vecs = (a.n_vocab + 3) / 4, i0 = p * kPartVec + tid;
@@ -373,68 +385,73 @@ __global__ __launch_bounds__(kPartThreads) void k_logprob_part(LogprobArgs a) {
   Sums r{m, 0.f, 0.f};
 #pragma unroll
   for (int b = 0; b < kPartVecs; ++b) add(r.s, r.u, v[b], a.scale, ref);
-  const int64_t slot = (int64_t)t * a.parts + p;
+  uint64_t* keys = a.keys + (int64_t)t * a.parts * kPartGroups;
+  uint64_t* sums = reinterpret_cast<uint64_t*>(a.sums) + 2 * (int64_t)t * a.parts;
   if (a.top_n > 0) {
     const uint64_t key = row_max(i0 < vecs ? key_of(top, (uint32_t)(4 * at + 3)) : 0);
-    if ((tid & 15) == 0) a.keys[slot * kPartGroups + (tid >> 4)] = key;
+    if ((tid & 15) == 0) put_device(keys + p * kPartGroups + (tid >> 4), key);
   }
   r = block_join<kPartThreads>(r, tmp);
   if (tid == 0) {
-    float* o = a.sums + 4 * slot;
-    o[0] = r.m;
-    o[1] = r.s;
-    o[2] = r.u;
+    put_device(sums + 2 * p, ((uint64_t)__float_as_uint(r.s) << 32) | __float_as_uint(r.m));
+    put_device(sums + 2 * p + 1, __float_as_uint(r.u));
   }
-}
-
-// Joins a row's parts.
-__global__ __launch_bounds__(kJoinThreads) void k_logprob_join(LogprobArgs a) {
-  __shared__ Sums tmp[kJoinThreads / 64];
-  __shared__ TopShared sh;
-  const int t = blockIdx.x, tid = threadIdx.x;
-  const float* row = a.x + t * a.ldx;
-  const uint64_t* keys = a.keys + (int64_t)t * a.parts * kPartGroups;
-  const int groups = a.parts * kPartGroups;
-  // the first of what each later step needs, all on their way together
-  const uint64_t first = a.top_n > 0 && tid < groups ? keys[tid] : 0;
+  // Keys and sums are device-scope atomic accesses (written through and
+  // reloaded by the L2s), so waiting for this lane's own stores before the
+  // barrier and the counter's update orders them without a device-scope fence.
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (tid == 0) s_last = atomicAdd(&a.cnt[t * kCounterStep], 1) == a.parts - 1;
+  __syncthreads();
+  if (!s_last) return;
+  if (tid == 0) atomicExch(&a.cnt[t * kCounterStep], 0);
+  // what each later step needs first, on its way together
   const Given given = first_given(a, t, row);
-  Sums r{-__builtin_inff(), 0.f, 0.f};
-  for (int p = tid; p < a.parts; p += kJoinThreads) {
-    const f32x4 o = *reinterpret_cast<const f32x4*>(a.sums + 4 * ((int64_t)t * a.parts + p));
-    Sums q{o[0], o[1], o[2]};
-    const float m = fmaxf(q.m, r.m);
-    shift(q, m);
-    shift(r, m);
+  const int groups = a.parts * kPartGroups;
+  uint64_t first[3] = {0, 0, 0};
+  if (a.top_n > 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (tid + i * kPartThreads < groups) first[i] = get_device(keys + tid + i * kPartThreads);
+  }
+  r = Sums{-__builtin_inff(), 0.f, 0.f};
+  for (int i = tid; i < a.parts; i += kPartThreads) {
+    const uint64_t ms = get_device(sums + 2 * i), u = get_device(sums + 2 * i + 1);
+    Sums q{__uint_as_float((uint32_t)ms), __uint_as_float((uint32_t)(ms >> 32)), __uint_as_float((uint32_t)u)};
+    const float big = fmaxf(q.m, r.m);
+    shift(q, big);
+    shift(r, big);
     r.s += q.s;
     r.u += q.u;
   }
-  r = block_join<kJoinThreads>(r, tmp);
+  r = block_join<kPartThreads>(r, tmp);
   const double log_s = log((double)r.s);
-  put_given<kJoinThreads>(a, t, row, r, log_s, given);
-  if (a.top_n > 0) {
-    uint64_t mine = first;
-    for (int g = tid + kJoinThreads; g < groups; g += kJoinThreads) mine = max_u64(mine, keys[g]);
-    put_top<kJoinThreads>(a, t, row, r, log_s, mine, sh,
-                          [&](auto f) {
-                            f(first, (uint32_t)tid);
-                            for (int g = tid + kJoinThreads; g < groups; g += kJoinThreads) f(keys[g], (uint32_t)g);
-                          },
-                          [](int listed) { return listed * kPartVecs * 16; },
-                          [](const uint32_t* list, int q, int) {
-                            const int g = (int)list[q / (kPartVecs * 16)], i = q % (kPartVecs * 16);
-                            return g / kPartGroups * kPartVec + (i >> 4) * kPartThreads + g % kPartGroups * 16 + (i & 15);
-                          });
-  }
+  put_given<kPartThreads>(a, t, row, r, log_s, given);
+  if (a.top_n == 0) return;
+  uint64_t mine = max_u64(max_u64(first[0], first[1]), first[2]);
+  for (int g = tid + 3 * kPartThreads; g < groups; g += kPartThreads) mine = max_u64(mine, get_device(keys + g));
+  put_top<kPartThreads>(a, t, row, r, log_s, mine, sh,
+                        [&](auto f) {
+#pragma unroll
+                          for (int i = 0; i < 3; ++i) f(first[i], (uint32_t)(tid + i * kPartThreads));
+                          for (int g = tid + 3 * kPartThreads; g < groups; g += kPartThreads)
+                            f(get_device(keys + g), (uint32_t)g);
+                        },
+                        [](int listed) { return listed * kPartVecs * 16; },
+                        [](const uint32_t* list, int q, int) {
+                          const int g = (int)list[q / (kPartVecs * 16)], i = q % (kPartVecs * 16);
+                          return g / kPartGroups * kPartVec + (i >> 4) * kPartThreads + g % kPartGroups * 16 + (i & 15);
+                        });
 }
 
 // Rows are shared by workgroups where whole rows leave compute units idle for
-// longer than the second launch takes: rows of more than 2^15 tokens, at most
-// one row for each 1024 of them.  Us as whole rows / in parts, five alternatives:
-// 32003 tokens 1 row 7.3 / 7.3, 64 rows 8.2 / 8.6; 50257 tokens 1 row 9.5 / 7.3,
-// 64 rows 10.7 / 9.8, 128 rows 11.6 / 14.0; 152064 tokens 1 row 17.8 / 7.9, 128
-// rows 22.6 / 21.0, 256 rows 32.9 / 33.7.
+// longer than joining takes: rows of more than 2^15 tokens, at most one row for
+// each 2048 of them.  Us as whole rows / in parts, five alternatives: 32003 tokens
+// 1 row 7.3 / 7.3; 50257 tokens 1 row 9.6 / 7.3, 16 rows 10.0 / 7.7; 152064
+// tokens 1 row 17.8 / 7.4, 16 rows 18.5 / 10.0, 64 rows 21.7 / 17.3, 128 rows
+// 22.7 / 32.7.
 int logprob_parts(int64_t n_tok, int64_t n_vocab) {
-  if (n_vocab <= 32768 || n_tok * 1024 > n_vocab || n_tok > 1024) return 0;
+  if (n_vocab <= 32768 || n_tok * 2048 > n_vocab || n_tok > kLogprobCounters) return 0;
   return (int)((n_vocab + 4 * kPartVec - 1) / (4 * kPartVec));
 }
 
@@ -444,9 +461,6 @@ hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   hipLaunchKernelGGL(k_logprob_part, dim3((unsigned)a.parts, (unsigned)a.n_tok), dim3(kPartThreads), 0, st, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_logprob_join, dim3((unsigned)a.n_tok), dim3(kJoinThreads), 0, st, a);
   return hipGetLastError();
 }
 

@@ -87,7 +87,7 @@ int gate_slices(int64_t n_tok, int64_t n_experts);
 hipError_t launch_router_gate(GateArgs a, hipStream_t st);
 
 // Log probabilities of a row of logits.
-constexpr int kPartGroupsOfRow = 16;  // keys of a part
+constexpr int kPartGroupsOfRow = 32;  // keys of a part
 struct LogprobArgs {
   const float* x;  // [n_tok][ldx]
   int64_t ldx;
@@ -102,7 +102,12 @@ struct LogprobArgs {
   int parts;        // of a row, 0: whole rows
   float* sums;      // [n_tok][parts][4]
   uint64_t* keys;   // [n_tok][parts][kPartGroupsOfRow]
+  int* cnt;         // arrival counters, kCounterStep apart
 };
+// Counters lie 256 bytes apart: the memory side takes the atomics of one line
+// one after the other.
+constexpr int kCounterStep = 64;
+constexpr int kLogprobCounters = 256;  // rows in parts at most
 // Parts of a row that a call with a workspace makes; 0: none.
 int logprob_parts(int64_t n_tok, int64_t n_vocab);
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st);

@@ -72,7 +72,7 @@ def check(qmv, x, given=None, n=0, scale=1.0, pad=0, ws="both"):
         else:
             assert ids is None and top is None
         if with_ws:
-            assert not buf[:4096].any()
+            assert not buf[:65536].any()
 
 
 def make(t, v, seed=0, spread=3.0):
@@ -206,4 +206,4 @@ def test_graphs_streams_and_one_workspace():
         again = qmv.token_logprobs(x[:n_tok], given[:n_tok], top_n=n, ws=other, stream=side)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(again, want)), rep
-    assert not ws[:4096].any()
+    assert not ws[:65536].any()

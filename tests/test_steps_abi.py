@@ -158,7 +158,7 @@ def test_logprob_refusals(change, status):
 
 def test_logprob_workspace_and_binding():
     f = q.token_logprobs_workspace_bytes
-    assert f(1, 152064, 20) > 4096 and f(5000, 152064, 20) == 0 and f(1, 30000, 20) == 0
+    assert f(1, 152064, 20) > 65536 and f(5000, 152064, 20) == 0 and f(1, 30000, 20) == 0
     for bad in ((0, 152064, 0), (1, 0, 0), (1, 152064, -1), (1, 152064, 33), (65537, 152064, 0), (1, (1 << 24) + 1, 0)):
         assert f(*bad) == 0, bad
     x = torch.zeros(2, 64)

@@ -561,7 +561,8 @@ qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, int64_t n_
  * rope     : HOST struct, read during the call only; its pointers are device
  *            pointers.
  *   pos       int32 [n_axes][n_tok]; a row whose position on the first axis is
- *             negative belongs to no sequence: it is neither read nor written.
+ *             negative belongs to no sequence: its values do not matter, and
+ *             its outputs are not written.
  *             NULL only if rot_dim is 0.
  *   inv_freq  fp32 [rot_dim / 2], finite.  NULL only if rot_dim is 0.
  *   pair_axis NULL (the first axis), or int32 [rot_dim / 2].

@@ -68,10 +68,13 @@ __device__ __forceinline__ double lanes_sum(double v) {
 // that cos and sin are made once a wave.  Squares are summed in fp64 (each is
 // exact, no length of x overflows it).  A pair's other half lies in the lane
 // (neighbouring pairs) or comes through LDS.  One read and one write of every
-// value bound it.
+// value bound it: 8192 tokens x 72 heads of 128 dims 132 us, 4.6 TB/s (a large
+// copy reaches 4.9), the vector ALU busy for half of that; one token 3.8 us, the
+// launch and two loads in a row.  All loads of a wave's first passes are on
+// their way before its angles are made (152 -> 146 us).
 // V4: the halves' distance is a multiple of four dims, so the partner values
-// of a lane are one 16-byte vector.
-template <int L, bool ADJACENT, bool V4>
+// of a lane are one 16-byte vector.  NT: stores that pass the caches by.
+template <int L, bool ADJACENT, bool V4, bool NT>
 __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a) {
   constexpr int HPP = 64 / L;  // heads of a pass
   __shared__ __align__(16) float s_x[kHeadWaves][256];
@@ -79,57 +82,67 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
   const int64_t g = (int64_t)blockIdx.x * kHeadWaves + wave;
   const int t = (int)(g / a.waves_a_token), part = (int)(g % a.waves_a_token);
   if (t >= a.n_tok) return;  // no barrier below
-  if (a.pos != nullptr && a.pos[t] < 0) return;
   const int d0 = 4 * (lane % L);
   const bool on = d0 < a.dim;
-  const int half = a.rot / 2;
-  float c[4], s[4];
-  int other[4];
-  bool turn[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int d = d0 + j;
-    c[j] = 1.f;
-    s[j] = 0.f;
-    turn[j] = false;
-    other[j] = d0 + j;
-    if (d < a.rot) {
-      const int i = ADJACENT ? d >> 1 : (d < half ? d : d - half);
-      const bool first = ADJACENT ? (d & 1) == 0 : d < half;
-      if (!ADJACENT) other[j] = first ? d + half : d - half;
-      const int axis = a.axis != nullptr ? a.axis[i] : 0;
-      if (axis >= 0 && axis < a.n_axes) {
-        turn[j] = true;
-        if (ADJACENT && (j & 1)) {  // the pair's angle once
-          c[j] = c[j - 1];
-          s[j] = -s[j - 1];
-        } else {
-          cos_sin(a.pos[(int64_t)axis * a.n_tok + t], a.freq[i], c[j], s[j]);
-          c[j] *= a.scale;
-          s[j] *= first ? -a.scale : a.scale;
-        }
-      }
+  const int total = a.heads[0] + a.heads[1];
+  // a pass's values; the next ones are on their way while a batch is worked on
+  auto fetch = [&](int p, f32x4& v) {
+    const int h = p * HPP + lane / L;
+    v = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (p < a.passes && h < total && on) {
+      const int m = h >= a.heads[0];
+      v = *reinterpret_cast<const f32x4*>(a.x[m] + t * a.ldx[m] + (int64_t)(h - m * a.heads[0]) * a.dim + d0);
     }
-  }
+  };
+  f32x4 x[kHeadBatch];
+#pragma unroll
+  for (int b = 0; b < kHeadBatch; ++b) fetch(part + b * a.waves_a_token, x[b]);
   f32x4 w[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     w[m] = f32x4{1.f, 1.f, 1.f, 1.f};
     if (a.w[m] != nullptr && on) w[m] = *reinterpret_cast<const f32x4*>(a.w[m] + d0);
   }
-  const int total = a.heads[0] + a.heads[1];
-  const int base = 4 * (lane & ~(L - 1));  // of the head's values in s_x
-  for (int p0 = part; p0 < a.passes; p0 += a.waves_a_token * kHeadBatch) {
-    f32x4 x[kHeadBatch];
+  // the pair of each of the lane's dims: its frequency and axis
+  const int half = a.rot / 2;
+  const int first_pos = a.pos != nullptr ? a.pos[t] : 0;
+  float freq[4];
+  int axis[4], other[4];
 #pragma unroll
-    for (int b = 0; b < kHeadBatch; ++b) {
-      const int h = (p0 + b * a.waves_a_token) * HPP + lane / L;
-      x[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (h < total && on) {
-        const int m = h >= a.heads[0];
-        x[b] = *reinterpret_cast<const f32x4*>(a.x[m] + t * a.ldx[m] + (int64_t)(h - m * a.heads[0]) * a.dim + d0);
+  for (int j = 0; j < 4; ++j) {
+    const int d = d0 + j;
+    axis[j] = -1;
+    other[j] = d;
+    freq[j] = 0.f;
+    if (d < a.rot) {
+      const int i = ADJACENT ? d >> 1 : (d < half ? d : d - half);
+      if (!ADJACENT) other[j] = d < half ? d + half : d - half;
+      freq[j] = a.freq[i];
+      axis[j] = a.axis != nullptr ? a.axis[i] : 0;
+      if (axis[j] >= a.n_axes) axis[j] = -1;
+    }
+  }
+  if (first_pos < 0) return;
+  float c[4], s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    c[j] = 1.f;
+    s[j] = 0.f;
+    if (axis[j] >= 0) {
+      if (ADJACENT && (j & 1)) {  // the pair's angle once
+        c[j] = c[j - 1];
+        s[j] = -s[j - 1];
+      } else {
+        const int pos = axis[j] == 0 ? first_pos : a.pos[(int64_t)axis[j] * a.n_tok + t];
+        cos_sin(pos, freq[j], c[j], s[j]);
+        const bool first = ADJACENT || d0 + j < half;
+        c[j] *= a.scale;
+        s[j] *= first ? -a.scale : a.scale;
       }
     }
+  }
+  const int base = 4 * (lane & ~(L - 1));  // of the head's values in s_x
+  for (int p0 = part; p0 < a.passes; p0 += a.waves_a_token * kHeadBatch) {
 #pragma unroll
     for (int b = 0; b < kHeadBatch; ++b) {
       const int p = p0 + b * a.waves_a_token;
@@ -138,6 +151,7 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
       const int m = h >= a.heads[0];
       const f32x4 wm = m ? w[1] : w[0];
       f32x4 v = x[b];
+      fetch(p + kHeadBatch * a.waves_a_token, x[b]);
       double ss = 0.0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) ss += (double)v[j] * (double)v[j];
@@ -167,36 +181,50 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
         __builtin_amdgcn_wave_barrier();
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = turn[j] ? fmaf(v[j], c[j], q[j] * s[j]) : v[j];
-      if (h < total && on)
-        *reinterpret_cast<f32x4*>(a.y[m] + t * a.ldy[m] + (int64_t)(h - m * a.heads[0]) * a.dim + d0) = v;
+      for (int j = 0; j < 4; ++j) v[j] = axis[j] >= 0 ? fmaf(v[j], c[j], q[j] * s[j]) : v[j];
+      if (h < total && on) {
+        f32x4* y = reinterpret_cast<f32x4*>(a.y[m] + t * a.ldy[m] + (int64_t)(h - m * a.heads[0]) * a.dim + d0);
+        if constexpr (NT)
+          __builtin_nontemporal_store(v, y);
+        else
+          *y = v;
+      }
     }
   }
 }
 
 namespace {
 
+template <int L, bool ADJACENT, bool V4>
+hipError_t launch(const HeadsArgs& a, unsigned grid, bool stream, hipStream_t st) {
+  const dim3 b(64 * kHeadWaves);
+  if (stream)
+    hipLaunchKernelGGL((k_head_norm_rope<L, ADJACENT, V4, true>), dim3(grid), b, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_head_norm_rope<L, ADJACENT, V4, false>), dim3(grid), b, 0, st, a);
+  return hipGetLastError();
+}
+
 template <int L>
 hipError_t launch(HeadsArgs a, int cus, hipStream_t st) {
   const int total = a.heads[0] + a.heads[1], hpp = 64 / L;
   a.passes = (total + hpp - 1) / hpp;
-  // a wave a pass until the device is full, then several, which share the angles
-  int64_t per = (int64_t)a.n_tok * a.passes / ((int64_t)cus * 16);
-  per = per < 1 ? 1 : (per > kHeadBatch ? kHeadBatch : per);
+  // a wave a pass until a compute unit has eight, then up to eight passes a wave,
+  // which share the angles (8192 x 72 heads, four / eight passes: 161 / 151 us)
+  int64_t per = (int64_t)a.n_tok * a.passes / ((int64_t)cus * 8);
+  per = per < 1 ? 1 : (per > 8 ? 8 : per);
   // below 2^25 waves, which is 2^31 threads (65536 tokens have 65536 at least)
   const int64_t least = ((int64_t)a.n_tok * a.passes >> 24) + 1;
   if (per < least) per = least;
   a.waves_a_token = (int)((a.passes + per - 1) / per);
   const int64_t waves = (int64_t)a.n_tok * a.waves_a_token;
-  const int64_t grid = (waves + kHeadWaves - 1) / kHeadWaves;
-  const dim3 b(64 * kHeadWaves);
-  if (a.adjacent)
-    hipLaunchKernelGGL((k_head_norm_rope<L, true, true>), dim3((unsigned)grid), b, 0, st, a);
-  else if (a.rot % 8 == 0)
-    hipLaunchKernelGGL((k_head_norm_rope<L, false, true>), dim3((unsigned)grid), b, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_head_norm_rope<L, false, false>), dim3((unsigned)grid), b, 0, st, a);
-  return hipGetLastError();
+  const unsigned grid = (unsigned)((waves + kHeadWaves - 1) / kHeadWaves);
+  // outputs that the caches would not keep for the next step pass them by (10 MB
+  // 9.6 -> 8.6 us, 20 MB 16.6 -> 11.6, 302 MB 136 -> 130)
+  const bool stream = (int64_t)a.n_tok * total * a.dim * 4 > (int64_t(8) << 20);
+  if (a.adjacent) return launch<L, true, true>(a, grid, stream, st);
+  if (a.rot % 8 == 0) return launch<L, false, true>(a, grid, stream, st);
+  return launch<L, false, false>(a, grid, stream, st);
 }
 
 }  // namespace

@@ -1112,9 +1112,14 @@ static qmv_status check_lora_sizes(int64_t n_items, int64_t max_rank, int64_t n_
   return QMV_OK;
 }
 
+// Workspace of qmv_lora: the list of tiles, 32 bytes for each token, then the
+// slices of h.
+static int64_t lora_tile_bytes(int64_t n_tok) { return (n_tok + 63) / 64 * 64 * 32; }
+
 QMV_API size_t qmv_lora_workspace_bytes(int64_t n_items, int64_t max_rank, int64_t n_tok) {
   if (check_lora_sizes(n_items, max_rank, n_tok) != QMV_OK) return 0;
-  return static_cast<size_t>(align256(4 * n_items * max_rank * n_tok * lora_slices(n_items, max_rank, n_tok)));
+  return static_cast<size_t>(lora_tile_bytes(n_tok) +
+                             align256(4 * n_items * max_rank * n_tok * lora_slices(n_items, max_rank, n_tok)));
 }
 
 QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_items, const float* x,
@@ -1142,7 +1147,8 @@ QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int
   if (ws_bytes < qmv_lora_workspace_bytes(n_items, max_rank, n_tok)) return QMV_ERR_WORKSPACE;
   a.call.ids = ids;
   a.call.ranks = ranks;
-  a.call.h = static_cast<float*>(ws);
+  a.call.tiles = static_cast<int32_t*>(ws);
+  a.call.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + lora_tile_bytes(n_tok));
   a.call.n_tok = static_cast<int>(n_tok);
   a.call.n_items = static_cast<int>(n_items);
   a.call.adapters = static_cast<int>(n_adapters);

@@ -2,12 +2,21 @@
 // projections, for gfx950: y = base + scale * B (A x), each token with the A
 // and B of its own adapter.
 //
-// Two launches: k_lora_down makes h = A x for all items, k_lora_up the outputs.
-// Both work on tiles of up to kTile tokens that share an adapter, found from
-// the ids of their aligned 64 tokens: a workgroup belongs to a token, and goes
-// on if as many tokens before it as a whole number of tiles hold its adapter.
-// So an adapter's weights are read once a tile, and tokens of different
-// adapters cost no more than their own weights.
+// Two launches: k_lora_down makes h = A x for all items and a list of the tiles
+// that it found, k_lora_up the outputs.  A tile is up to four tokens that share
+// an adapter among an aligned 64, so an adapter's weights are read once a tile, and
+// tokens of different adapters cost no more than their own weights.  Weights enter
+// as the fp32 numbers that they are and products and sums are fp32: nothing is
+// rounded but sums.
+//
+// Bounds: two launches of some 2 us, each with a chain of loads (ids, ranks,
+// weights; tile, h and weights) before it streams; for many adapters their bytes.
+// 16 adapters of ranks up to 64 on 2 x 14336 rows (62 MB): 20.5 us, 3 TB/s; 64
+// tokens of three adapters on 4096 x 14336: 11.6; 700 tokens: 23.
+// Matrix instructions were measured and dropped: their operands want neighbouring
+// lanes on different rows, which loads at a quarter of the rate (down, 700 tokens
+// 10.4 -> 19 to 21 us), and through LDS the outputs of single tokens took longer
+// (16 adapters 22.1 -> 24.2).
 #include "qmv_device.h"
 #include "qmv_steps.h"
 
@@ -17,11 +26,15 @@ namespace {
 
 constexpr int kTile = 4;       // tokens of a tile
 constexpr int kWaves = 4;      // of a workgroup
+constexpr int kSlots = 24;     // workgroups that share 64 tokens: one each for the 16 to 23 tiles of up to eight adapters
 constexpr int kDownRows = 4;   // of A in a wave
 constexpr int kChunk = 512;    // columns of a wave's step: 8 a lane
 constexpr int kUpThreads = 64 * kWaves;
-constexpr int64_t kDownTarget = 512, kUpTarget = 1024;
 constexpr int kUpAhead = 4;    // steps of rows whose loads are in flight
+// Workgroups of a launch, about: more of them start more often, fewer leave
+// compute units idle (outputs' target 256 / 512 / 1024 / 2048: 16 adapters 25 /
+// 20.5 / 21.6 / 23.7 us, 700 tokens 26 / 23.0 / 23.7 / 24.9).
+constexpr int64_t kDownTarget = 512, kUpTarget = 512;
 
 // Kernel arguments.  The host writes them out at some 5 ns a byte, so a call's
 // one to four items do not carry the room of eight (three items as one array of
@@ -31,6 +44,7 @@ struct DownArgs {
   const float* x;
   int64_t ldx;
   int k, slice;
+  const float* scales;
   const void* a[kLoraItems];
 };
 struct UpItem {
@@ -43,7 +57,6 @@ struct UpItem {
 template <int N>
 struct UpArgs {
   LoraCall c;
-  const float* scales;
   int steps;  // of rows that a workgroup takes
   UpItem item[N];
 };
@@ -74,47 +87,65 @@ struct Raw8 {
 struct Tile {
   int n;        // tokens, 0: another workgroup has them
   int adapter;  // -1: none
+  int rank;
   int tokens;   // lane j: the j-th one
   __device__ __forceinline__ int token(int j) const { return __builtin_amdgcn_readlane(tokens, min(j, n - 1)); }
 };
 
-// The tile that starts at token t, in every wave alike; id: the adapter of
-// token `lane` of t's 64.
-__device__ __forceinline__ Tile tile_of(int id, int t) {
-  const int lane = threadIdx.x & 63, at = t & 63;
-  Tile r;
-  r.adapter = __builtin_amdgcn_readlane(id, at);
-  uint64_t m = __ballot(id == r.adapter);
-  const int before = __popcll(m & ((1ull << at) - 1));
+// The aligned 64 tokens of a workgroup, one a lane.
+struct Block {
+  int base;
+  int adapter;  // -1: none, -2: past the end
+  int rank;
+  bool start;   // whether the token may start a tile
+  int place;    // among those
+};
+
+__device__ __forceinline__ Block block_of(const LoraCall& a, int base) {
+  const int lane = threadIdx.x & 63;
+  Block b;
+  b.base = base;
+  b.adapter = -2;
+  if (base + lane < a.n_tok) {
+    const int id = a.ids[base + lane];
+    b.adapter = id < 0 || id >= a.adapters ? -1 : id;
+  }
+  b.rank = 0;
+  if (b.adapter >= 0) b.rank = a.ranks != nullptr ? max(0, min(a.ranks[b.adapter], a.max_rank)) : a.max_rank;
+  // a token starts a tile if a whole number of tiles of its adapter come before
+  // it; from the ninth adapter on, and where every token has a workgroup of its
+  // own, every token may (tile_of looks)
+  uint64_t left = __ballot(b.adapter != -2), starts = 0;
+  const uint64_t below = (1ull << lane) - 1;
+  for (int i = 0; i < 8 && left != 0 && a.n_tok > a.slots; ++i) {
+    const int id = __builtin_amdgcn_readlane(b.adapter, __ffsll((unsigned long long)left) - 1);
+    const uint64_t m = __ballot(b.adapter == id);
+    starts |= __ballot(b.adapter == id && __popcll(m & below) % kTile == 0);
+    left &= ~m;
+  }
+  starts |= left;
+  b.start = (starts >> lane) & 1;
+  b.place = (int)__popcll(starts & below);
+  return b;
+}
+
+// The block's tile at place `place`; false: there is none any more.
+__device__ __forceinline__ bool tile_of(const Block& b, int place, Tile& r) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t here = __ballot(b.start && b.place == place);
+  if (here == 0) return false;
+  const int at = __ffsll((unsigned long long)here) - 1;
+  r.adapter = __builtin_amdgcn_readlane(b.adapter, at);
+  uint64_t m = __ballot(b.adapter == r.adapter);
+  const int before = (int)__popcll(m & ((1ull << at) - 1));
   m &= ~0ull << at;
   r.n = before % kTile == 0 ? min((int)__popcll(m), kTile) : 0;
   // each of them writes its number to the lane of its place; the others go to
   // the last lane, which is a place only if there are no others
-  const int place = (m >> lane) & 1 ? (int)__popcll(m & ((1ull << lane) - 1)) : 63;
-  r.tokens = __builtin_amdgcn_ds_permute(4 * place, (t & ~63) + lane);
-  return r;
-}
-
-// The tokens that a slot looks at, one of each 16 of its 64: tiles of tokens
-// side by side begin 8 apart, those of tokens in turn at neighbours, and both
-// kinds fall on different slots.
-constexpr int kSlots = 16;
-__device__ __forceinline__ int slot_token(int slot, int q) {
-  return (slot / kSlots) * 64 + q * kSlots + ((slot - 3 * q) & (kSlots - 1));
-}
-
-// The adapters of t's 64 tokens, one a lane (-1: none, -2: past the end).
-__device__ __forceinline__ int ids_of(const LoraCall& a, int t) {
-  const int i = (t & ~63) + (threadIdx.x & 63);
-  if (i >= a.n_tok) return -2;
-  const int id = a.ids[i];
-  return id < 0 || id >= a.adapters ? -1 : id;
-}
-
-__device__ __forceinline__ int rank_of(const LoraCall& a, int adapter) {
-  if (adapter < 0) return 0;
-  if (a.ranks == nullptr) return a.max_rank;
-  return max(0, min(a.ranks[adapter], a.max_rank));
+  const int to = (m >> lane) & 1 ? (int)__popcll(m & ((1ull << lane) - 1)) : 63;
+  r.tokens = __builtin_amdgcn_ds_permute(4 * to, b.base + lane);
+  r.rank = __builtin_amdgcn_readlane(b.rank, at);
+  return true;
 }
 
 // TG tokens by kDownRows rows of A over the columns lo .. hi - 1: the sums in
@@ -174,16 +205,20 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_down(DownArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r0 = (blockIdx.x % groups) * kDownRows * kWaves + __builtin_amdgcn_readfirstlane(wave) * kDownRows;
   const int lo = blockIdx.z * a.slice, hi = min(lo + a.slice, a.k);
-  const int id = ids_of(a.c, slot_token(blockIdx.y, 0));
+  const Block block = block_of(a.c, (int)blockIdx.y / a.c.slots * 64);
   const void* w = a.a[item];
-  for (int q = 0; q < 64 / kSlots; ++q) {
-    const int t = slot_token(blockIdx.y, q);
-    if (t >= a.c.n_tok) continue;
-    const Tile tile = tile_of(id, t);
-    const int n = tile.n;
-    if (n == 0) continue;
-    const int rank = rank_of(a.c, tile.adapter);
-    if (r0 >= rank) continue;
+  Tile tile;
+  int p = (int)blockIdx.y % a.c.slots;
+  for (; tile_of(block, p, tile); p += a.c.slots) {
+    const int n = tile.n, rank = tile.rank;
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x < 8) {
+      const int f = threadIdx.x;
+      const int token = __shfl(tile.tokens, max(0, min(f - 4, n - 1)));  // with every lane that holds one on
+      const int scale = tile.adapter >= 0 && a.scales != nullptr ? __float_as_int(a.scales[tile.adapter]) : 0x3F800000;
+      const int v = f == 0 ? n : f == 1 ? tile.adapter : f == 2 ? rank : f == 3 ? scale : token;
+      a.c.tiles[8 * (block.base + p) + f] = v;
+    }
+    if (n == 0 || r0 >= rank) continue;
     int64_t row[kDownRows];
 #pragma unroll
     for (int r = 0; r < kDownRows; ++r)  // rows past the rank repeat the last one
@@ -205,6 +240,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_lora_down(DownArgs a) {
     if (lane < kDownRows * tg && r < rank && j < n)
       a.c.h[(((int64_t)blockIdx.z * a.c.n_tok + at) * a.c.n_items + item) * a.c.max_rank + r] = s;
   }
+  // the end of the slot's list
+  if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && p < 64) a.c.tiles[8 * (block.base + p)] = -1;
 }
 
 namespace {
@@ -248,7 +285,7 @@ __device__ __forceinline__ void fold_group(float* v, int lane, int& at, bool& ow
 // lanes a row, TG tokens at once.  The weights and base of kUpAhead steps are
 // on their way while one is worked on.
 template <int DT, int LPR, int TG>
-__device__ __forceinline__ void up(const LoraCall& a, const float* scales, const UpItem& it, int m, const Tile& tile, int rank, float* hs,
+__device__ __forceinline__ void up(const LoraCall& a, float scale, const UpItem& it, int m, const Tile& tile, int rank, float* hs,
                                    int n0, int steps) {
   constexpr int OWN = TG > LPR ? TG / LPR : 1;  // values that a lane stores
   constexpr int kStep = kUpThreads / LPR;
@@ -288,7 +325,6 @@ __device__ __forceinline__ void up(const LoraCall& a, const float* scales, const
   };
 #pragma unroll
   for (int i = 0; i < kUpAhead; ++i) fetch(i, b[i], base[i]);
-  const float scale = scales != nullptr ? scales[tile.adapter] : 1.f;
   __syncthreads();  // the tile before is done with hs
   // h: the slices' sums, eight loads in flight
   const int64_t step = (int64_t)a.n_tok * a.n_items * a.max_rank;
@@ -362,13 +398,22 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(UpArgs<N> a) {
   const UpItem it = a.item[m];
   const int n0 = ((int)blockIdx.x - it.first) * (kUpThreads / LPR) * a.steps;
   const int rows = min(kUpThreads / LPR * a.steps, it.n - n0);
-  const int id = ids_of(a.c, slot_token(blockIdx.y, 0));
-  for (int q = 0; q < 64 / kSlots; ++q) {
-    const int t = slot_token(blockIdx.y, q);
-    if (t >= a.c.n_tok) continue;
-    const Tile tile = tile_of(id, t);
+  const int base = (int)blockIdx.y / a.c.slots * 64;
+  for (int p = (int)blockIdx.y % a.c.slots; p < 64; p += a.c.slots) {
+    // the list that k_lora_down wrote, through the scalar cache
+    typedef const __attribute__((address_space(4))) int* Scalars;
+    const Scalars f = (Scalars)(uintptr_t)(a.c.tiles + 8 * (base + p));
+    Tile tile;
+    tile.n = f[0];
+    tile.adapter = f[1];
+    tile.rank = f[2];
+    const float scale = __int_as_float(f[3]);
+    const int lane = threadIdx.x & 3;
+    const int t0 = f[4], t1 = f[5], t2 = f[6], t3 = f[7];
+    tile.tokens = lane < 2 ? (lane == 0 ? t0 : t1) : (lane == 2 ? t2 : t3);
+    if (tile.n < 0) break;
     if (tile.n == 0) continue;
-    const int rank = rank_of(a.c, tile.adapter);
+    const int rank = tile.rank;
     if (rank == 0) {  // no adapter: y = base
       if (it.y == it.base) continue;
       for (int j = 0; j < tile.n; ++j) {
@@ -379,9 +424,9 @@ __global__ __launch_bounds__(kUpThreads) void k_lora_up(UpArgs<N> a) {
       continue;
     }
     const int steps = (rows + kUpThreads / LPR - 1) / (kUpThreads / LPR);
-    if (tile.n == 1) up<DT, LPR, 1>(a.c, a.scales, it, m, tile, rank, hs, n0, steps);
-    else if (tile.n == 2) up<DT, LPR, 2>(a.c, a.scales, it, m, tile, rank, hs, n0, steps);
-    else up<DT, LPR, 4>(a.c, a.scales, it, m, tile, rank, hs, n0, steps);
+    if (tile.n == 1) up<DT, LPR, 1>(a.c, scale, it, m, tile, rank, hs, n0, steps);
+    else if (tile.n == 2) up<DT, LPR, 2>(a.c, scale, it, m, tile, rank, hs, n0, steps);
+    else up<DT, LPR, 4>(a.c, scale, it, m, tile, rank, hs, n0, steps);
   }
 }
 
@@ -401,14 +446,11 @@ int lora_slices(int64_t n_items, int64_t max_rank, int64_t n_tok) {
 
 namespace {
 
-unsigned lora_slots(int n_tok) { return n_tok < kSlots ? n_tok : (n_tok + 63) / 64 * kSlots; }
-
 template <int DT, int LPR, int N>
 hipError_t launch_up(const LoraArgs& a, hipStream_t st) {
   constexpr int kStep = kUpThreads / LPR;
   UpArgs<N> u{};
   u.c = a.call;
-  u.scales = a.scales;
   int64_t steps = 0;
   for (int i = 0; i < a.call.n_items; ++i) steps += (a.item[i].n + kStep - 1) / kStep;
   const int64_t tiles = likely_tiles(a.call.n_tok), want = (kUpTarget + tiles - 1) / tiles;
@@ -419,7 +461,7 @@ hipError_t launch_up(const LoraArgs& a, hipStream_t st) {
     u.item[i] = UpItem{m.b, m.base, m.y, m.ldb, m.ldy, m.n, (int)wgs};
     wgs += (m.n + kStep * u.steps - 1) / (kStep * u.steps);
   }
-  hipLaunchKernelGGL((k_lora_up<DT, LPR, N>), dim3((unsigned)wgs, lora_slots(a.call.n_tok)), dim3(kUpThreads), 0, st, u);
+  hipLaunchKernelGGL((k_lora_up<DT, LPR, N>), dim3((unsigned)wgs, (unsigned)((a.call.n_tok + 63) / 64 * a.call.slots)), dim3(kUpThreads), 0, st, u);
   return hipGetLastError();
 }
 
@@ -442,14 +484,16 @@ hipError_t launch(LoraArgs& a, hipStream_t st) {
   const int want = min(lora_slices(a.call.n_items, a.call.max_rank, a.call.n_tok), most);
   d.slice = (most + want - 1) / want * kChunk;
   a.call.slices = (a.k + d.slice - 1) / d.slice;
+  a.call.slots = min(a.call.n_tok, kSlots);
   d.c = a.call;
   d.x = a.x;
   d.ldx = a.ldx;
   d.k = a.k;
+  d.scales = a.scales;
   for (int i = 0; i < a.call.n_items; ++i) d.a[i] = a.item[i].a;
   const int rows = kDownRows * kWaves, groups = (a.call.max_rank + rows - 1) / rows;
   hipLaunchKernelGGL((k_lora_down<DT>),
-                     dim3((unsigned)(a.call.n_items * groups), lora_slots(a.call.n_tok), (unsigned)a.call.slices),
+                     dim3((unsigned)(a.call.n_items * groups), (unsigned)((a.call.n_tok + 63) / 64 * a.call.slots), (unsigned)a.call.slices),
                      dim3(64 * kWaves), 0, st, d);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -44,8 +44,9 @@ struct LoraCall {
   const int32_t* ids;    // [n_tok]
   const int32_t* ranks;  // NULL, or [adapters]
   float* h;              // [slices][n_tok][n_items][max_rank]
+  int32_t* tiles;        // [n_tok rounded up to 64][8]: a tile's tokens, adapter, rank, scale and the tokens
   int n_tok, n_items, adapters, max_rank;
-  int slices;  // of k; set at launch
+  int slices, slots;  // of k, and of each 64 tokens; set at launch
 };
 struct LoraArgs {
   LoraCall call;

@@ -1,12 +1,12 @@
 """Low-rank adapters against the formula in 64 bits.
 
 Tolerance, in half steps u = 2^-24: weights are exact as fp32 numbers, so only
-sums round.  A lane adds its products in turn, m = 8 * ceil(k / 2048) of them at
-most (8 columns a step, a step every 2048, the slices sharing them), then 6
-steps over the wave, 3 over the waves, and up to 15 over the slices: h is off by
-(m + 24) u of its terms' sizes S_h.  The second product sums 8 terms in a lane, 5
-steps over the lanes, the scale and the base: 16 u of its own terms.  Together
-(m + 40) u * |scale| * sum |b| S_h, and u of the base."""
+sums round.  A lane adds its products in turn, at most m = 8 * ceil(k / 512) of
+them (8 columns of each 512, if one slice has them all), then 6 steps over the
+wave and up to 15 over the slices: h is off by (m + 21) u of its terms' sizes
+S_h.  The second product sums 8 terms in a lane, 5 steps over the lanes, the
+scale and the base: 15 u of its own terms.  Together less than (m + 40) u *
+|scale| * sum |b| S_h, and u of the base."""
 import numpy as np
 import pytest
 import torch
@@ -24,7 +24,7 @@ def reference(x, a, b, base, ids, ranks, scales):
     k = x.shape[1]
     x, y = x.double(), base.double().clone()
     tol = U * y.abs()
-    m = 8 * -(-k // 2048) + 40
+    m = 8 * -(-k // 512) + 40
     for e in sorted(set(ids.tolist())):
         if not 0 <= e < a.shape[0]:
             continue

@@ -616,8 +616,9 @@ qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq,
  *   y        fp32 [n_tok][ldy]; columns 0 .. n_rows - 1 of every row are
  *            written.  y of different items must not overlap.
  * x        : fp32 [n_tok][ldx] (device), 16-byte aligned, ldx >= k, ldx % 4 == 0.
- * ids      : int32 [n_tok] (device), in any order; rows are dealt to
- *            workgroups by eight of one adapter among each aligned 64, so an
+ * ids      : int32 [n_tok] (device), in any order; an adapter's weights are
+ *            read once for up to four of its rows among each aligned 64 (from
+ *            the ninth adapter there on only for neighbouring ones), so an
  *            adapter's rows are best neighbours.
  * ranks    : NULL (max_rank), or int32 [n_adapters] (device), taken as within
  *            0 .. max_rank;  scales: NULL (1), or fp32 [n_adapters] (device).

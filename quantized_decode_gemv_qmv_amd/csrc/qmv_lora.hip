@@ -27,6 +27,7 @@ namespace {
 constexpr int kTile = 4;       // tokens of a tile
 constexpr int kWaves = 4;      // of a workgroup
 constexpr int kSlots = 24;     // workgroups that share 64 tokens: one each for the 16 to 23 tiles of up to eight adapters
+constexpr int kCounted = 8;    // adapters of 64 tokens whose tokens are counted
 constexpr int kDownRows = 4;   // of A in a wave
 constexpr int kChunk = 512;    // columns of a wave's step: 8 a lane
 constexpr int kUpThreads = 64 * kWaves;
@@ -95,12 +96,19 @@ struct Tile {
 // The aligned 64 tokens of a workgroup, one a lane.
 struct Block {
   int base;
-  int adapter;  // -1: none, -2: past the end
+  int adapter;     // -1: none, -2: past the end
   int rank;
-  bool start;   // whether the token may start a tile
-  int place;    // among those
+  bool start;      // whether the token may start a tile
+  int place;       // among those
+  uint64_t apart;  // tokens whose tiles are of neighbours only
+  uint64_t turns;  // tokens whose adapter is not the one before's
 };
 
+// Tiles are of four tokens of an adapter wherever they stand among the 64 for
+// the first kCounted adapters, whose tokens are counted; of neighbours for others,
+// which takes no loop (a batch of many requests has each one's tokens side by
+// side).  Where every token has a workgroup of its own each may start a tile, and
+// tile_of looks whether it does.
 __device__ __forceinline__ Block block_of(const LoraCall& a, int base) {
   const int lane = threadIdx.x & 63;
   Block b;
@@ -112,18 +120,25 @@ __device__ __forceinline__ Block block_of(const LoraCall& a, int base) {
   }
   b.rank = 0;
   if (b.adapter >= 0) b.rank = a.ranks != nullptr ? max(0, min(a.ranks[b.adapter], a.max_rank)) : a.max_rank;
-  // a token starts a tile if a whole number of tiles of its adapter come before
-  // it; from the ninth adapter on, and where every token has a workgroup of its
-  // own, every token may (tile_of looks)
-  uint64_t left = __ballot(b.adapter != -2), starts = 0;
   const uint64_t below = (1ull << lane) - 1;
-  for (int i = 0; i < 8 && left != 0 && a.n_tok > a.slots; ++i) {
-    const int id = __builtin_amdgcn_readlane(b.adapter, __ffsll((unsigned long long)left) - 1);
-    const uint64_t m = __ballot(b.adapter == id);
-    starts |= __ballot(b.adapter == id && __popcll(m & below) % kTile == 0);
-    left &= ~m;
+  uint64_t left = __ballot(b.adapter != -2), starts = left;
+  b.apart = b.turns = 0;
+  if (a.n_tok > a.slots) {  // uniform
+    starts = 0;
+    for (int i = 0; i < kCounted && left != 0; ++i) {
+      const int id = __builtin_amdgcn_readlane(b.adapter, __ffsll((unsigned long long)left) - 1);
+      const uint64_t m = __ballot(b.adapter == id);
+      starts |= __ballot(b.adapter == id && __popcll(m & below) % kTile == 0);
+      left &= ~m;
+    }
+    if (left != 0) {
+      const int before = __shfl_up(b.adapter, 1, 64);
+      b.turns = __ballot(lane == 0 || before != b.adapter);
+      const int first = 63 - __clzll((long long)(b.turns & (below | 1ull << lane)));
+      b.apart = left;
+      starts |= __ballot((lane - first) % kTile == 0) & left;
+    }
   }
-  starts |= left;
   b.start = (starts >> lane) & 1;
   b.place = (int)__popcll(starts & below);
   return b;
@@ -136,6 +151,13 @@ __device__ __forceinline__ bool tile_of(const Block& b, int place, Tile& r) {
   if (here == 0) return false;
   const int at = __ffsll((unsigned long long)here) - 1;
   r.adapter = __builtin_amdgcn_readlane(b.adapter, at);
+  r.rank = __builtin_amdgcn_readlane(b.rank, at);
+  if ((b.apart >> at) & 1) {  // neighbours, up to where the adapter changes
+    const uint64_t next = at < 63 ? b.turns >> (at + 1) : 0;
+    r.n = min(next != 0 ? __ffsll((unsigned long long)next) : 64 - at, kTile);
+    r.tokens = b.base + at + lane;
+    return true;
+  }
   uint64_t m = __ballot(b.adapter == r.adapter);
   const int before = (int)__popcll(m & ((1ull << at) - 1));
   m &= ~0ull << at;
@@ -144,7 +166,6 @@ __device__ __forceinline__ bool tile_of(const Block& b, int place, Tile& r) {
   // the last lane, which is a place only if there are no others
   const int to = (m >> lane) & 1 ? (int)__popcll(m & ((1ull << lane) - 1)) : 63;
   r.tokens = __builtin_amdgcn_ds_permute(4 * to, b.base + lane);
-  r.rank = __builtin_amdgcn_readlane(b.rank, at);
   return true;
 }
 

@@ -89,11 +89,12 @@ def test_lengths(k):
 
 
 @pytest.mark.parametrize("t", [1, 2, 3, 7, 8, 9, 16, 63, 64, 65, 130, 500])
-@pytest.mark.parametrize("pattern", ["one", "own", "mixed", "runs"])
+@pytest.mark.parametrize("pattern", ["one", "own", "mixed", "runs", "short runs", "any"])
 def test_tokens(t, pattern):
     qmv = need_gpu()
     ids = {"one": [1] * t, "own": [i % 20 for i in range(t)], "mixed": [-1 if i % 4 == 3 else (7 * i) % 5 for i in range(t)],
-           "runs": [i * 6 // t for i in range(t)]}[pattern]
+           "runs": [i * 6 // t for i in range(t)], "short runs": [i // 5 % 20 for i in range(t)],
+           "any": [(i * i + i // 3) % 23 - 2 for i in range(t)]}[pattern]
     check(qmv, t, 256, [48, 300], 16, 20, ids, "bf16", ranks=[16, 3, 0, 8, 13] * 4, base="same")
 
 

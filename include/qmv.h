@@ -611,10 +611,12 @@ qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq,
  *            an adapter's rank on may hold anything;
  *   n_rows   1 .. QMV_MAX_LORA_ROWS;
  *   base     NULL (zeros), or fp32 [n_tok][ldb], the projection's output; it
- *            may be the item's y with ldb == ldy, else it must not overlap any
- *            item's y;
+ *            may be the item's y with ldb == ldy, else it shares no value with
+ *            any item's y;
  *   y        fp32 [n_tok][ldy]; columns 0 .. n_rows - 1 of every row are
- *            written.  y of different items must not overlap.
+ *            written.  y of different items share no value (they may be columns
+ *            of the same rows, with one stride).  Where these rules are broken:
+ *            QMV_ERR_INVALID_ARG.
  * x        : fp32 [n_tok][ldx] (device), 16-byte aligned, ldx >= k, ldx % 4 == 0.
  * ids      : int32 [n_tok] (device), in any order; an adapter's weights are
  *            read once for up to four of its rows among each aligned 64 (from

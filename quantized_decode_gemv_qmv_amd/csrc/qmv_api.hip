@@ -1122,6 +1122,19 @@ QMV_API size_t qmv_lora_workspace_bytes(int64_t n_items, int64_t max_rank, int64
                              align256(4 * n_items * max_rank * n_tok * lora_slices(n_items, max_rank, n_tok)));
 }
 
+// Whether two fp32 row arrays of n_tok rows share a value: their extents meet,
+// and they are not columns beside each other of rows of one stride.
+static bool rows_meet(const float* p, int64_t ldp, int64_t np, const float* q, int64_t ldq, int64_t nq, int64_t n_tok) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t ea = a + 4 * static_cast<uintptr_t>((n_tok - 1) * ldp + np);
+  const uintptr_t eb = b + 4 * static_cast<uintptr_t>((n_tok - 1) * ldq + nq);
+  if (ea <= b || eb <= a) return false;
+  if (ldp != ldq) return true;
+  const int64_t at = static_cast<int64_t>(a < b ? b - a : a - b) / 4 % ldp;  // of the later one in the earlier one's rows
+  const int64_t first = a < b ? np : nq, second = a < b ? nq : np;
+  return at < first || at + second > ldp;
+}
+
 QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_items, const float* x,
                             int64_t ldx, int64_t n_tok, int64_t k, const int32_t* ids, int64_t n_adapters,
                             int64_t max_rank, const int32_t* ranks, const float* scales, void* ws, size_t ws_bytes,
@@ -1142,6 +1155,15 @@ QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int
     if (!aligned(m.a, 16) || !aligned(m.b, 16) || !aligned(m.y, 4) || !aligned(m.base, 4)) return QMV_ERR_MISALIGNED;
     a.item[i] = LoraItem{m.a, m.b, m.base, m.y, m.ldb, m.ldy, static_cast<int>(m.n_rows)};
   }
+  for (int64_t i = 0; i < n_items; ++i)
+    for (int64_t j = 0; j < n_items; ++j) {
+      const qmv_lora_item &p = items[i], &q = items[j];
+      if (i < j && rows_meet(p.y, p.ldy, p.n_rows, q.y, q.ldy, q.n_rows, n_tok)) return QMV_ERR_INVALID_ARG;
+      // the base of an item may be its own y, and nothing else that is written
+      if (q.base != nullptr && !(i == j && q.base == q.y && q.ldb == q.ldy) &&
+          rows_meet(p.y, p.ldy, p.n_rows, q.base, q.ldb, q.n_rows, n_tok))
+        return QMV_ERR_INVALID_ARG;
+    }
   if (!aligned(x, 16) || ldx % 4 || !aligned(ids, 4) || !aligned(ranks, 4) || !aligned(scales, 4) || !aligned(ws, 256))
     return QMV_ERR_MISALIGNED;
   if (ws_bytes < qmv_lora_workspace_bytes(n_items, max_rank, n_tok)) return QMV_ERR_WORKSPACE;

@@ -145,10 +145,11 @@ def test_scores_that_vanish():
     assert gi.cpu().tolist() == [[0, 1, 2, 3]] and torch.equal(gw.cpu(), torch.full((1, 4), 0.75))
 
 
-@pytest.mark.parametrize("t,k", [(1, 4096), (2, 1056), (7, 64), (64, 2048)])
-def test_q8_of_x(t, k):
+@pytest.mark.parametrize("t,k,e", [(1, 4096, 40), (2, 1056, 40), (7, 64, 40), (64, 2048, 40), (4, 4128, 5), (3, 96, 4),
+                                   (40, 288, 17)])
+def test_q8_of_x(t, k, e):
     qmv = need_gpu()
-    x, wr, _ = make(t, k, 40)
+    x, wr, _ = make(t, k, e)
     xq = torch.zeros(qmv.act_bytes(t, k), dtype=torch.uint8, device="cuda")
     check(qmv, x, wr, 4, xq=xq)
     want = qmv.quantize_act(torch.from_numpy(x).cuda())

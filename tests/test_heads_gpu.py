@@ -121,6 +121,12 @@ def test_rows_of_no_sequence_and_far_positions():
     check(qmv, 6, 4, 2, 96, 96, axes=3, pos=pos)
 
 
+def test_the_most_tokens():
+    qmv = need_gpu()
+    check(qmv, 65536, 1, 1, 16, 16)
+    check(qmv, 300, 257, 31, 32, 24, adjacent=True)
+
+
 def test_values_at_the_ends():
     """Rows of zeros, of values whose squares leave fp32's range either way."""
     qmv = need_gpu()

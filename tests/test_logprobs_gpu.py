@@ -98,6 +98,14 @@ def test_rows(t):
     check(qmv, x, rng.integers(0, 20011, (t, 3)), 7, scale=1.25)
 
 
+def test_the_most_rows_and_tokens():
+    qmv = need_gpu()
+    x, rng = make(65536, 40)
+    check(qmv, x, rng.integers(0, 40, (65536, 1)), 2)
+    x, rng = make(2, 3_000_001)
+    check(qmv, x, rng.integers(0, 3_000_001, (2, 700)), 32)
+
+
 @pytest.mark.parametrize("v", [300, 5000, 60000])
 def test_ties(v):
     """Few different values: the lower index first, also where all are equal or zeros differ in sign."""

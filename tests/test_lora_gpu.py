@@ -106,6 +106,33 @@ def test_many_rows_and_items():
     check(qmv, 300, 128, [5000], 32, 2, [i // 150 for i in range(300)], "bf16", base="none", scaled=False)
 
 
+def test_the_most_tokens():
+    qmv = need_gpu()
+    check(qmv, 4096, 64, [70, 33], 8, 7, [i // 613 - 1 for i in range(4096)], "f16", base="same")
+    check(qmv, 4095, 32, [9], 16, 300, [(i * 7) % 300 for i in range(4095)], "bf16", ranks=[1 + i % 16 for i in range(300)])
+
+
+def test_columns_of_one_buffer():
+    """The items' outputs as columns of the same rows, in place, and a row stride on base alone."""
+    qmv = need_gpu()
+    t, k, r = 6, 128, 8
+    g = torch.Generator().manual_seed(1)
+    x, ids = torch.randn(t, k, generator=g), torch.tensor([0, 1, 1, -1, 0, 0], dtype=torch.int32)
+    outs = [50, 7, 20]
+    ab = [(torch.randn(2, r, k, generator=g), torch.randn(2, n, r, generator=g)) for n in outs]
+    whole0 = torch.randn(t, 80, generator=g)
+    want = [reference(x, a, b, whole0[:, at:at + b.shape[1]], ids, [r, r], [1.0, 1.0])
+            for (a, b), at in zip(ab, (0, 50, 57))]
+    whole, other = whole0.cuda(), whole0.cuda()
+    dab = [(a.cuda(), b.cuda()) for a, b in ab]
+    cols = [whole[:, 0:50], whole[:, 50:57], whole[:, 57:77]]
+    qmv.lora(x.cuda(), ids.cuda(), [(a, b, c, c) for (a, b), c in zip(dab, cols)])
+    apart = qmv.lora(x.cuda(), ids.cuda(), [(a, b, other[:, at:at + b.shape[1]], None) for (a, b), at in zip(dab, (0, 50, 57))])
+    for c, o, (y, tol) in zip(cols, apart, want):
+        assert torch.all((c.double().cpu() - y).abs() <= tol) and torch.equal(c, o)
+    assert torch.equal(whole[:, 77:].cpu(), whole0[:, 77:])
+
+
 def test_no_adapter_at_all():
     qmv = need_gpu()
     for base in ("same", "other", "none"):

@@ -79,6 +79,32 @@ def test_lora_refusals(change, status):
     assert lora(**change) == status
 
 
+def test_lora_overlaps():
+    """Items that write the same values, or another's base, are refused; columns of the same rows are not."""
+    def call(items, t=3):
+        arr = (q._LoraItem * len(items))(*[q._LoraItem(FAKE, FAKE, n, b, lb, y, ly) for n, b, lb, y, ly in items])
+        return q.lib().qmv_lora(0, arr, len(items), FAKE, 64, t, 64, FAKE, 4, 16, None, None, FAKE, 1 << 40, None)
+
+    y = FAKE + (1 << 20)
+    bad = [[(100, None, 0, y, 100), (100, None, 0, y, 100)],
+           [(100, None, 0, y, 200), (100, None, 0, y + 4 * 99, 200)],
+           [(100, None, 0, y + 4 * 99, 200), (100, None, 0, y, 200)],
+           [(100, None, 0, y, 200), (101, None, 0, y + 400, 200)],
+           [(100, None, 0, y, 200), (100, None, 0, y + 400, 201)],
+           [(100, y + 4, 100, y, 100)], [(100, y, 101, y, 100)],
+           [(100, None, 0, y, 100), (100, y, 100, y + (1 << 20), 100)],
+           [(100, y + (1 << 20), 100, y, 100), (100, None, 0, y + (1 << 20), 100)]]
+    for items in bad:
+        assert call(items) == INVALID, items
+    if torch.cuda.is_available():
+        return  # right ones would run on these addresses
+    good = [[(100, None, 0, y, 200), (100, None, 0, y + 400, 200)], [(100, y, 100, y, 100)],
+            [(100, y, 100, y, 100), (50, y + 1200, 50, y + 1200, 50)],
+            [(100, y, 200, y, 200), (100, y + 400, 200, y + 400, 200)]]
+    for items in good:
+        assert call(items) == 5, items  # QMV_ERR_HIP: the launch found no device
+
+
 def test_lora_workspace_and_binding():
     f = q.lora_workspace_bytes
     assert f(1, 16, 1) >= 64 and f(8, 256, 4096) >= 8 * 256 * 4096 * 4

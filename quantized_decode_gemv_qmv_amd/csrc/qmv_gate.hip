@@ -5,6 +5,13 @@
 // is held in fp64: fp32 logits of another summing order would pick others
 // where two choices are within 1e-7 of each other, and the routed matvecs of
 // two steps over the same token would differ.
+//
+// Up to four tokens one launch does it all (1 x 128 experts of 4096 columns 6.3 us:
+// the launch, one load of the weights, the handoff to the last workgroup of some 2
+// us, its choice of some 2); more tokens take the matrix unit and a second launch
+// (64 x 256 of 5120: 14.5 us, of which 8.7 and 6.6; the products alone would take
+// 2.1).  On the vector ALU the logits of 64 tokens took 15.4 us; chosen by the last
+// workgroup of 16 tokens, 64 tokens took 18 to 26 us in one launch.
 #include "qmv_device.h"
 #include "qmv_steps.h"
 
@@ -82,10 +89,10 @@ __device__ __forceinline__ int wave_first(uint64_t key, int index) {
   return __ffsll((unsigned long long)b) - 1;
 }
 
-// One token's choice by one wave.  l: the lane's logits, of experts lane + 64 i;
-// sc: an array of 64 PER doubles in LDS of this wave's own.
+// One token's choice by one wave.  l and bias: the lane's logits and biases, of
+// experts lane + 64 i; sc: an array of 64 PER doubles in LDS of this wave's own.
 template <int PER>
-__device__ __forceinline__ void gate_select(const GateArgs& a, int t, double (&l)[PER], double* sc) {
+__device__ __forceinline__ void gate_select(const GateArgs& a, int t, double (&l)[PER], const float (&bias)[PER], double* sc) {
   const int lane = threadIdx.x & 63;
   // scores
   if (a.sigmoid) {
@@ -113,7 +120,7 @@ __device__ __forceinline__ void gate_select(const GateArgs& a, int t, double (&l
     const int e = lane + 64 * i;
     key[i] = 0;
     if (e < a.n_experts) {
-      const double c = l[i] + (a.bias != nullptr ? (double)a.bias[e] : 0.0);
+      const double c = l[i] + (double)bias[i];
       key[i] = place(c);
       if (a.groups > 1) sc[e] = c;
     }
@@ -139,45 +146,89 @@ __device__ __forceinline__ void gate_select(const GateArgs& a, int t, double (&l
       v = fmax(fmin(u, p), fmax(v, q));
       u = fmax(u, p);
     }
-    uint64_t worth = g < a.groups && first == 0 ? place(a.group_best == 2 ? u + v : u) : 0;
-    uint64_t kept = 0;
-    for (int j = 0; j < a.top_groups; ++j) {
-      const int w = wave_first(worth, lane);
-      kept |= 1ull << (w >> shift);
-      if (lane == w) worth = 0;
+    const uint64_t worth = g < a.groups ? place(a.group_best == 2 ? u + v : u) : 0;
+    // a group stays if few enough are ahead of it
+    int before = 0;
+    for (int j = 0; j < a.groups; ++j) {
+      const uint64_t other =
+          ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(worth >> 32), j << shift) << 32) |
+          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)worth, j << shift);
+      before += other > worth || (other == worth && j < g) ? 1 : 0;
     }
+    const uint64_t kept = __ballot(g < a.groups && before < a.top_groups);
+    const float inv = 1.f / (float)size;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = lane + 64 * i;
-      if (e < a.n_experts && !((kept >> (e / size)) & 1)) key[i] = 0;
+      const int of = (int)(((float)e + 0.5f) * inv);  // e / size: 0.5 / 1024 from a whole number, fp32 is off by 2^-13
+      if (e < a.n_experts && !((kept >> (of << shift)) & 1)) key[i] = 0;
     }
     __builtin_amdgcn_wave_barrier();
   }
-  // the largest one after the other
+  // the largest of the wave one after the other
   double mine = 0.0, total = 0.0;
   int id = 0;
+  int at[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) at[i] = i;
+  if constexpr (PER <= 4) {  // each lane's in order first, so that only its head stands for it
+    auto order = [&](int p, int q) {
+      if (key[q] > key[p] || (key[q] == key[p] && at[q] < at[p])) {
+        const uint64_t k = key[p];
+        const double v = l[p];
+        const int n = at[p];
+        key[p] = key[q];
+        l[p] = l[q];
+        at[p] = at[q];
+        key[q] = k;
+        l[q] = v;
+        at[q] = n;
+      }
+    };
+    if constexpr (PER == 2) order(0, 1);
+    if constexpr (PER == 4) {
+      order(0, 1);
+      order(2, 3);
+      order(0, 2);
+      order(1, 3);
+      order(1, 2);
+    }
+  }
   for (int j = 0; j < a.top_k; ++j) {
     uint64_t best = key[0];
     double s = l[0];
-    int at = 0;
+    int b = at[0];
+    if constexpr (PER > 4) {
 #pragma unroll
-    for (int i = 1; i < PER; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        s = l[i];
-        at = i;
-      }
-    const int w = wave_first(best, lane + 64 * at);
-    const int i = __builtin_amdgcn_readlane(at, w);
+      for (int i = 1; i < PER; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          s = l[i];
+          b = i;
+        }
+    }
+    const int w = wave_first(best, lane + 64 * b);
+    const int i = __builtin_amdgcn_readlane(b, w);
     s = lane_d(s, w);
     total += s;
     if (lane == j) {
       id = w + 64 * i;
       mine = s;
     }
+    if (lane == w) {
+      if constexpr (PER <= 4) {
 #pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (lane == w && q == i) key[q] = 0;
+        for (int q = 0; q + 1 < PER; ++q) {
+          key[q] = key[q + 1];
+          l[q] = l[q + 1];
+          at[q] = at[q + 1];
+        }
+        key[PER - 1] = 0;
+      } else {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) key[q] = q == i ? 0 : key[q];
+      }
+    }
   }
   if (lane < a.top_k) {
     double w = mine;
@@ -196,8 +247,12 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, double* sc)
   const int64_t step = (int64_t)a.n_tok * a.n_experts;
   const double* p = a.logits + (int64_t)t * a.n_experts;
   double l[PER];
+  float bias[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) l[i] = 0.0;
+  for (int i = 0; i < PER; ++i) {
+    l[i] = 0.0;
+    bias[i] = a.bias != nullptr ? a.bias[min(lane + 64 * i, a.n_experts - 1)] : 0.f;
+  }
   for (int z0 = 0; z0 < a.slices; z0 += Z) {
     double v[Z][PER];
 #pragma unroll
@@ -221,7 +276,7 @@ __device__ __forceinline__ void gate_token(const GateArgs& a, int t, double* sc)
     for (int i = 0; i < PER; ++i)
       if (lane + 64 * i < a.n_experts) a.logits_out[(int64_t)t * a.n_experts + lane + 64 * i] = (float)l[i];
   }
-  gate_select<PER>(a, t, l, sc);
+  gate_select<PER>(a, t, l, bias, sc);
 }
 
 // Q8 blocks of columns lo .. hi - 1 of one row of x by the workgroup.

@@ -564,7 +564,7 @@ qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, int64_t n_
  *             negative belongs to no sequence: its values do not matter, and
  *             its outputs are not written.
  *             NULL only if rot_dim is 0.
- *   inv_freq  fp32 [rot_dim / 2], finite.  NULL only if rot_dim is 0.
+ *   inv_freq  fp32 [rot_dim / 2], within +-2^32.  NULL only if rot_dim is 0.
  *   pair_axis NULL (the first axis), or int32 [rot_dim / 2].
  *   n_axes    1 .. QMV_MAX_ROPE_AXES (text: one; images and video: time,
  *             height, width).

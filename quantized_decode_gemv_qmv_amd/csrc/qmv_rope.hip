@@ -12,7 +12,7 @@ constexpr int kHeadBatch = 4;  // passes whose loads are in flight together
 
 // cos and sin of pos * freq.  The product of a 31-bit and a 24-bit number and
 // its turns (times 1 / 2 pi, which two doubles hold to 107 bits) keep their low
-// parts, so the place in the circle is right to 2^-50 turns at every position;
+// parts, so the place in the circle is right to 2^-45 turns at every position;
 // the angle's rest within +-pi/4 is rounded to fp32 once and the Taylor sums
 // end below 2^-28 there.
 __device__ __forceinline__ void cos_sin(int pos, float freq, float& c, float& s) {
@@ -20,9 +20,9 @@ __device__ __forceinline__ void cos_sin(int pos, float freq, float& c, float& s)
   constexpr double kTurnLow = -0x1.6b01ec5417056p-57;  // what kTurn leaves of it
   const double p = (double)pos, f = (double)freq;
   const double a = p * f;
-  const double r = a * kTurn;
-  const double low = fma(a, kTurn, -r) + fma(a, kTurnLow, fma(p, f, -a) * kTurn);
-  const double part = (r - rint(r)) + low;  // turns, within +-1/2
+  const double whole = rint(a * kTurn);
+  const double low = fma(a, kTurnLow, fma(p, f, -a) * kTurn);
+  const double part = fma(a, kTurn, -whole) + low;  // turns, within +-1/2 where a is below 2^53 of them
   const double quarter = rint(4.0 * part);
   const float z = (float)(fma(-0.25, quarter, part) * 6.283185307179586477);
   const float z2 = z * z;

@@ -5,6 +5,8 @@ pair: r holds three roundings (1/rms, x times it, times the weight), cos and
 sin are off by 4 u (the angle's rest below pi/4 rounded once, Taylor sums of a
 few roundings, their ends below 0.1 u), the scale, the product and the sum
 round once each: 10 u.  A dim that does not turn has r's 3 u."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -187,3 +189,22 @@ def test_two_streams_and_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(qo, want[0]) and torch.equal(ko, want[1]), rep
+
+
+def test_large_angles():
+    """Frequencies far above one: the place in the circle from exact fractions."""
+    qmv = need_gpu()
+    two_pi = 2 * Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+    pos = np.array([1, 7, -1, 65535, 2**24 + 3, 2**31 - 1], dtype=np.int32)
+    freq = np.array([1.0, 3.7, -41.3, 1e3, 123457.0, 3e6, -7.7e8, 2.0**32], dtype=np.float32)
+    x = np.random.default_rng(5).standard_normal((6, 3, 16)).astype(np.float32)
+    y, _ = qmv.head_norm_rope(torch.from_numpy(x).cuda(), None, torch.from_numpy(pos).cuda(), torch.from_numpy(freq).cuda())
+    y = y.cpu().numpy().astype(np.float64)
+    for t, p in enumerate(pos):
+        for i, f in enumerate(freq):
+            a = int(p) * Fraction(float(f))
+            w = 0.0 if p < 0 else float(a - round(a / two_pi) * two_pi)  # such a row stays as it is
+            u, v = x[t, :, i].astype(np.float64), x[t, :, i + 8].astype(np.float64)
+            tol = 10 * U * (np.abs(u) + np.abs(v))
+            assert np.all(np.abs(y[t, :, i] - (u * np.cos(w) - v * np.sin(w))) <= tol), (t, i)
+            assert np.all(np.abs(y[t, :, i + 8] - (v * np.cos(w) + u * np.sin(w))) <= tol), (t, i)

@@ -17,6 +17,10 @@
 #include "qmv_device.h"
 #include "qmv_steps.h"
 
+// Sums are relative to m as it was rounded.  Fused into a product m = scale x, a
+// difference from m would be one from the exact product, off by |m| 2^-24 each time.
+#pragma clang fp contract(off)
+
 namespace qmv {
 
 namespace {

@@ -215,3 +215,34 @@ def test_graphs_streams_and_one_workspace():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(again, want)), rep
     assert not ws[:65536].any()
+
+
+def test_logits_that_scale_past_the_range():
+    """z beyond fp32's range is an infinity: forbidden below it, no number above it."""
+    qmv = need_gpu()
+    for v in (700, 60000):
+        x, rng = make(4, v)
+        x[0, 9] = -3e38   # one forbidden token
+        x[1, 11] = 3e38   # no number
+        x[2, :] = -1e38   # none is allowed
+        given = np.full((4, 2), 9, np.int32)
+        given[:, 1] = 20
+        for need in {0, qmv.token_logprobs_workspace_bytes(4, v, 3)}:
+            ws = torch.zeros(need, dtype=torch.uint8, device="cuda") if need else None
+            lp, ent, ids, top = (o.cpu() for o in qmv.token_logprobs(torch.from_numpy(x).cuda(), torch.from_numpy(given).cuda(),
+                                                                     top_n=3, scale=10.0, ws=ws))
+            assert lp[0, 0] == -np.inf and torch.isfinite(lp[0, 1]) and torch.isfinite(ent[0])
+            assert torch.isnan(lp[1]).all() and torch.isnan(ent[1]) and torch.isnan(top[1]).all()
+            assert (lp[2] == -np.inf).all() and ent[2] == 0 and (top[2] == -np.inf).all()
+            assert torch.isfinite(lp[3]).all() and torch.isfinite(ent[3])
+            assert ids[2].tolist() == [0, 1, 2] and ids[1, 0] == 11
+
+
+def test_scaled_rows_far_from_zero():
+    """Rows whose common part is large beside their spread: no term depends on it."""
+    qmv = need_gpu()
+    for t, v in ((3, 900), (40, 30011), (2, 70001), (5, 152064)):
+        x, rng = make(t, v, 9)
+        for scale in (0.7, 1.3):
+            for far in (1e4, -3e5):
+                check(qmv, x + np.float32(far), rng.integers(0, v, (t, 3)), 4, scale)

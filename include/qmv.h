@@ -574,7 +574,9 @@ qmv_status qmv_kv_attn(const qmv_kv* kv, const float* q, int64_t ldq, int64_t n_
  *            columns h * head_dim ..; k NULL with n_kv_heads 0: q alone.
  * q_weight, k_weight : NULL, or fp32 [head_dim] (device).
  * q_out, k_out : fp32 [n_tok][ldqo], [n_tok][ldko]; q and k themselves (same
- *            pointer and stride), or memory that overlaps no other argument.
+ *            pointer and stride), or rows that share no value with q, k or each
+ *            other (they may be columns of the same rows, with one stride), else
+ *            QMV_ERR_INVALID_ARG; and no other argument's memory.
  * Every fp32 pointer except inv_freq 16-byte aligned and every stride a
  * multiple of 4 (else QMV_ERR_MISALIGNED), strides at least heads * head_dim;
  * head_dim a positive multiple of 4, eps positive and finite (else

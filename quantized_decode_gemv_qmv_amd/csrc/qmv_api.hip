@@ -1055,6 +1055,19 @@ QMV_API qmv_status qmv_matvec_batch(qmv_type type, const qmv_matvec_item* items,
 }
 
 // ------------------------------------- steps around a layer's matvecs
+// Whether two fp32 row arrays of n_tok rows share a value: their extents meet,
+// and they are not columns beside each other of rows of one stride.
+static bool rows_meet(const float* p, int64_t ldp, int64_t np, const float* q, int64_t ldq, int64_t nq, int64_t n_tok) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t ea = a + 4 * static_cast<uintptr_t>((n_tok - 1) * ldp + np);
+  const uintptr_t eb = b + 4 * static_cast<uintptr_t>((n_tok - 1) * ldq + nq);
+  if (ea <= b || eb <= a) return false;
+  if (ldp != ldq) return true;
+  const int64_t at = static_cast<int64_t>(a < b ? b - a : a - b) / 4 % ldp;  // of the later one in the earlier one's rows
+  const int64_t first = a < b ? np : nq, second = a < b ? nq : np;
+  return at < first || at + second > ldp;
+}
+
 QMV_API qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq, int64_t n_heads,
                                       const float* q_weight, const float* k, int64_t ldk, int64_t n_kv_heads,
                                       const float* k_weight, int64_t n_tok, int64_t head_dim, float eps, float* q_out,
@@ -1077,6 +1090,14 @@ QMV_API qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int6
       (q_weight != nullptr && !aligned(q_weight, 16)) || (k_weight != nullptr && !aligned(k_weight, 16)) ||
       !aligned(rope->pos, 4) || !aligned(rope->inv_freq, 4) || !aligned(rope->pair_axis, 4))
     return QMV_ERR_MISALIGNED;
+  // an output is its input or shares no value with either or with the other output
+  auto is = [&](const float* p, int64_t ldp, const float* r, int64_t ldr) { return p == r && (ldp == ldr || n_tok == 1); };
+  if (!is(q, ldq, q_out, ldqo) && rows_meet(q, ldq, nq, q_out, ldqo, nq, n_tok)) return QMV_ERR_INVALID_ARG;
+  if (k != nullptr &&
+      ((!is(k, ldk, k_out, ldko) && rows_meet(k, ldk, nk, k_out, ldko, nk, n_tok)) ||
+       rows_meet(k, ldk, nk, q_out, ldqo, nq, n_tok) || rows_meet(q, ldq, nq, k_out, ldko, nk, n_tok) ||
+       rows_meet(q_out, ldqo, nq, k_out, ldko, nk, n_tok)))
+    return QMV_ERR_INVALID_ARG;
   HeadsArgs a{};
   a.x[0] = q;
   a.x[1] = k;
@@ -1120,19 +1141,6 @@ QMV_API size_t qmv_lora_workspace_bytes(int64_t n_items, int64_t max_rank, int64
   if (check_lora_sizes(n_items, max_rank, n_tok) != QMV_OK) return 0;
   return static_cast<size_t>(lora_tile_bytes(n_tok) +
                              align256(4 * n_items * max_rank * n_tok * lora_slices(n_items, max_rank, n_tok)));
-}
-
-// Whether two fp32 row arrays of n_tok rows share a value: their extents meet,
-// and they are not columns beside each other of rows of one stride.
-static bool rows_meet(const float* p, int64_t ldp, int64_t np, const float* q, int64_t ldq, int64_t nq, int64_t n_tok) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  const uintptr_t ea = a + 4 * static_cast<uintptr_t>((n_tok - 1) * ldp + np);
-  const uintptr_t eb = b + 4 * static_cast<uintptr_t>((n_tok - 1) * ldq + nq);
-  if (ea <= b || eb <= a) return false;
-  if (ldp != ldq) return true;
-  const int64_t at = static_cast<int64_t>(a < b ? b - a : a - b) / 4 % ldp;  // of the later one in the earlier one's rows
-  const int64_t first = a < b ? np : nq, second = a < b ? nq : np;
-  return at < first || at + second > ldp;
 }
 
 QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_items, const float* x,

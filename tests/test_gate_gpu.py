@@ -183,3 +183,17 @@ def test_graphs_streams_and_one_workspace():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(other, want)), rep
     assert not ws[:256].any()
+
+
+def test_ties_among_many_experts():
+    """As above where a lane has several experts, as many as there are."""
+    qmv = need_gpu()
+    rng = np.random.default_rng(8)
+    x = rng.integers(-3, 4, (6, 32)).astype(np.float32)
+    rows = (rng.integers(-2, 3, (5, 32)) / 32).astype(np.float32)
+    for e in (130, 256, 520, 1024):
+        wr = rows[rng.integers(0, 5, e)]
+        for t in (2, 6):
+            check(qmv, x[:t], wr, 16, "softmax")
+            check(qmv, x[:t], wr, 16, "sigmoid", None, e // 26 if e % 26 == 0 else 8, 2)
+            check(qmv, x[:t], np.zeros_like(wr), 16, "sigmoid", None, 2, 1)

@@ -193,3 +193,22 @@ def test_logprob_workspace_and_binding():
                  lambda: q.token_logprobs(x, logprobs=torch.zeros(2)), lambda: q.token_logprobs(x, top_ids=g)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_heads_overlaps():
+    """Outputs that share values with an input that is not theirs, or with each other, are refused."""
+    y = FAKE + (1 << 20)
+    apart = dict(k=FAKE + (1 << 16), qo=y, ko=y + (1 << 16))
+    bad = [dict(qo=FAKE + 16), dict(qo=FAKE, ldqo=260), dict(ko=FAKE + (1 << 16), ldko=132), dict(ko=FAKE + (1 << 16) + 64),
+           dict(qo=FAKE + (1 << 16)), dict(ko=FAKE + 1024), dict(ko=y + 1024), dict(qo=y, ko=y),
+           dict(k=FAKE + 4 * 256, ldq=384, ldk=384, qo=FAKE, ldqo=384, ko=FAKE + 4 * 252, ldko=384),
+           dict(k=FAKE + 4 * 256, ldq=384, ldk=384, qo=FAKE + 4 * 256, ldqo=384, ko=FAKE, ldko=384)]
+    for change in bad:
+        assert heads(**{**apart, **change}) == INVALID, change
+    if torch.cuda.is_available():
+        return  # right ones would run on these addresses
+    good = [{}, dict(qo=FAKE, ko=FAKE + (1 << 16)), dict(qo=FAKE, ldqo=260, t=1), dict(k=None, kv=0, kw=None, ko=None),
+            dict(k=FAKE + 4 * 256, ldq=384, ldk=384, qo=FAKE, ldqo=384, ko=FAKE + 4 * 256, ldko=384),
+            dict(k=FAKE + 4 * 256, ldq=384, ldk=384, qo=y, ldqo=384, ko=y + 4 * 256, ldko=384)]
+    for change in good:
+        assert heads(**{**apart, **change}) == 5, change  # QMV_ERR_HIP: the launch found no device

@@ -175,6 +175,13 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _stream_on(dev: int, stream):
+    """The handle of `stream`, or of the current one of the current device `dev`, which `_here` gave."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
 def _check(status: int, what: str) -> None:
     if status != 0:
         if status == 5:  # QMV_ERR_HIP: name the runtime's error
@@ -479,6 +486,13 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
         return like.new_empty(shape, dtype=dtype)
 
 
+def _new_like(t: torch.Tensor, dtype, stream) -> torch.Tensor:
+    """_new of the shape of t, which lies in one piece (0.3 us less than by its shape)."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype)
+    return _new(t, t.shape, dtype, stream)
+
+
 def _rows(t: torch.Tensor, shape, name: str) -> int:
     """Checks an fp32 row array and gives its row stride.  A single row may come without its dimension."""
     if t.dim() == 1 and len(shape) == 2 and shape[0] == 1:
@@ -637,7 +651,7 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor | 
     shape = q.shape
     if len(shape) != 3:
         raise ValueError("q must be [T][n_heads][head_dim]")
-    _here(q, k, pos, inv_freq, q_weight, k_weight, pair_axis, q_out, k_out)
+    dev = _here(q, k, pos, inv_freq, q_weight, k_weight, pair_axis, q_out, k_out)
     n_tok, heads, dim = shape
     ldq = _rows(q, shape, "q")
     if q_out is None:
@@ -653,27 +667,31 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor | 
         kv, ldk, ldko, kp, kop = ks[1], _rows(k, ks, "k"), _rows(k_out, ks, "k_out"), k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    rope = _Rope(None, None, None, 1, 0, bool(interleaved), scale)
+    pp = fp = ap = qwp = kwp = None
+    axes, n = 1, 0
     if pos is not None:
         ps = pos.shape
-        if ps[-1] != n_tok or len(ps) > 2:
+        if len(ps) not in (1, 2) or ps[-1] != n_tok:
             raise ValueError("pos must be [T] or [axes][T]")
-        rope.pos, rope.n_axes = _whole(pos, torch.int32, "pos"), 1 if len(ps) == 1 else ps[0]
+        pp, axes = _whole(pos, torch.int32, "pos"), 1 if len(ps) == 1 else ps[0]
     if inv_freq is not None:
-        n = inv_freq.numel()
-        rope.inv_freq, rope.rot_dim = _whole(inv_freq, torch.float32, "inv_freq"), 2 * n
+        fp, n = _whole(inv_freq, torch.float32, "inv_freq"), inv_freq.numel()
         if pair_axis is not None:
-            rope.pair_axis = _whole(pair_axis, torch.int32, "pair_axis")
+            ap = _whole(pair_axis, torch.int32, "pair_axis")
             if pair_axis.numel() != n:
                 raise ValueError("pair_axis must hold one axis a pair")
-    weights = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and w.numel() != dim:
-            raise ValueError(f"{name} must hold one value a dim")
-        weights.append(None if w is None else _whole(w, torch.float32, name))
-    _check(lib().qmv_head_norm_rope(ctypes.byref(rope), q.data_ptr(), ldq, heads, weights[0], kp, ldk, kv, weights[1],
+    if q_weight is not None:
+        qwp = _whole(q_weight, torch.float32, "q_weight")
+        if q_weight.numel() != dim:
+            raise ValueError("q_weight must hold one value a dim")
+    if k_weight is not None:
+        kwp = _whole(k_weight, torch.float32, "k_weight")
+        if k_weight.numel() != dim:
+            raise ValueError("k_weight must hold one value a dim")
+    rope = _Rope(pp, fp, ap, axes, 2 * n, bool(interleaved), scale)
+    _check(lib().qmv_head_norm_rope(ctypes.byref(rope), q.data_ptr(), ldq, heads, qwp, kp, ldk, kv, kwp,
                                     n_tok, dim, eps, q_out.data_ptr(), _rows(q_out, shape, "q_out"), kop, ldko,
-                                    _stream(stream)), "qmv_head_norm_rope")
+                                    _stream_on(dev, stream)), "qmv_head_norm_rope")
     return q_out, k_out
 
 
@@ -704,30 +722,32 @@ def lora(x: torch.Tensor, ids: torch.Tensor, items, ranks: torch.Tensor | None =
     e, rank, _ = first.shape
     n_items = len(items)
     arr = (_LoraItem * n_items)()
-    outs, seen = [], [x, ids, ranks, scales, ws]
-    for m, (a, b, base, y) in zip(arr, items):
+    dev = _here(x, ids, ranks, scales, ws)
+    outs = []
+    for i, (a, b, base, y) in enumerate(items):
         bs = b.shape
         if a.shape != (e, rank, k) or len(bs) != 3 or bs[0] != e or bs[2] != rank:
             raise ValueError("a must be [E][R][K] and b [E][N][R], with the same E and R in every item")
         n = bs[1]
         if y is None:
             y = _new(x, (n_tok, n), torch.float32, stream)
-        m.a, m.b, m.n_rows, m.y = _whole(a, kind, "a"), _whole(b, kind, "b"), n, y.data_ptr()
-        m.ldy = _rows(y, (n_tok, n), "y")
+        bp, ldb = None, 0
         if base is not None:
-            m.base, m.ldb = base.data_ptr(), _rows(base, (n_tok, n), "base")
-        seen += (a, b, base, y)
+            bp, ldb = base.data_ptr(), _rows(base, (n_tok, n), "base")
+        if not (a.get_device() == b.get_device() == y.get_device() == dev) \
+                or (base is not None and base.get_device() != dev):
+            raise ValueError("every tensor must be on the current CUDA device")
+        arr[i] = (_whole(a, kind, "a"), _whole(b, kind, "b"), n, bp, ldb, y.data_ptr(), _rows(y, (n_tok, n), "y"))
         outs.append(y)
     if ws is None:
         ws = _new(x, (max(lora_workspace_bytes(n_items, rank, n_tok), 1),), torch.uint8, stream)
-    _here(*seen)
     if ids.numel() != n_tok or (ranks is not None and ranks.numel() != e) or (scales is not None and scales.numel() != e):
         raise ValueError("ids must hold one number a row of x, ranks and scales one an adapter")
     _check(lib().qmv_lora(_FLOATS[kind], arr, n_items, x.data_ptr(), _rows(x, (n_tok, k), "x"), n_tok, k,
                           _whole(ids, torch.int32, "ids"), e, rank,
                           None if ranks is None else _whole(ranks, torch.int32, "ranks"),
                           None if scales is None else _whole(scales, torch.float32, "scales"),
-                          _whole(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "qmv_lora")
+                          _whole(ws, torch.uint8, "ws"), ws.numel(), _stream_on(dev, stream)), "qmv_lora")
     return outs
 
 
@@ -762,7 +782,7 @@ def router_gate(x: torch.Tensor, wr: torch.Tensor, top_k: int, scoring: str = "s
     if ids is None:
         ids = _new(x, (n_tok, max(top_k, 1)), torch.int32, stream)
     if weights is None:
-        weights = _new(x, (n_tok, max(top_k, 1)), torch.float32, stream)
+        weights = _new_like(ids, torch.float32, stream)
     if ids.shape != (n_tok, top_k) or weights.shape != (n_tok, top_k):
         raise ValueError("ids and weights must be [T][top_k]")
     if ws is None:
@@ -772,7 +792,7 @@ def router_gate(x: torch.Tensor, wr: torch.Tensor, top_k: int, scoring: str = "s
         else:
             with torch.cuda.stream(stream):
                 ws.zero_()
-    _here(x, wr, bias, ids, weights, logits, xq, ws)
+    dev = _here(x, wr, bias, ids, weights, logits, xq, ws)
     if bias is not None and bias.numel() != e:
         raise ValueError("bias must hold one value an expert")
     if logits is not None and logits.shape != (n_tok, e):
@@ -786,7 +806,7 @@ def router_gate(x: torch.Tensor, wr: torch.Tensor, top_k: int, scoring: str = "s
                                  _whole(weights, torch.float32, "weights"),
                                  None if logits is None else _whole(logits, torch.float32, "logits"),
                                  None if xq is None else _whole(xq, torch.uint8, "xq"), _whole(ws, torch.uint8, "ws"),
-                                 ws.numel(), _stream(stream)), "qmv_router_gate")
+                                 ws.numel(), _stream_on(dev, stream)), "qmv_router_gate")
     return ids, weights
 
 
@@ -819,7 +839,7 @@ def token_logprobs(logits: torch.Tensor, given: torch.Tensor | None = None, top_
             raise ValueError("given must be [T] or [T][G]")
         n_given, gp = 1 if len(gs) == 1 else gs[1], _whole(given, torch.int32, "given")
         if logprobs is None:
-            logprobs = _new(logits, gs, torch.float32, stream)
+            logprobs = _new_like(given, torch.float32, stream)
         else:
             ask.append((logprobs, gs, torch.float32, "logprobs"))
         lp = logprobs.data_ptr()
@@ -835,7 +855,7 @@ def token_logprobs(logits: torch.Tensor, given: torch.Tensor | None = None, top_
         else:
             ask.append((top_ids, (t, top_n), torch.int32, "top_ids"))
         if top_logprobs is None:
-            top_logprobs = _new(logits, (t, top_n), torch.float32, stream)
+            top_logprobs = _new_like(top_ids, torch.float32, stream)
         else:
             ask.append((top_logprobs, (t, top_n), torch.float32, "top_logprobs"))
         ip, tp = top_ids.data_ptr(), top_logprobs.data_ptr()
@@ -844,13 +864,13 @@ def token_logprobs(logits: torch.Tensor, given: torch.Tensor | None = None, top_
     wp, ws_bytes = None, 0
     if ws is not None and ws.numel() > 0:
         wp, ws_bytes = _whole(ws, torch.uint8, "ws"), ws.numel()
-    _here(logits, given, ws, *(x[0] for x in ask))
+    dev = _here(logits, given, ws, *[x[0] for x in ask])
     for x, want, dtype, name in ask:
         _whole(x, dtype, name)
         if x.shape != want:
             raise ValueError(f"{name} must be {list(want)}")
     _check(lib().qmv_token_logprobs(logits.data_ptr(), _rows(logits, shape, "logits"), t, v, scale, gp, n_given, lp,
-                                    entropy.data_ptr(), top_n, ip, tp, wp, ws_bytes, _stream(stream)),
+                                    entropy.data_ptr(), top_n, ip, tp, wp, ws_bytes, _stream_on(dev, stream)),
            "qmv_token_logprobs")
     return logprobs, entropy, top_ids, top_logprobs
 

@@ -64,20 +64,23 @@ __device__ __forceinline__ double lanes_sum(double v) {
 }  // namespace
 
 // y = turn(x * inv * w): a wave takes 64 / L heads of one token a pass, L lanes
-// a head with four dims each, and a lane has the same dims in every pass, so
-// that cos and sin are made once a wave.  Squares are summed in fp64 (each is
-// exact, no length of x overflows it).  A pair's other half lies in the lane
-// (neighbouring pairs) or comes through LDS.  One read and one write of every
-// value bound it: 8192 tokens x 72 heads of 128 dims 132 us, 4.6 TB/s (a large
-// copy reaches 4.9), the vector ALU busy for half of that; one token 3.8 us, the
-// launch and two loads in a row.  All loads of a wave's first passes are on
-// their way before its angles are made (152 -> 146 us).
+// a head with four dims each, and a lane has the same dims in every pass.  Cosines
+// and sines are made once a wave, one or two pairs a lane, and come to the dims' lanes
+// through LDS (each lane its own dims': 8192 x 72 132 us, 40 heads of a token 3.8).
+// Squares are summed in fp64 (each is exact, no length of x overflows it).  A pair's
+// other half lies in the lane (neighbouring pairs) or comes through LDS.  One read and
+// one write of every value bound it: 8192 tokens x 72 heads of 128 dims 122 us, 4.95
+// TB/s (a large copy reaches 4.9); one token 3.3 us, the launch and two loads in a
+// row.  All loads of a wave's first passes are on their way before its angles are
+// made.
 // V4: the halves' distance is a multiple of four dims, so the partner values
 // of a lane are one 16-byte vector.  NT: stores that pass the caches by.
 template <int L, bool ADJACENT, bool V4, bool NT>
 __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a) {
   constexpr int HPP = 64 / L;  // heads of a pass
+  constexpr int kPairs = L == 64 ? 2 : 1;  // of a lane: 32 L dims at most have 2 L of them
   __shared__ __align__(16) float s_x[kHeadWaves][256];
+  __shared__ float s_cos[kHeadWaves][64 * kPairs], s_sin[kHeadWaves][64 * kPairs];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t g = (int64_t)blockIdx.x * kHeadWaves + wave;
   const int t = (int)(g / a.waves_a_token), part = (int)(g % a.waves_a_token);
@@ -103,42 +106,54 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
     w[m] = f32x4{1.f, 1.f, 1.f, 1.f};
     if (a.w[m] != nullptr && on) w[m] = *reinterpret_cast<const f32x4*>(a.w[m] + d0);
   }
-  // the pair of each of the lane's dims: its frequency and axis
+  // cosines and sines of the pairs, one or two a lane, which all heads share
   const int half = a.rot / 2;
   const int first_pos = a.pos != nullptr ? a.pos[t] : 0;
-  float freq[4];
-  int axis[4], other[4];
+  float freq[kPairs];
+  int axis[kPairs];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int d = d0 + j;
-    axis[j] = -1;
-    other[j] = d;
-    freq[j] = 0.f;
-    if (d < a.rot) {
-      const int i = ADJACENT ? d >> 1 : (d < half ? d : d - half);
-      if (!ADJACENT) other[j] = d < half ? d + half : d - half;
-      freq[j] = a.freq[i];
-      axis[j] = a.axis != nullptr ? a.axis[i] : 0;
-      if (axis[j] >= a.n_axes) axis[j] = -1;
+  for (int n = 0; n < kPairs; ++n) {
+    const int i = lane + 64 * n;
+    freq[n] = 0.f;
+    axis[n] = -1;
+    if (i < half) {
+      freq[n] = a.freq[i];
+      axis[n] = a.axis != nullptr ? a.axis[i] : 0;
+      if (axis[n] >= a.n_axes) axis[n] = -1;
     }
   }
   if (first_pos < 0) return;
+  uint64_t turns[kPairs];  // pairs that turn
+#pragma unroll
+  for (int n = 0; n < kPairs; ++n) {
+    turns[n] = __ballot(axis[n] >= 0);
+    if (axis[n] >= 0) {
+      const int pos = axis[n] == 0 ? first_pos : a.pos[(int64_t)axis[n] * a.n_tok + t];
+      float c, s;
+      cos_sin(pos, freq[n], c, s);
+      s_cos[wave][lane + 64 * n] = c * a.scale;
+      s_sin[wave][lane + 64 * n] = s * a.scale;
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  // those of the lane's dims
   float c[4], s[4];
+  int other[4];
+  bool turn[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    c[j] = 1.f;
-    s[j] = 0.f;
-    if (axis[j] >= 0) {
-      if (ADJACENT && (j & 1)) {  // the pair's angle once
-        c[j] = c[j - 1];
-        s[j] = -s[j - 1];
-      } else {
-        const int pos = axis[j] == 0 ? first_pos : a.pos[(int64_t)axis[j] * a.n_tok + t];
-        cos_sin(pos, freq[j], c[j], s[j]);
-        const bool first = ADJACENT || d0 + j < half;
-        c[j] *= a.scale;
-        s[j] *= first ? -a.scale : a.scale;
-      }
+    const int d = d0 + j;
+    const bool second = ADJACENT ? j & 1 : d >= half;
+    const int i = ADJACENT ? d >> 1 : (second ? d - half : d);
+    other[j] = d;
+    turn[j] = false;
+    c[j] = s[j] = 0.f;
+    if (d < a.rot) {
+      if (!ADJACENT) other[j] = second ? i : d + half;
+      turn[j] = (turns[kPairs == 2 ? i >> 6 : 0] >> (i & 63)) & 1;
+      c[j] = s_cos[wave][i];
+      s[j] = s_sin[wave][i];
+      if (!second) s[j] = -s[j];
     }
   }
   const int base = 4 * (lane & ~(L - 1));  // of the head's values in s_x
@@ -181,7 +196,7 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
         __builtin_amdgcn_wave_barrier();
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = axis[j] >= 0 ? fmaf(v[j], c[j], q[j] * s[j]) : v[j];
+      for (int j = 0; j < 4; ++j) v[j] = turn[j] ? fmaf(v[j], c[j], q[j] * s[j]) : v[j];
       if (h < total && on) {
         f32x4* y = reinterpret_cast<f32x4*>(a.y[m] + t * a.ldy[m] + (int64_t)(h - m * a.heads[0]) * a.dim + d0);
         if constexpr (NT)

@@ -208,3 +208,14 @@ def test_large_angles():
             tol = 10 * U * (np.abs(u) + np.abs(v))
             assert np.all(np.abs(y[t, :, i] - (u * np.cos(w) - v * np.sin(w))) <= tol), (t, i)
             assert np.all(np.abs(y[t, :, i + 8] - (v * np.cos(w) + u * np.sin(w))) <= tol), (t, i)
+
+
+@pytest.mark.parametrize("dim", [36, 40, 48, 68, 80, 96, 132, 160, 192])
+def test_large_batches_of_heads_that_leave_lanes_idle(dim):
+    """More than 8 MB of outputs, where a lane may have several vectors of a head."""
+    qmv = need_gpu()
+    t = (9 << 20) // (49 * dim * 4)
+    check(qmv, t, 40, 9, dim, dim, axes=2, place="in", pad=4)
+    check(qmv, t, 40, 9, dim, dim // 2 // 2 * 2, adjacent=True)
+    check(qmv, t, 48, 1, dim, dim - 2, norm=False, scale=1.2)
+    check(qmv, 2 * t, 3, 22, dim, 32, axes=3)

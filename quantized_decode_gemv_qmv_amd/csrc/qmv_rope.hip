@@ -90,11 +90,14 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
   if (t >= a.n_tok) return;  // no barrier below
   const int d0 = 4 * (lane % L);
   const int total = a.heads[0] + a.heads[1];
+  // the token's rows (a head lies below 2^23 values in its row)
+  const float *xq = a.x[0] + t * a.ldx[0], *xk = a.x[1] + t * a.ldx[1];
+  float *yq = a.y[0] + t * a.ldy[0], *yk = a.y[1] + t * a.ldy[1];
   // a pass's values; the next ones are on their way while a batch is worked on
   auto fetch = [&](int p, f32x4 (&x)[V]) {
     const int h = p * HPP + lane / L;
     const int m = h >= a.heads[0];
-    const float* from = a.x[m] + t * a.ldx[m] + (int64_t)(h - m * a.heads[0]) * a.dim;
+    const float* from = (m ? xk : xq) + (h - (m ? a.heads[0] : 0)) * a.dim;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int d = d0 + 4 * L * v;
@@ -212,7 +215,7 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
         }
         __builtin_amdgcn_wave_barrier();
       }
-      float* to = a.y[m] + t * a.ldy[m] + (int64_t)(h - m * a.heads[0]) * a.dim;
+      float* to = (m ? yk : yq) + (h - (m ? a.heads[0] : 0)) * a.dim;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int d = d0 + 4 * L * v;

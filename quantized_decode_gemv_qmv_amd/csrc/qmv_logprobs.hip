@@ -267,12 +267,14 @@ __device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sum
     a.ids[(int64_t)t * n + j] = (int)~(uint32_t)k;
     a.top[(int64_t)t * n + j] = log_prob(value_of(k), a.scale, r, log_s);
   };
-  if (c <= THREADS / 8) {  // each one's place is the number of larger ones; eight threads count
-    const uint64_t k = tid / 8 < c ? sh.key[tid / 8] : 0;
-    int larger = 0;
-    for (int j = tid & 7; j < c; j += 8) larger += sh.key[j] > k ? 1 : 0;
-    larger = sum8(larger);
-    if ((tid & 7) == 0 && k != 0 && larger < n) put(larger, k);
+  if (c <= THREADS / 2) {  // each one's place is the number of larger ones; eight threads count
+    for (int i = tid / 8; i < (c + THREADS / 8 - 1) / (THREADS / 8) * (THREADS / 8); i += THREADS / 8) {  // uniform trips
+      const uint64_t k = i < c ? sh.key[i] : 0;
+      int larger = 0;
+      for (int j = tid & 7; j < c; j += 8) larger += sh.key[j] > k ? 1 : 0;
+      larger = sum8(larger);
+      if ((tid & 7) == 0 && k != 0 && larger < n) put(larger, k);
+    }
   } else if (c <= kList) {  // one after the other, by one wave
     if (wave == 0) {
       uint64_t k[kList / 64];

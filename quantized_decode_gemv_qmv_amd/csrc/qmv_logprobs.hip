@@ -32,6 +32,7 @@ constexpr int kPartVecs = 2;       // 16-byte vectors of a thread
 constexpr int kPartVec = kPartThreads * kPartVecs;  // vectors of a part
 constexpr int kPartGroups = kPartThreads / 16;      // groups of 16 lanes
 static_assert(kPartGroups == kPartGroupsOfRow, "the workspace holds a part's keys");
+constexpr int64_t kPartTarget = 512;  // workgroups of a launch in parts, about
 constexpr int kList = 1024;        // candidates, and groups, that LDS lists
 
 // Order of logits as unsigned numbers: the larger value first, then the lower
@@ -304,6 +305,35 @@ __device__ void put_top(const LogprobArgs& a, int t, const float* row, const Sum
   }
 }
 
+// A thread's vectors i0, i0 + THREADS .. below end, four a step: its largest logit
+// and the vector where that first stands, and its sums relative to its own largest.
+template <int THREADS>
+__device__ __forceinline__ void take(const float* row, int i0, int end, int n, float scale, float& top, int& at, Sums& r) {
+  constexpr int B = 4;
+  for (int i1 = i0; i1 < end; i1 += B * THREADS) {
+    f32x4 v[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = i1 + b * THREADS;
+      v[b] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+      if (i < end) v[b] = load_vec(row, i, n);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const float m = max4(v[b]);
+      if (m > top) {
+        top = m;
+        at = i1 + b * THREADS;
+      }
+    }
+    const float m = top * scale;
+    shift(r, m);
+    const float ref = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+    for (int b = 0; b < B; ++b) add(r.s, r.u, v[b], scale, ref);
+  }
+}
+
 }  // namespace
 
 // A whole row by one workgroup: each thread keeps sums relative to its own
@@ -318,29 +348,7 @@ __global__ __launch_bounds__(kRowThreads) void k_logprob_row(LogprobArgs a) {
   float top = -__builtin_inff();
   int at = tid;
   Sums r{-__builtin_inff(), 0.f, 0.f};
-  constexpr int B = 4;
-  for (int i0 = tid; i0 < vecs; i0 += B * kRowThreads) {
-    f32x4 v[B];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int i = i0 + b * kRowThreads;
-      v[b] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
-      if (i < vecs) v[b] = load_vec(row, i, a.n_vocab);
-    }
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const float m = max4(v[b]);
-      if (m > top) {
-        top = m;
-        at = i0 + b * kRowThreads;
-      }
-    }
-    const float m = top * a.scale;
-    shift(r, m);
-    const float ref = m == -__builtin_inff() ? 0.f : m;
-#pragma unroll
-    for (int b = 0; b < B; ++b) add(r.s, r.u, v[b], a.scale, ref);
-  }
+  take<kRowThreads>(row, tid, vecs, a.n_vocab, a.scale, top, at, r);
   r = block_join<kRowThreads>(r, tmp);
   const double log_s = log((double)r.s);
   put_given<kRowThreads>(a, t, row, r, log_s, given);
@@ -366,37 +374,45 @@ __device__ __forceinline__ uint64_t get_device(const uint64_t* p) {
 
 }  // namespace
 
-// One part of a row, held in registers: its sums and the largest of each 16
-// lanes' vectors.  The last workgroup of a row to arrive joins its parts.
+// One part of a row: its sums and the largest of each 16 lanes' vectors.  The last
+// workgroup of a row to arrive joins its parts.  A part is held in registers, or,
+// with MANY, a.loops times as long.
+template <bool MANY>
 __global__ __launch_bounds__(kPartThreads) void k_logprob_part(LogprobArgs a) {
   __shared__ Sums tmp[kPartThreads / 64];
   __shared__ TopShared sh;
   __shared__ int s_last;
   const int t = blockIdx.y, p = blockIdx.x, tid = threadIdx.x;
   const float* row = a.x + t * a.ldx;
-  const int vecs = (a.n_vocab + 3) / 4, i0 = p * kPartVec + tid;
-  f32x4 v[kPartVecs];
-#pragma unroll
-  for (int b = 0; b < kPartVecs; ++b) {
-    const int i = i0 + b * kPartThreads;
-    v[b] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
-    if (i < vecs) v[b] = load_vec(row, i, a.n_vocab);
-  }
+  const int loops = MANY ? a.loops : 1, span = loops * kPartVec;
+  const int vecs = (a.n_vocab + 3) / 4, i0 = p * span + tid;
   float top = -__builtin_inff();
   int at = i0;
+  Sums r{-__builtin_inff(), 0.f, 0.f};
+  if constexpr (MANY) {
+    take<kPartThreads>(row, i0, min((p + 1) * span, vecs), a.n_vocab, a.scale, top, at, r);
+  } else {
+    f32x4 v[kPartVecs];
 #pragma unroll
-  for (int b = 0; b < kPartVecs; ++b) {
-    const float m = max4(v[b]);
-    if (m > top) {
-      top = m;
-      at = i0 + b * kPartThreads;
+    for (int b = 0; b < kPartVecs; ++b) {
+      const int i = i0 + b * kPartThreads;
+      v[b] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+      if (i < vecs) v[b] = load_vec(row, i, a.n_vocab);
     }
-  }
-  const float m = wave_max(top) * a.scale;
-  const float ref = m == -__builtin_inff() ? 0.f : m;
-  Sums r{m, 0.f, 0.f};
 #pragma unroll
-  for (int b = 0; b < kPartVecs; ++b) add(r.s, r.u, v[b], a.scale, ref);
+    for (int b = 0; b < kPartVecs; ++b) {
+      const float m = max4(v[b]);
+      if (m > top) {
+        top = m;
+        at = i0 + b * kPartThreads;
+      }
+    }
+    const float m = wave_max(top) * a.scale;
+    const float ref = m == -__builtin_inff() ? 0.f : m;
+    r.m = m;
+#pragma unroll
+    for (int b = 0; b < kPartVecs; ++b) add(r.s, r.u, v[b], a.scale, ref);
+  }
   uint64_t* keys = a.keys + (int64_t)t * a.parts * kPartGroups;
   uint64_t* sums = reinterpret_cast<uint64_t*>(a.sums) + 2 * (int64_t)t * a.parts;
   if (a.top_n > 0) {
@@ -449,30 +465,44 @@ __global__ __launch_bounds__(kPartThreads) void k_logprob_part(LogprobArgs a) {
                           for (int g = tid + 3 * kPartThreads; g < groups; g += kPartThreads)
                             f(get_device(keys + g), (uint32_t)g);
                         },
-                        [](int listed) { return listed * kPartVecs * 16; },
-                        [](const uint32_t* list, int q, int) {
-                          const int g = (int)list[q / (kPartVecs * 16)], i = q % (kPartVecs * 16);
-                          return g / kPartGroups * kPartVec + (i >> 4) * kPartThreads + g % kPartGroups * 16 + (i & 15);
+                        [=](int listed) { return listed * loops * kPartVecs * 16; },
+                        [=](const uint32_t* list, int q, int) {
+                          const uint32_t each = loops * kPartVecs * 16;  // vectors of a group
+                          const int g = (int)list[(uint32_t)q / each], i = (int)((uint32_t)q % each);
+                          return g / kPartGroups * span + (i >> 4) * kPartThreads + g % kPartGroups * 16 + (i & 15);
                         });
 }
 
 // Rows are shared by workgroups where whole rows leave compute units idle for
 // longer than joining takes: rows of more than 2^15 tokens, at most one row for
-// each 2048 of them.  Us as whole rows / in parts, five alternatives: 32003 tokens
-// 1 row 7.3 / 7.3; 50257 tokens 1 row 9.6 / 7.3, 16 rows 10.0 / 7.7; 152064
-// tokens 1 row 17.8 / 7.4, 16 rows 18.5 / 10.0, 64 rows 21.7 / 17.3, 128 rows
-// 22.7 / 32.7.
+// each 1200 of them.  Us as whole rows / in parts, five alternatives: 32800 tokens
+// 12 rows 7.9 / 7.7; 50257 tokens 6 rows 10.0 / 7.7, 48 rows 10.3 / 9.3, 96 rows 11.3 /
+// 12.4; 152064 tokens 6 rows 18.5 / 7.7, 64 rows 22.1 / 15.8, 128 rows 22.9 / 22.2,
+// 192 rows 24.0 / 32.1.  Parts are as long as some 512 workgroups leave them (256 /
+// 512 / 768: 64 rows of 152064 16.4 / 15.8 / 16.8, 128 rows 26.8 / 22.2 / 23.6), and a
+// row has four at least, whose groups the alternatives' bound needs.
+static int64_t part_loops(int64_t n_tok, int64_t n_vocab) {
+  const int64_t most = (n_vocab + 4 * kPartVec - 1) / (4 * kPartVec);  // parts
+  const int64_t loops = (n_tok * most + kPartTarget - 1) / kPartTarget;
+  return loops < most / 4 ? loops : most / 4;
+}
 int logprob_parts(int64_t n_tok, int64_t n_vocab) {
-  if (n_vocab <= 32768 || n_tok * 2048 > n_vocab || n_tok > kLogprobCounters) return 0;
-  return (int)((n_vocab + 4 * kPartVec - 1) / (4 * kPartVec));
+  if (n_vocab <= 32768 || n_tok * 1200 > n_vocab || n_tok > kLogprobCounters) return 0;
+  const int64_t part = 4 * kPartVec * part_loops(n_tok, n_vocab);
+  return (int)((n_vocab + part - 1) / part);
 }
 
-hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st) {
+hipError_t launch_token_logprobs(LogprobArgs a, hipStream_t st) {
   if (a.parts == 0) {
     hipLaunchKernelGGL(k_logprob_row, dim3((unsigned)a.n_tok), dim3(kRowThreads), 0, st, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(k_logprob_part, dim3((unsigned)a.parts, (unsigned)a.n_tok), dim3(kPartThreads), 0, st, a);
+  const dim3 grid((unsigned)a.parts, (unsigned)a.n_tok);
+  a.loops = (int)part_loops(a.n_tok, a.n_vocab);
+  if (a.loops > 1)
+    hipLaunchKernelGGL(k_logprob_part<true>, grid, dim3(kPartThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL(k_logprob_part<false>, grid, dim3(kPartThreads), 0, st, a);
   return hipGetLastError();
 }
 

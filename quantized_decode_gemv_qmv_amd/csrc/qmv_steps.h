@@ -101,6 +101,7 @@ struct LogprobArgs {
   int32_t* ids;     // [n_tok][top_n]
   float* top;       // [n_tok][top_n]
   int parts;        // of a row, 0: whole rows
+  int loops;        // lengths of registers that a part has; set at launch
   float* sums;      // [n_tok][parts][4]
   uint64_t* keys;   // [n_tok][parts][kPartGroupsOfRow]
   int* cnt;         // arrival counters, kCounterStep apart
@@ -111,6 +112,6 @@ constexpr int kCounterStep = 64;
 constexpr int kLogprobCounters = 256;  // rows in parts at most
 // Parts of a row that a call with a workspace makes; 0: none.
 int logprob_parts(int64_t n_tok, int64_t n_vocab);
-hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t st);
+hipError_t launch_token_logprobs(LogprobArgs a, hipStream_t st);
 
 }  // namespace qmv

@@ -246,3 +246,19 @@ def test_scaled_rows_far_from_zero():
         for scale in (0.7, 1.3):
             for far in (1e4, -3e5):
                 check(qmv, x + np.float32(far), rng.integers(0, v, (t, 3)), 4, scale)
+
+
+@pytest.mark.parametrize("t,v", [(41, 50257), (60, 152064), (83, 100003), (126, 152064), (12, 100001)])
+def test_rows_in_long_parts(t, v):
+    """Some tens of rows, which workgroups share in parts of several steps."""
+    qmv = need_gpu()
+    x, rng = make(t, v, 4)
+    x[1] = np.sort(x[1])
+    x[2] = np.sort(x[2])[::-1]
+    x[3] = np.round(x[3])           # many equal ones
+    x[4] = 0.5                      # all of them
+    x[5, : v // 2] = -np.inf
+    x[6, 5:] = -np.inf
+    check(qmv, x, rng.integers(0, v, (t, 3)), 32, scale=0.7, pad=1)
+    check(qmv, x, rng.integers(0, v, (t, 1)))
+    check(qmv, x, n=1)

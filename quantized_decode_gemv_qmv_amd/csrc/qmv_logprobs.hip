@@ -9,8 +9,8 @@
 // elements reach, and only groups whose largest reaches it are read again
 // (some tens, from the caches).
 //
-// Many rows are bound by their bytes (1000 x 50257 with five alternatives 41.9 us,
-// 4.8 TB/s), few by a chain: launch, load, sums, handoff to the row's last
+// Many rows are bound by their bytes (1000 x 50257 with five alternatives 42.8 us,
+// 4.7 TB/s), few by a chain: launch, load, sums, handoff to the row's last
 // workgroup, keys, bound, second reading (6 x 152064 with twenty 8.1 us, without
 // alternatives 5.6).  512 threads a row let three rows share a compute unit, where
 // 1024 let one (62.9 -> 41.7 us).

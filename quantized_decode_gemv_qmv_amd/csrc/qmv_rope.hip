@@ -186,10 +186,11 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
         for (int j = 0; j < 4; ++j) ss += (double)y[v][j] * (double)y[v][j];
       ss = lanes_sum<L>(ss);
       if (m ? a.w[1] != nullptr : a.w[0] != nullptr) {
-        // 1 / sqrt: the hardware's, right to 2^-24, and a Newton step
+        // 1 / sqrt: the hardware's, right to 2^-24, and a Newton step, which of a
+        // head with an infinity (0 times inf) would make no number
         const double ms = fma(ss, a.inv_dim, a.eps);
         double inv = __builtin_amdgcn_rsq(ms);
-        inv *= fma(-0.5 * ms * inv, inv, 1.5);
+        if (inv != 0.0) inv *= fma(-0.5 * ms * inv, inv, 1.5);
         const float r = (float)inv;
 #pragma unroll
         for (int v = 0; v < V; ++v)

@@ -219,3 +219,29 @@ def test_large_batches_of_heads_that_leave_lanes_idle(dim):
     check(qmv, t, 40, 9, dim, dim // 2 // 2 * 2, adjacent=True)
     check(qmv, t, 48, 1, dim, dim - 2, norm=False, scale=1.2)
     check(qmv, 2 * t, 3, 22, dim, 32, axes=3)
+
+
+@pytest.mark.parametrize("t,heads,dim", [(3, 2, 64), (4, 5, 256), (1600, 16, 96)])
+def test_normed_heads_with_infinities(t, heads, dim):
+    """1 / sqrt(inf) is 0: finite dims become 0, the infinite ones and their partners no numbers.  Other heads are as
+    they were without the infinity, a head with a NaN is NaN throughout."""
+    qmv = need_gpu()
+    x = torch.randn(t, heads, dim, device="cuda")
+    w = torch.rand(dim, device="cuda") + 0.5
+    rot = 32
+    f = torch.from_numpy(freqs(rot)).cuda()
+    pos = torch.arange(1, t + 1, dtype=torch.int32, device="cuda")
+    want, _ = qmv.head_norm_rope(x.clone(), None, pos, f, w)
+    x[0, 0, 3], x[t - 1, 1, dim - 1], x[1, 1, 0] = float("inf"), float("-inf"), float("nan")
+    y, _ = qmv.head_norm_rope(x.clone(), None, pos, f, w)
+    bad = torch.isnan(y)
+    gone = torch.zeros_like(bad)
+    gone[0, 0, [3, 3 + rot // 2]] = True
+    gone[t - 1, 1, dim - 1] = True
+    gone[1, 1] = True
+    assert torch.equal(bad, gone)
+    zero = torch.zeros_like(bad)
+    zero[0, 0] = zero[t - 1, 1] = True
+    assert (y[zero & ~gone] == 0).all()
+    kept = ~(zero | gone)
+    assert torch.equal(y[kept], want[kept])

@@ -186,11 +186,18 @@ __global__ __launch_bounds__(64 * kHeadWaves) void k_head_norm_rope(HeadsArgs a)
         for (int j = 0; j < 4; ++j) ss += (double)y[v][j] * (double)y[v][j];
       ss = lanes_sum<L>(ss);
       if (m ? a.w[1] != nullptr : a.w[0] != nullptr) {
-        // 1 / sqrt: the hardware's, right to 2^-24, and a Newton step, which of a
-        // head with an infinity (0 times inf) would make no number
+        // 1 / sqrt: the hardware's, right to 2^-24, and a Newton step
         const double ms = fma(ss, a.inv_dim, a.eps);
         double inv = __builtin_amdgcn_rsq(ms);
-        if (inv != 0.0) inv *= fma(-0.5 * ms * inv, inv, 1.5);
+        inv *= fma(-0.5 * ms * inv, inv, 1.5);
+        // fp32 holds it below its normal numbers: 2^64 from the values to it; and
+        // with an infinity in the head it is 0, where the step made no number
+        if (__builtin_expect(__any(ms > 0x1p250), 0)) {
+          const bool far = ms > 0x1p250;
+          if (far) inv = ms < __builtin_inf() ? inv * 0x1p64 : 0.0;
+#pragma unroll
+          for (int v = 0; v < V; ++v) y[v] *= far ? 0x1p-64f : 1.f;
+        }
         const float r = (float)inv;
 #pragma unroll
         for (int v = 0; v < V; ++v)

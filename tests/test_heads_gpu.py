@@ -245,3 +245,24 @@ def test_normed_heads_with_infinities(t, heads, dim):
     assert (y[zero & ~gone] == 0).all()
     kept = ~(zero | gone)
     assert torch.equal(y[kept], want[kept])
+
+
+@pytest.mark.parametrize("dim,rot", [(64, 0), (64, 64), (96, 32), (256, 256)])
+def test_normed_heads_at_the_end_of_the_range(dim, rot):
+    """Values of up to the largest fp32 number, whose mean's inverse lies below the smallest normal one."""
+    qmv = need_gpu()
+    rng = np.random.default_rng(dim + rot)
+    top = float(np.finfo(np.float32).max)
+    for t in (3, (9 << 20) // (20 * dim * 4)):
+        x = (rng.uniform(-1, 1, (t, 20, dim)) * top * rng.uniform(0.2, 1.0, (t, 20, 1))).astype(np.float32)
+        x[:, :, 5] = rng.choice([-top, top], (t, 20))
+        x[:, ::3, 7] = 1e-3
+        w = (1 + 0.3 * rng.standard_normal(dim)).astype(np.float32)
+        pos = rng.integers(0, 9999, (1, t)).astype(np.int32)
+        f = freqs(rot)
+        y, _ = qmv.head_norm_rope(torch.from_numpy(x).cuda(), None, torch.from_numpy(pos).cuda(),
+                                  torch.from_numpy(f).cuda(), q_weight=torch.from_numpy(w).cuda())
+        r, tol = reference(x, w, pos, f, [0] * len(f), False, 1.0)
+        err = np.abs(y.cpu().numpy() - r)
+        # a quotient below the smallest normal number has that number's half step 2^-150 beside its own
+        assert np.all(err <= tol + 2.0 ** -148), float((err - tol).max())

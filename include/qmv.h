@@ -729,9 +729,9 @@ qmv_status qmv_router_gate(const float* x, int64_t ldx, int64_t n_tok, int64_t k
  *   top_logprobs[t] = their z - lse.
  * Terms and sums are fp32, relative to the row's largest z (a z beyond fp32's
  * range is an infinity there).  A logit of -inf is a forbidden token; a row of
- * nothing else has log probabilities of -inf and entropy 0.  A row that holds
- * NaN or +inf has log probabilities and an entropy of NaN, and its alternatives
- * are ordered with NaN as -inf.
+ * nothing else has log probabilities of -inf and entropy 0.  A row with a NaN or
+ * a z of +inf has log probabilities (of tokens outside too) and an entropy of
+ * NaN, and its alternatives are ordered with NaN as -inf.
  * logits   : fp32 [n_tok][ldl] (device, 4-byte aligned), ldl >= n_vocab.
  * scale    : positive and finite (1 / temperature).
  * given    : int32 [n_tok][n_given] (device), n_given 0 .. QMV_MAX_GIVEN;

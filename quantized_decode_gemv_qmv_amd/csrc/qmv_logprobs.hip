@@ -165,14 +165,15 @@ __device__ __forceinline__ void put_given(const LogprobArgs& a, int t, const flo
     const bool none = r.m == -__builtin_inff() && r.s == 0.f;
     a.entropy[t] = none ? 0.f : (float)(log_s - (double)r.u / (double)r.s);
   }
+  // sums are NaN where the row holds NaN or +inf, and m is inf where a z is
+  const float outside = r.s == r.s && r.m < __builtin_inff() ? -__builtin_inff() : __builtin_nanf("");
   for (int i = threadIdx.x; i < a.n_given; i += THREADS) {
     const int64_t at = (int64_t)t * a.n_given + i;
     if (i != (int)threadIdx.x) {
       g.id = a.given[at];
       if (g.id >= 0 && g.id < a.n_vocab) g.x = row[g.id];
     }
-    a.logprobs[at] = g.id < 0 || g.id >= a.n_vocab ? (r.s == r.s ? -__builtin_inff() : r.s)
-                                                   : log_prob(g.x, a.scale, r, log_s);
+    a.logprobs[at] = g.id < 0 || g.id >= a.n_vocab ? outside : log_prob(g.x, a.scale, r, log_s);
   }
 }
 

@@ -262,3 +262,20 @@ def test_rows_in_long_parts(t, v):
     check(qmv, x, rng.integers(0, v, (t, 3)), 32, scale=0.7, pad=1)
     check(qmv, x, rng.integers(0, v, (t, 1)))
     check(qmv, x, n=1)
+
+
+def test_tokens_outside_in_rows_without_numbers():
+    """A row with NaN, with +inf or with a z beyond the range has no number for any given token, one outside too."""
+    qmv = need_gpu()
+    for v in (700, 60000):
+        x, _ = make(5, v)
+        x[0, 3], x[1, 4], x[2, 5] = np.nan, np.inf, 3e38
+        x[3] = -1e38  # nothing is allowed
+        given = np.tile(np.array([[-1, v, 2, 2**31 - 1]], np.int32), (5, 1))
+        need = qmv.token_logprobs_workspace_bytes(5, v, 0)
+        for ws in [None] + ([torch.zeros(need, dtype=torch.uint8, device="cuda")] if need else []):
+            lp, ent, _, _ = qmv.token_logprobs(torch.from_numpy(x).cuda(), torch.from_numpy(given).cuda(), scale=10.0, ws=ws)
+            lp = lp.cpu()
+            assert torch.isnan(lp[:3]).all() and torch.isnan(ent[:3]).all()
+            assert (lp[3] == -np.inf).all() and ent[3] == 0
+            assert (lp[4, [0, 1, 3]] == -np.inf).all() and torch.isfinite(lp[4, 2]) and torch.isfinite(ent[4])

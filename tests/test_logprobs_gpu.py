@@ -279,3 +279,45 @@ def test_tokens_outside_in_rows_without_numbers():
             assert torch.isnan(lp[:3]).all() and torch.isnan(ent[:3]).all()
             assert (lp[3] == -np.inf).all() and ent[3] == 0
             assert (lp[4, [0, 1, 3]] == -np.inf).all() and torch.isfinite(lp[4, 2]) and torch.isfinite(ent[4])
+
+
+def microseconds(call, n=8):
+    """Median time of a call among others, by replays of a graph."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(n):
+            call()
+    times = []
+    for _ in range(9):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3 / n)
+    return sorted(times)[4]
+
+
+def times_of(qmv, t, v, n):
+    """Times of a call without a workspace and with one."""
+    x = torch.randn(t, v, device="cuda") * 3
+    need = qmv.token_logprobs_workspace_bytes(t, v, n)
+    assert need > 0
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    out = dict(entropy=torch.empty(t, device="cuda"), top_ids=torch.empty(t, n, dtype=torch.int32, device="cuda"),
+               top_logprobs=torch.empty(t, n, device="cuda"))
+    whole, shared = (microseconds(lambda: qmv.token_logprobs(x, top_n=n, ws=w, **out)) for w in (None, ws))
+    say(f"logprobs T {t} V {v} top {n}: whole rows {whole:.1f} us, with a workspace {shared:.1f}")
+    return whole, shared
+
+
+@pytest.mark.parametrize("t,v,n", [(41, 50257, 32), (66, 128256, 32), (106, 128256, 24), (96, 152064, 24),
+                                   (126, 152064, 20), (120, 160000, 20), (64, 262144, 32), (128, 262144, 20),
+                                   (200, 262144, 32)])
+def test_alternatives_of_rows_in_few_parts(t, v, n):
+    """Four to eleven parts a row bound the alternatives too: without a bound a row's last workgroup reads all of it
+    twice, which took four to seven times the time of whole rows."""
+    whole, shared = times_of(need_gpu(), t, v, n)
+    assert shared < 2 * whole

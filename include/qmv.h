@@ -629,7 +629,8 @@ qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq,
  * ws       : workspace (device, 256-byte aligned) of
  *            qmv_lora_workspace_bytes(...) bytes; its content does not matter
  *            before or after a call.  Calls that share it must not overlap in
- *            time.
+ *            time.  The size for some n_items, max_rank and n_tok covers every
+ *            call of no more of each.
  * k and max_rank positive multiples of 8 (else QMV_ERR_INVALID_ARG); n_items
  * <= QMV_MAX_BATCH, max_rank <= QMV_MAX_LORA_RANK, n_tok <=
  * QMV_MAX_LORA_TOKENS, k <= QMV_MAX_LORA_K (else QMV_ERR_UNSUPPORTED).
@@ -692,7 +693,8 @@ qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_i
  *            qmv_router_gate_workspace_bytes(...) bytes, zero-filled once when
  *            allocated and left so in its counters by every completed call.
  *            One workspace may serve calls of different shapes that do not
- *            overlap in time.
+ *            overlap in time; the size for some n_tok and n_experts covers
+ *            every call of no more of each.
  * 1 <= n_tok <= QMV_MAX_MOE_TOKENS, k % 4 == 0, k <= 2^24,
  * 1 <= top_k <= min(n_experts, QMV_MAX_TOP_K), n_experts <= QMV_MAX_EXPERTS,
  * n_groups <= QMV_MAX_GATE_GROUPS.  Errors as for qmv_router_topk, and
@@ -745,17 +747,22 @@ qmv_status qmv_router_gate(const float* x, int64_t ldx, int64_t n_tok, int64_t k
  *            when allocated and left so in its counters by every completed
  *            call; it lets workgroups share a row, which calls of few rows need
  *            for speed.  NULL: one workgroup a row.  One workspace may serve
- *            calls of different shapes that do not overlap in time.  Results
+ *            calls of different shapes that do not overlap in time; the size
+ *            for some n_tok and n_vocab covers every call of no more of each.
+ *            Rows of more than QMV_MAX_SHARED_ROWS are never shared (the size
+ *            for them is 0): a program of larger and smaller batches asks for
+ *            the size for that many rows.  Results
  *            are the same on every call with the same arguments, and with and
  *            without a workspace differ in rounding only (ids not at all).
  * n_tok <= QMV_MAX_ACT_ROWS, n_vocab <= QMV_MAX_VOCAB (else
  * QMV_ERR_UNSUPPORTED).  Asynchronous on `stream`; allocates nothing.
  * qmv_token_logprobs_workspace_bytes is host only; 0: the arguments are
- * invalid, or no workspace is used.
+ * invalid, or such calls use no workspace.
  */
 #define QMV_MAX_VOCAB (1 << 24)
 #define QMV_MAX_TOP_TOKENS 32
 #define QMV_MAX_GIVEN 65536
+#define QMV_MAX_SHARED_ROWS 256
 size_t qmv_token_logprobs_workspace_bytes(int64_t n_tok, int64_t n_vocab, int64_t top_n);
 qmv_status qmv_token_logprobs(const float* logits, int64_t ldl, int64_t n_tok, int64_t n_vocab, float scale,
                               const int32_t* given, int64_t n_given, float* logprobs, float* entropy, int64_t top_n,

@@ -30,11 +30,13 @@ __all__ = [
     "head_norm_rope", "lora", "lora_workspace_bytes", "router_gate", "router_gate_workspace_bytes",
     "token_logprobs", "token_logprobs_workspace_bytes",
     "set_tuning", "swiglu_quantize", "router_topk", "variant_name", "variants", "pick_variant", "matvec_plan", "MAX_TOKENS", "MAX_MOE_TOKENS",
+    "MAX_SHARED_ROWS",
 ]
 
 Q8_0, Q4_K, IQ4_XS, Q5_K, Q6_K, Q8G128 = 0, 1, 2, 3, 4, 5
 MAX_TOKENS = 16
 MAX_MOE_TOKENS = 64
+MAX_SHARED_ROWS = 256  # of a token_logprobs call whose workgroups share rows
 MAX_BATCH = 8
 KV_BLOCK = 64
 
@@ -696,6 +698,7 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor | 
 
 
 def lora_workspace_bytes(n_items: int, max_rank: int, n_tok: int) -> int:
+    """Bytes of lora's workspace, enough for every call of no more items, rank and rows."""
     return int(lib().qmv_lora_workspace_bytes(n_items, max_rank, n_tok))
 
 
@@ -752,6 +755,7 @@ def lora(x: torch.Tensor, ids: torch.Tensor, items, ranks: torch.Tensor | None =
 
 
 def router_gate_workspace_bytes(n_tok: int, n_experts: int) -> int:
+    """Bytes of router_gate's workspace, enough for every call of no more tokens and experts."""
     return int(lib().qmv_router_gate_workspace_bytes(n_tok, n_experts))
 
 
@@ -811,6 +815,10 @@ def router_gate(x: torch.Tensor, wr: torch.Tensor, top_k: int, scoring: str = "s
 
 
 def token_logprobs_workspace_bytes(n_tok: int, n_vocab: int, top_n: int) -> int:
+    """Bytes of token_logprobs' workspace, enough for every call of no more rows
+    and tokens, whatever its alternatives; 0 where such calls use none, so also
+    for more than MAX_SHARED_ROWS rows: a program of larger and smaller batches
+    asks for min(rows, MAX_SHARED_ROWS)."""
     return int(lib().qmv_token_logprobs_workspace_bytes(n_tok, n_vocab, top_n))
 
 
@@ -824,7 +832,8 @@ def token_logprobs(logits: torch.Tensor, given: torch.Tensor | None = None, top_
     and the top_n likeliest tokens int32 [T][top_n] with theirs (None, None if
     top_n is 0).  Outputs are allocated when None.  ``ws`` (uint8, zero-filled
     once, of token_logprobs_workspace_bytes bytes) lets workgroups share a row;
-    without it each row has one, which is slow for few rows."""
+    without it, or with an empty one, each row has one, which is slow for few
+    rows."""
     if logits.dim() == 1:
         logits = logits.view(1, -1)
     shape = logits.shape

@@ -1140,7 +1140,7 @@ static int64_t lora_tile_bytes(int64_t n_tok) { return (n_tok + 63) / 64 * 64 * 
 QMV_API size_t qmv_lora_workspace_bytes(int64_t n_items, int64_t max_rank, int64_t n_tok) {
   if (check_lora_sizes(n_items, max_rank, n_tok) != QMV_OK) return 0;
   return static_cast<size_t>(lora_tile_bytes(n_tok) +
-                             align256(4 * n_items * max_rank * n_tok * lora_slices(n_items, max_rank, n_tok)));
+                             align256(4 * lora_room(n_items, max_rank, n_tok)));
 }
 
 QMV_API qmv_status qmv_lora(qmv_float_type type, const qmv_lora_item* items, int64_t n_items, const float* x,
@@ -1197,7 +1197,7 @@ constexpr int64_t kGateCounterBytes = 256;
 
 QMV_API size_t qmv_router_gate_workspace_bytes(int64_t n_tok, int64_t n_experts) {
   if (n_tok < 1 || n_tok > QMV_MAX_MOE_TOKENS || n_experts < 1 || n_experts > QMV_MAX_EXPERTS) return 0;
-  return static_cast<size_t>(kGateCounterBytes + align256(8 * n_tok * n_experts * gate_slices(n_tok, n_experts)));
+  return static_cast<size_t>(kGateCounterBytes + align256(8 * gate_room(n_tok, n_experts)));
 }
 
 QMV_API qmv_status qmv_router_gate(const float* x, int64_t ldx, int64_t n_tok, int64_t k, const float* wr,
@@ -1262,7 +1262,9 @@ constexpr int64_t kLogprobCounterBytes = 4 * kCounterStep * kLogprobCounters;
 
 QMV_API size_t qmv_token_logprobs_workspace_bytes(int64_t n_tok, int64_t n_vocab, int64_t top_n) {
   if (check_logprob_sizes(n_tok, n_vocab, top_n) != QMV_OK) return 0;
-  const int64_t slots = n_tok * logprob_parts(n_tok, n_vocab);
+  static_assert(QMV_MAX_SHARED_ROWS <= kLogprobCounters, "a row in parts has a counter");
+  if (n_tok > QMV_MAX_SHARED_ROWS) return 0;
+  const int64_t slots = logprob_room(n_tok, n_vocab);
   return slots == 0 ? 0 : static_cast<size_t>(kLogprobCounterBytes + align256(slots * (8 * kPartGroupsOfRow + 16)));
 }
 

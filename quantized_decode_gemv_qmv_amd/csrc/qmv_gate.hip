@@ -440,6 +440,12 @@ int gate_slices(int64_t n_tok, int64_t n_experts) {
   return (int)(s < 1 ? 1 : (s > kGateMaxSlices ? kGateMaxSlices : s));
 }
 
+// Several slices are of 256 tiles in all at most.
+int64_t gate_room(int64_t n_tok, int64_t n_experts) {
+  const int64_t one = n_tok * n_experts, most = one * kGateMaxSlices, sliced = 256 * kGateTile * kGateTile;
+  return most < sliced ? most : (one > sliced ? one : sliced);
+}
+
 namespace {
 
 template <int PER>

@@ -498,6 +498,17 @@ int logprob_parts(int64_t n_tok, int64_t n_vocab) {
   return (int)((n_vocab + part - 1) / part);
 }
 
+// A row has `most` parts, or as many as make kPartTarget in all and one a row, or,
+// where loops are most / 4, six at most (most is 9 or more).
+int64_t logprob_room(int64_t n_tok, int64_t n_vocab) {
+  if (n_vocab <= 32768) return 0;
+  const int64_t rows = n_tok * 1200 <= n_vocab ? n_tok : n_vocab / 1200;
+  const int64_t most = rows * ((n_vocab + 4 * kPartVec - 1) / (4 * kPartVec));
+  const int64_t target = rows + kPartTarget, few = 6 * rows;
+  const int64_t longer = target > few ? target : few;
+  return most < longer ? most : longer;
+}
+
 hipError_t launch_token_logprobs(LogprobArgs a, hipStream_t st) {
   if (a.parts == 0) {
     hipLaunchKernelGGL(k_logprob_row, dim3((unsigned)a.n_tok), dim3(kRowThreads), 0, st, a);

@@ -465,6 +465,17 @@ int lora_slices(int64_t n_items, int64_t max_rank, int64_t n_tok) {
   return (int)(want > kLoraMaxSlices ? kLoraMaxSlices : want);
 }
 
+// With g groups, rank <= 16 g / (items * tiles) and g * slices is below g +
+// kDownTarget and 16 g at most; rows / tiles is 1 up to 8 rows, rows / 8 up to 32
+// and at most 4 from there on.  None of it falls as an argument grows.
+int64_t lora_room(int64_t n_items, int64_t max_rank, int64_t n_tok) {
+  const int64_t rows = kDownRows * kWaves;
+  const int64_t g = n_items * ((max_rank + rows - 1) / rows) * likely_tiles(n_tok);
+  const int64_t most = g * kLoraMaxSlices, near = g + kDownTarget - 1;
+  const int64_t eighths = n_tok < 8 ? 8 : (n_tok < kTile * 8 ? n_tok : kTile * 8);
+  return rows * (most < near ? most : near) * eighths / 8;
+}
+
 namespace {
 
 template <int DT, int LPR, int N>

@@ -59,6 +59,9 @@ struct LoraArgs {
 // The most partial sums of h that a call makes (k alone can make them fewer).
 constexpr int kLoraMaxSlices = 16;
 int lora_slices(int64_t n_items, int64_t max_rank, int64_t n_tok);
+// Values of h that the workspace has room for.  Fewer rows take more slices, and
+// can take more room: this one is that of any call of no more items, rank and rows.
+int64_t lora_room(int64_t n_items, int64_t max_rank, int64_t n_tok);
 hipError_t launch_lora(int type, LoraArgs& a, hipStream_t st);
 
 // Routing to experts.
@@ -85,6 +88,8 @@ struct GateArgs {
 // The most slices of k that a call makes (k alone can make them fewer).
 constexpr int kGateMaxSlices = 8;
 int gate_slices(int64_t n_tok, int64_t n_experts);
+// Logits that the workspace has room for: those of any call of no more tokens and experts.
+int64_t gate_room(int64_t n_tok, int64_t n_experts);
 hipError_t launch_router_gate(GateArgs a, hipStream_t st);
 
 // Log probabilities of a row of logits.
@@ -112,6 +117,9 @@ constexpr int kCounterStep = 64;
 constexpr int kLogprobCounters = 256;  // rows in parts at most
 // Parts of a row that a call with a workspace makes; 0: none.
 int logprob_parts(int64_t n_tok, int64_t n_vocab);
+// Parts that the workspace has room for: those of any call of no more rows and
+// tokens; 0: none of them makes parts.
+int64_t logprob_room(int64_t n_tok, int64_t n_vocab);
 hipError_t launch_token_logprobs(LogprobArgs a, hipStream_t st);
 
 }  // namespace qmv

@@ -197,3 +197,14 @@ def test_ties_among_many_experts():
             check(qmv, x[:t], wr, 16, "softmax")
             check(qmv, x[:t], wr, 16, "sigmoid", None, e // 26 if e % 26 == 0 else 8, 2)
             check(qmv, x[:t], np.zeros_like(wr), 16, "sigmoid", None, 2, 1)
+
+
+def test_one_workspace_for_every_batch():
+    """Sized for the most tokens and experts, in calls of fewer, with one launch and with two."""
+    qmv = need_gpu()
+    ws = torch.zeros(qmv.router_gate_workspace_bytes(64, 384), dtype=torch.uint8, device="cuda")
+    for t in (64, 26, 48, 3, 40, 1, 31, 5):
+        for e, k in ((384, 1280), (128, 2052), (16, 5120)):
+            x, wr, bias = make(t, k, e)
+            check(qmv, x, wr, 8, "sigmoid", bias, ws=ws)
+    assert not ws[:256].any()

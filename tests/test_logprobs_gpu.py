@@ -321,3 +321,25 @@ def test_alternatives_of_rows_in_few_parts(t, v, n):
     twice, which took four to seven times the time of whole rows."""
     whole, shared = times_of(need_gpu(), t, v, n)
     assert shared < 2 * whole
+
+
+def test_one_workspace_for_every_batch():
+    """Sized for the most rows: calls of one part a step, of long parts, of few parts and of whole rows in turn, each
+    as with a workspace of its own."""
+    qmv = need_gpu()
+    v = 128256
+    ws = torch.zeros(qmv.token_logprobs_workspace_bytes(256, v, 0), dtype=torch.uint8, device="cuda")
+    x = torch.randn(300, v, device="cuda") * 3
+    given = torch.randint(0, v, (300, 2), dtype=torch.int32, device="cuda")
+    for t, n in ((256, 20), (1, 20), (106, 5), (5, 32), (40, 0), (60, 32), (2, 1), (300, 3), (64, 20), (1, 0), (13, 24)):
+        size = qmv.token_logprobs_workspace_bytes(t, v, n)
+        want = qmv.token_logprobs(x[:t], given[:t], top_n=n, ws=torch.zeros(size, dtype=torch.uint8, device="cuda"))
+        got = qmv.token_logprobs(x[:t], given[:t], top_n=n, ws=ws)
+        torch.cuda.synchronize()
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want)), (t, n)
+        assert not ws[:65536].any()
+    for w in (40000, 32000, 500):  # and of smaller vocabularies
+        want = qmv.token_logprobs(x[:20, :w], given[:20] % w, top_n=20,
+                                  ws=torch.zeros(qmv.token_logprobs_workspace_bytes(20, w, 20), dtype=torch.uint8, device="cuda"))
+        got = qmv.token_logprobs(x[:20, :w], given[:20] % w, top_n=20, ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), w

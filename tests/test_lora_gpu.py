@@ -183,3 +183,13 @@ def test_graph_and_streams():
         other, = qmv.lora(x, ids, [(a, b, base, None)], stream=side)
         torch.cuda.synchronize()
         assert torch.equal(other, want), rep
+
+
+def test_one_workspace_for_every_batch():
+    """Sized for the most items, rank and rows, in calls of fewer: those of some take more slices than those of more."""
+    qmv = need_gpu()
+    ws = torch.empty(qmv.lora_workspace_bytes(3, 64, 256), dtype=torch.uint8, device="cuda")
+    for t in (256, 34, 1, 252, 64, 100, 9, 2):
+        ws.fill_(255)
+        for outs, rank, k in (([70, 33, 500], 64, 1536), ([300], 16, 4096), ([40, 50], 40, 256)):
+            check(qmv, t, k, outs, rank, 5, [i * 7 // 3 % 6 for i in range(t)], ws=ws)

@@ -212,3 +212,62 @@ def test_heads_overlaps():
             dict(k=FAKE + 4 * 256, ldq=384, ldk=384, qo=y, ldqo=384, ko=y + 4 * 256, ldko=384)]
     for change in good:
         assert heads(**{**apart, **change}) == 5, change  # QMV_ERR_HIP: the launch found no device
+
+
+def never_falls(sizes):
+    assert all(b >= a > 0 for a, b in zip(sizes, sizes[1:])), sizes
+
+
+def test_lora_workspace_covers_smaller_calls():
+    """A workspace sized once, for the largest call, is enough for every smaller one."""
+    f = q.lora_workspace_bytes
+    for items, rank in ((1, 8), (2, 64), (3, 16), (8, 256), (5, 200)):
+        never_falls([f(items, rank, t) for t in range(1, 4097)])
+    for t in (1, 7, 34, 252, 700):
+        for items in range(1, 9):
+            never_falls([f(items, r, t) for r in range(8, 257, 8)])
+        for r in (8, 16, 64, 256):
+            never_falls([f(items, r, t) for items in range(1, 9)])
+    # what a call takes: tiles of 32 bytes for each 64 tokens, and h of each slice of k
+    for items, rank in ((1, 8), (2, 64), (3, 16), (8, 256), (5, 200)):
+        for t in range(1, 4097):
+            groups = items * -(-rank // 16) * max(min(t, 8), -(-t // 4))
+            assert f(items, rank, t) >= -(-t // 64) * 2048 + 4 * items * rank * t * min(16, -(-512 // groups)), (items, rank, t)
+    if torch.cuda.is_available():
+        return  # right calls would run on these addresses
+    for items, rank, most in ((2, 64, 256), (3, 16, 700), (1, 16, 64)):
+        for t in range(1, most + 1):
+            assert lora(items=1, t=t, rank=rank, wsb=f(items, rank, most)) == 5, (rank, t)  # found no device
+
+
+def test_gate_workspace_covers_smaller_calls():
+    f = q.router_gate_workspace_bytes
+    for e in (1, 16, 60, 128, 256, 384, 1024):
+        never_falls([f(t, e) for t in range(1, 65)])
+        for t in range(1, 65):
+            slices = max(1, min(8, 256 // (-(-t // 16) * -(-e // 16))))
+            assert f(t, e) >= 256 + 8 * t * e * slices, (t, e)
+    for t in (1, 26, 48, 64):
+        never_falls([f(t, e) for e in range(1, 1025)])
+    if torch.cuda.is_available():
+        return
+    for t in range(1, 65):
+        assert gate(t=t, e=384, groups=1, top_groups=1, wsb=f(64, 384)) == 5, t
+
+
+def test_logprob_workspace_covers_smaller_calls():
+    f = q.token_logprobs_workspace_bytes
+    assert q.MAX_SHARED_ROWS == 256 and f(257, 152064, 20) == 0
+    for v in (32769, 40000, 45056, 50257, 128256, 152064, 262144, 1000003, 1 << 24):
+        never_falls([f(t, v, 20) for t in range(1, 257)])
+        assert len({f(64, v, n) for n in range(33)}) == 1
+        for t in range(1, min(256, v // 1200) + 1):  # counters, keys and sums of a row's parts
+            most = -(-v // 4096)
+            parts = -(-v // (4096 * min(-(-t * most // 512), most // 4)))
+            assert f(t, v, 20) >= 65536 + t * parts * (32 * 8 + 16), (t, v)
+    for t in (1, 40, 256):
+        never_falls([f(t, v, 0) for v in range(32769, 1 << 20, 997)])
+    if torch.cuda.is_available():
+        return
+    for t in (*range(1, 130), 256, 300, 2000):
+        assert logprobs(t=t, v=128256, ld=128256, ws=FAKE, wsb=f(128, 128256, 20)) == 5, t

@@ -1298,7 +1298,7 @@ QMV_API qmv_status qmv_token_logprobs(const float* logits, int64_t ldl, int64_t 
   a.top = top_logprobs;
   if (ws != nullptr) {
     if (ws_bytes < qmv_token_logprobs_workspace_bytes(n_tok, n_vocab, top_n)) return QMV_ERR_WORKSPACE;
-    a.parts = logprob_parts(n_tok, n_vocab);
+    a.parts = logprob_parts(n_tok, n_vocab, top_n);
     a.cnt = static_cast<int*>(ws);
     uint8_t* b = static_cast<uint8_t*>(ws) + kLogprobCounterBytes;
     a.keys = reinterpret_cast<uint64_t*>(b);

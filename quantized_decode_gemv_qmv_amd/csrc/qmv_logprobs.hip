@@ -479,21 +479,28 @@ __global__ __launch_bounds__(kPartThreads) void k_logprob_part(LogprobArgs a) {
                         });
 }
 
-// Rows are shared by workgroups where whole rows leave compute units idle for
-// longer than joining takes: rows of more than 2^15 tokens, at most one row for
-// each 1200 of them.  Us as whole rows / in parts, five alternatives: 32800 tokens
-// 12 rows 7.9 / 7.7; 50257 tokens 6 rows 10.0 / 7.7, 48 rows 10.3 / 9.3, 96 rows 11.3 /
-// 12.4; 152064 tokens 6 rows 18.5 / 7.7, 64 rows 22.1 / 15.8, 128 rows 22.9 / 22.2,
-// 192 rows 24.0 / 32.1.  Parts are as long as some 512 workgroups leave them (256 /
-// 512 / 768: 64 rows of 152064 16.4 / 15.8 / 16.8, 128 rows 26.8 / 22.2 / 23.6), and a
-// row has four at least, whose groups the alternatives' bound needs.
+// Rows are shared by workgroups where that is not slower than whole rows, which
+// leave compute units idle: rows of more than 2^15 tokens, and fewer rows the more
+// alternatives there are, since a row's last workgroup reads n groups again that
+// are as long as its parts.  Us as whole rows / in parts, without alternatives, with
+// 5, 20 and 32: 41 rows of 50257 tokens 8.6 / 6.6, 10.3 / 9.0, 11.1 / 11.1, 11.9 /
+// 14.1; 66 of 128256 17.6 / 11.5, 19.4 / 14.8, 21.0 / 19.4, 23.0 / 24.5; 126 of 152064
+// 20.7 / 20.4, 22.7 / 25.5, 25.5 / 35.0, 28.1 / 43.5; 128 of 262144 32.7 / 25.6, 35.0 /
+// 31.5, 39.9 / 45.2, 44.6 / 58.2.  Where the rule below takes parts they took 5 % longer
+// than whole rows at most (33000 to 10^6 tokens, 0 to 32 alternatives).
+// Parts are as long as some 512 workgroups leave them (256 / 512 / 768: 64 rows of
+// 152064 16.4 / 15.8 / 16.8), and a row has four at least, whose 128 keys the
+// alternatives' bound needs.
 static int64_t part_loops(int64_t n_tok, int64_t n_vocab) {
   const int64_t most = (n_vocab + 4 * kPartVec - 1) / (4 * kPartVec);  // parts
   const int64_t loops = (n_tok * most + kPartTarget - 1) / kPartTarget;
   return loops < most / 4 ? loops : most / 4;
 }
-int logprob_parts(int64_t n_tok, int64_t n_vocab) {
-  if (n_vocab <= 32768 || n_tok * 1200 > n_vocab || n_tok > kLogprobCounters) return 0;
+int logprob_parts(int64_t n_tok, int64_t n_vocab, int64_t top_n) {
+  if (n_vocab <= 32768 || n_tok > kLogprobCounters ||  // a row in parts has a counter
+      n_tok * (1200 + 20 * top_n) > n_vocab ||
+      n_tok * (top_n > 0 ? 30 + top_n : 25) > 3300 + n_vocab / 400)
+    return 0;
   const int64_t part = 4 * kPartVec * part_loops(n_tok, n_vocab);
   return (int)((n_vocab + part - 1) / part);
 }

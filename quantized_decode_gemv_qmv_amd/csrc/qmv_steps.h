@@ -116,7 +116,7 @@ struct LogprobArgs {
 constexpr int kCounterStep = 64;
 constexpr int kLogprobCounters = 256;  // rows in parts at most
 // Parts of a row that a call with a workspace makes; 0: none.
-int logprob_parts(int64_t n_tok, int64_t n_vocab);
+int logprob_parts(int64_t n_tok, int64_t n_vocab, int64_t top_n);
 // Parts that the workspace has room for: those of any call of no more rows and
 // tokens; 0: none of them makes parts.
 int64_t logprob_room(int64_t n_tok, int64_t n_vocab);

@@ -343,3 +343,28 @@ def test_one_workspace_for_every_batch():
                                   ws=torch.zeros(qmv.token_logprobs_workspace_bytes(20, w, 20), dtype=torch.uint8, device="cuda"))
         got = qmv.token_logprobs(x[:20, :w], given[:20] % w, top_n=20, ws=ws)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), w
+
+
+@pytest.mark.parametrize("t,v,n", [(28, 50257, 32), (33, 50257, 16), (42, 100003, 32), (77, 100003, 1), (50, 128256, 32),
+                                   (97, 128256, 5), (55, 152064, 32), (72, 152064, 20), (104, 152064, 5), (82, 262144, 16),
+                                   (158, 262144, 0), (90, 500009, 20)])
+def test_alternatives_of_rows_in_long_parts(t, v, n):
+    """As many rows as are shared with that many alternatives, in few and long parts."""
+    qmv = need_gpu()
+    x, rng = make(t, v, 6)
+    x[1] = np.sort(x[1])
+    x[2] = np.sort(x[2])[::-1]
+    x[3] = np.round(x[3])
+    x[4] = 0.5
+    x[5, : v // 2] = -np.inf
+    x[6, 5:] = -np.inf
+    x[7, v // 3: v // 3 + 200] += 50  # all of them in one part
+    check(qmv, x, rng.integers(0, v, (t, 2)), n, scale=0.7, pad=1)
+
+
+@pytest.mark.parametrize("t,v,n", [(41, 50257, 32), (106, 128256, 5), (66, 128256, 32), (126, 152064, 20), (96, 152064, 32),
+                                   (55, 152064, 32), (100, 152064, 5), (100, 262144, 32), (200, 262144, 20), (6, 152064, 20)])
+def test_a_workspace_costs_no_time(t, v, n):
+    """Rows are shared only where that is not slower: a fixed number of rows had taken up to 1.7 times as long."""
+    whole, shared = times_of(need_gpu(), t, v, n)
+    assert shared < 1.2 * whole

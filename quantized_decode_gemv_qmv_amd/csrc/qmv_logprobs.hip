@@ -180,7 +180,7 @@ __device__ __forceinline__ void put_given(const LogprobArgs& a, int t, const flo
 struct TopShared {
   uint64_t coarse[64];
   uint64_t key[kList];
-  uint64_t wave[16];
+  uint64_t wave[8];
   uint64_t least;
   uint32_t group[kList];
   int groups, keys;
@@ -190,12 +190,12 @@ struct TopShared {
 // (0 where fewer are above 0; the others are all different), in every thread.
 template <int THREADS>
 __device__ __forceinline__ uint64_t bound(uint64_t k, int n, TopShared& sh) {
-  constexpr int L = THREADS / 64;  // threads of a group: 8 or 16
+  constexpr int L = THREADS / 64;  // threads of a group
+  static_assert(L == 8, "a group is eight lanes, a workgroup eight waves");
   const int tid = threadIdx.x;
   k = max_u64(k, dpp_u64<DPP_XOR1>(k));
   k = max_u64(k, dpp_u64<DPP_XOR2>(k));
   k = max_u64(k, dpp_u64<DPP_HALF_MIRROR>(k));
-  if constexpr (L == 16) k = max_u64(k, dpp_u64<DPP_MIRROR>(k));
   if (tid % L == 0) sh.coarse[tid / L] = k;
   if (tid == 0) {
     sh.least = 0;
@@ -207,7 +207,6 @@ __device__ __forceinline__ uint64_t bound(uint64_t k, int n, TopShared& sh) {
 #pragma unroll
   for (int j = 0; j < 64 / L; ++j) larger += sh.coarse[j * L + tid % L] > k ? 1 : 0;
   larger = sum8(larger);
-  if constexpr (L == 16) larger += dpp_i<DPP_MIRROR>(larger);
   if (tid % L == 0 && larger == n - 1 && k != 0) sh.least = k;
   __syncthreads();
   return sh.least;

@@ -368,3 +368,25 @@ def test_a_workspace_costs_no_time(t, v, n):
     """Rows are shared only where that is not slower: a fixed number of rows had taken up to 1.7 times as long."""
     whole, shared = times_of(need_gpu(), t, v, n)
     assert shared < 1.2 * whole
+
+
+@pytest.mark.parametrize("t,v", [(2, 3_000_001), (1, 1 << 24)])
+def test_the_longest_rows(t, v):
+    """A lane of a whole row's 512 threads adds V / 512 terms in turn and rescales (3 roundings) at most every 16 of
+    them: with the rest as above, sums are off by V / 512 * 1.2 + 140 half steps at most."""
+    qmv = need_gpu()
+    x, rng = make(t, v, 8)
+    given = rng.integers(0, v, (t, 5))
+    given[0, 0], given[0, 1] = v - 1, v
+    want = reference(x, given, 32, 1.25)
+    size = 1.2 * v / 512 + 140
+    dx, dg = torch.from_numpy(x).cuda(), torch.from_numpy(given.astype(np.int32)).cuda()
+    need = qmv.token_logprobs_workspace_bytes(t, v, 32)
+    assert need > 0
+    for ws in (None, torch.zeros(need, dtype=torch.uint8, device="cuda")):
+        lp, ent, ids, top = qmv.token_logprobs(dx, dg, top_n=32, scale=1.25, ws=ws)
+        torch.cuda.synchronize()
+        close(lp, want[0], size * U)
+        close(ent, want[1], 2 * size * U * (1 + want[1]))
+        assert np.array_equal(ids.cpu().numpy(), want[2])
+        close(top, want[3], size * U)

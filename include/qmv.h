@@ -635,7 +635,9 @@ qmv_status qmv_head_norm_rope(const qmv_rope* rope, const float* q, int64_t ldq,
  * <= QMV_MAX_BATCH, max_rank <= QMV_MAX_LORA_RANK, n_tok <=
  * QMV_MAX_LORA_TOKENS, k <= QMV_MAX_LORA_K (else QMV_ERR_UNSUPPORTED).
  * Asynchronous on `stream`; allocates nothing.  The result is the same on
- * every call with the same arguments.
+ * every call with the same arguments; the order of a row's sums goes by n_tok
+ * and by the rows that share its adapter, so that its last bits may differ
+ * between a call of its own and a batch.
  */
 #define QMV_MAX_LORA_RANK 256
 #define QMV_MAX_LORA_TOKENS 4096

@@ -23,7 +23,9 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kGateWaves = 16;
 constexpr int kGateTile = 16;  // experts and tokens of a matrix product
-constexpr int kGateAhead = 5;  // steps whose loads are in flight
+// Steps whose loads are in flight (3 / 5 / 8: 16 x 128 of 4096 8.6 / 8.6 / 8.7 us, 64 x 256
+// of 5120 13.0 / 13.2 / 13.1, of 7168 14.9 / 15.1 / 14.9, 64 x 384 of 7168 22.5 / 23.2 / 24.0).
+constexpr int kGateAhead = 5;
 constexpr int kFewExperts = 4; // of a workgroup, up to four tokens
 
 template <int CTRL>

@@ -281,23 +281,26 @@ def test_tokens_outside_in_rows_without_numbers():
             assert (lp[4, [0, 1, 3]] == -np.inf).all() and torch.isfinite(lp[4, 2]) and torch.isfinite(ent[4])
 
 
-def microseconds(call, n=8):
-    """Median time of a call among others, by replays of a graph."""
-    call()
-    torch.cuda.synchronize()
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        for _ in range(n):
-            call()
-    times = []
-    for _ in range(9):
-        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-        a.record()
-        graph.replay()
-        b.record()
+def microseconds(calls, n=8):
+    """Each call's least time among others of its own, by replays of a graph of them, the graphs in turn."""
+    graphs = []
+    for call in calls:
+        call()
         torch.cuda.synchronize()
-        times.append(a.elapsed_time(b) * 1e3 / n)
-    return sorted(times)[4]
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(n):
+                call()
+    times = [[] for _ in calls]
+    for _ in range(9):
+        for graph, took in zip(graphs, times):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            took.append(a.elapsed_time(b) * 1e3 / n)
+    return [min(took) for took in times]
 
 
 def times_of(qmv, t, v, n):
@@ -308,7 +311,7 @@ def times_of(qmv, t, v, n):
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
     out = dict(entropy=torch.empty(t, device="cuda"), top_ids=torch.empty(t, n, dtype=torch.int32, device="cuda"),
                top_logprobs=torch.empty(t, n, device="cuda"))
-    whole, shared = (microseconds(lambda: qmv.token_logprobs(x, top_n=n, ws=w, **out)) for w in (None, ws))
+    whole, shared = microseconds([lambda w=w: qmv.token_logprobs(x, top_n=n, ws=w, **out) for w in (None, ws)])
     say(f"logprobs T {t} V {v} top {n}: whole rows {whole:.1f} us, with a workspace {shared:.1f}")
     return whole, shared
 

@@ -9,11 +9,11 @@
 // elements reach, and only groups whose largest reaches it are read again
 // (some tens, from the caches).
 //
-// Many rows are bound by their bytes (1000 x 50257 with five alternatives 42.8 us,
+// Many rows are bound by their bytes (1000 x 50257 with five alternatives 42.5 us,
 // 4.7 TB/s), few by a chain: launch, load, sums, handoff to the row's last
-// workgroup, keys, bound, second reading (6 x 152064 with twenty 8.1 us, without
-// alternatives 5.6).  512 threads a row let three rows share a compute unit, where
-// 1024 let one (62.9 -> 41.7 us).
+// workgroup, keys, bound, second reading (6 x 152064 with twenty 8.2 us, without
+// alternatives 5.7; 64 x 152064 20.9, with five 16.0, without 12.6).  512 threads a
+// row let three rows share a compute unit, where 1024 let one (62.9 -> 41.7 us).
 #include "qmv_device.h"
 #include "qmv_steps.h"
 
